@@ -15,6 +15,9 @@ from ._binding import (  # noqa: F401
     fk_lloyd,
     fk_lloyd_host,
     fk_norms,
+    fk_page_tables,
+    fk_paged_attn,
+    fk_qk_norm_rope,
     fk_status_string,
     fk_trace_begin,
     fk_trace_end,
@@ -24,6 +27,7 @@ from ._binding import (  # noqa: F401
     FK_NOALLOC_SCRATCH_BYTES,
     fk_version,
     fk_workspace_size,
+    fk_workspace_size_attn,
     fk_workspace_size_host,
     fkb_assign_materialized,
     fkb_mfma_peak,

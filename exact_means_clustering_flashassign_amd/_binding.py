@@ -32,6 +32,13 @@ class fk_trace_t(ctypes.Structure):
                 ("assign_ms", ctypes.c_double), ("update_ms", ctypes.c_double)]
 
 
+class fk_kv_cache_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("key_bias", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("bias_stride", ctypes.c_int64 * 3)]
+
+
 def load(path: Optional[str] = None):
     """Load libfkmeans.so (once) and declare its signatures."""
     global _lib
@@ -59,6 +66,14 @@ def load(path: Optional[str] = None):
         "fk_lloyd_host": (ctypes.c_int, [P, ctypes.c_int, I64, I64, I64, I64, P, I32,
                                          ctypes.c_float, I64, P, P, ctypes.POINTER(I32), P, SZ,
                                          P]),
+        "fk_page_tables": (ctypes.c_int, [P, P, P, I64, P, I64, I64, I64, I64, I64, P, P, P, P, P,
+                                          P, P]),
+        "fk_qk_norm_rope": (ctypes.c_int, [P, P, P, P, P, P, ctypes.c_int, I64, I64, I64, I64, P,
+                                           P, ctypes.c_float, P, I64, I64, I32, P, P, P, P, P,
+                                           P]),
+        "fk_paged_attn": (ctypes.c_int, [P, P, ctypes.c_int, I64, I64, P, P, I64, I64, P, I64,
+                                         ctypes.c_float, ctypes.c_float, P, P, P, SZ, P]),
+        "fk_workspace_size_attn": (SZ, [ctypes.c_int, I64, I64, I64, I64]),
         "fk_trace_begin": (ctypes.c_int, [I32]),
         "fk_trace_end": (ctypes.c_int, [ctypes.POINTER(fk_trace_t)]),
     }
@@ -294,6 +309,199 @@ def fk_lloyd_host(x_host, init, max_iter: int, tol: float, chunk: int, ids=None,
                               _stream(start))
     _check(st, "fk_lloyd_host")
     return ids, centers, int(n_iter.value)
+
+
+# ---------------------------------------------------------------------------
+# paged key-value cache
+# ---------------------------------------------------------------------------
+_strides2 = ctypes.c_int64 * 2
+
+
+def _on(t, name, dtype, shape, dev):
+    """Checks of a contiguous device tensor on `dev`; its address."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, dims, dev):
+    """Checks of a strided device tensor with contiguous rows, for the forward-only calls."""
+    if t.dim() != dims or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name} must be a {dims}-dimensional {dtype} tensor on {dev}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.requires_grad:
+        raise ValueError(f"{name} requires grad: the call has no backward pass, detach it first")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the elements of {name}'s rows must be contiguous")
+    return t.stride()
+
+
+def _first_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.device
+
+
+def _kv_cache(k_cache, v_cache, key_bias, dtype, heads, dim, dev):
+    """fk_kv_cache_t of (pages, page, heads, dim) tensors in any axis order of memory."""
+    sk = _rows(k_cache, "k_cache", dtype, 4, dev)
+    sv = _rows(v_cache, "v_cache", dtype, 4, dev)
+    shape = k_cache.shape
+    if v_cache.shape != shape:
+        raise ValueError(f"v_cache must have k_cache's shape {tuple(shape)}, got "
+                         f"{tuple(v_cache.shape)}")
+    if shape[3] != dim or (heads is not None and shape[2] != heads):
+        raise ValueError(f"k_cache {tuple(shape)} does not hold {heads} heads of {dim} elements")
+    c = fk_kv_cache_t(k_cache.data_ptr(), v_cache.data_ptr(), None, *shape, sk[:3], sv[:3])
+    if key_bias is not None:
+        sb = _rows(key_bias.unsqueeze(-1), "key_bias", _torch().float32, 4, dev)
+        if key_bias.shape != shape[:3]:
+            raise ValueError(f"key_bias must have shape {tuple(shape[:3])}, got "
+                             f"{tuple(key_bias.shape)}")
+        c.key_bias = key_bias.data_ptr()
+        c.bias_stride[:] = sb[:3]
+    return c
+
+
+def fk_page_tables(len_old, len_new, free_pages, page: int, width: int, tokens: int, table=None,
+                   out=None):
+    """Block tables and slots of a step: requests of len_old (B) tokens get
+    len_new (B) more, pages taken from free_pages (F) in order; table (B,W)
+    holds the pages they have (None: none). All int32 on the GPU. Returns
+    (table (B,width), lens (B), cu_tokens (B+1), cu_pages (B+1), slots (tokens),
+    positions (tokens)); `out`: those six tensors, to write into."""
+    torch = _torch()
+    i32, dev = torch.int32, _first_device(len_old, "len_old")
+    if len_old.dim() != 1 or free_pages.dim() != 1:
+        raise ValueError("len_old and free_pages must be one-dimensional")
+    B, width, tokens = len_old.shape[0], int(width), int(tokens)
+    shapes = ((B, width), (B,), (B + 1,), (B + 1,), (tokens,), (tokens,))
+    if out is None:
+        if width < 1 or tokens < 0:
+            raise ValueError("width must be at least 1 and tokens non-negative")
+        out = tuple(torch.empty(s, dtype=i32, device=dev) for s in shapes)
+    names = ("table", "lens", "cu_tokens", "cu_pages", "slots", "positions")
+    if len(out) != 6:
+        raise ValueError("out must hold " + ", ".join(names))
+    width_in, tin = 0, None
+    if table is not None:
+        if table.dim() != 2:
+            raise ValueError("table must be two-dimensional")
+        width_in = table.shape[1]
+        tin = _on(table, "table", i32, (B, width_in), dev)
+    st = load().fk_page_tables(
+        _on(len_old, "len_old", i32, (B,), dev), _on(len_new, "len_new", i32, (B,), dev), tin,
+        width_in, _on(free_pages, "free_pages", i32, free_pages.shape, dev), free_pages.shape[0],
+        B, int(page), width, tokens,
+        *(_on(t, "out " + n, i32, s, dev) for t, n, s in zip(out, names, shapes)),
+        _stream(len_old))
+    _check(st, "fk_page_tables")
+    return tuple(out)
+
+
+def fk_qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-6, rope=None,
+                    positions=None, interleaved: bool = False, slots=None, k_cache=None,
+                    v_cache=None, key_bias=None, q_out=None, k_out=None):
+    """q (T,Hq,D), k and v (T,Hkv,D): per-head RMS norm with the weights (D)
+    (none: no norm) and rotation of the first rot elements by rope (max_pos,
+    rot) fp32, cosines then sines, at positions (T) int32 (none: no rotation).
+    With slots (T) int32, keys and values are stored in k_cache and v_cache
+    (pages, page, Hkv, D), with a key_bias (pages, page, Hkv) of 0. Returns
+    (q_out, k_out); k_out is None with a cache unless given."""
+    torch = _torch()
+    dt, dev = q.dtype, _first_device(q, "q")
+    code = dtype_code(dt)
+    sq, sk = _rows(q, "q", dt, 3, dev), _rows(k, "k", dt, 3, dev)
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k.shape != (T, Hkv, D):
+        raise ValueError(f"k must have shape {(T, 'Hkv', D)}, got {tuple(k.shape)}")
+    cache = vp = sv = sp = None
+    if slots is not None:
+        if v is None or k_cache is None or v_cache is None:
+            raise ValueError("slots need v, k_cache and v_cache")
+        sv = _rows(v, "v", dt, 3, dev)
+        if v.shape != k.shape:
+            raise ValueError(f"v must have k's shape {tuple(k.shape)}, got {tuple(v.shape)}")
+        vp, sv = v.data_ptr(), _strides2(sv[0], sv[1])
+        sp = _on(slots, "slots", torch.int32, (T,), dev)
+        cache = ctypes.byref(_kv_cache(k_cache, v_cache, key_bias, dt, Hkv, D, dev))
+    elif v is not None or k_cache is not None or v_cache is not None or key_bias is not None:
+        raise ValueError("v and the cache need slots")
+    elif k_out is None:
+        k_out = torch.empty((T, Hkv, D), dtype=dt, device=dev)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    rot = max_pos = 0
+    rp = pp = None
+    if rope is not None:
+        if rope.dim() != 2 or positions is None:
+            raise ValueError("rope must be (max_pos, rot), with positions")
+        max_pos, rot = rope.shape
+        rp = _on(rope, "rope", torch.float32, (max_pos, rot), dev)
+        pp = _on(positions, "positions", torch.int32, (T,), dev)
+    st = load().fk_qk_norm_rope(
+        q.data_ptr(), _strides2(sq[0], sq[1]), k.data_ptr(), _strides2(sk[0], sk[1]), vp, sv,
+        code, T, Hq, Hkv, D,
+        None if q_weight is None else _on(q_weight, "q_weight", dt, (D,), dev),
+        None if k_weight is None else _on(k_weight, "k_weight", dt, (D,), dev), eps,
+        rp, max_pos, rot, bool(interleaved), pp, sp, cache,
+        _on(q_out, "q_out", dt, (T, Hq, D), dev),
+        None if k_out is None else _on(k_out, "k_out", dt, (T, Hkv, D), dev), _stream(q))
+    _check(st, "fk_qk_norm_rope")
+    return q_out, k_out
+
+
+def fk_workspace_size_attn(dtype, B: int, Hq: int, Hkv: int, D: int) -> int:
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    return int(load().fk_workspace_size_attn(code, B, Hq, Hkv, D))
+
+
+def fk_paged_attn(q, k_cache, v_cache, table, lens, scale: Optional[float] = None,
+                  softcap: float = 0.0, key_bias=None, max_len: int = 0, out=None, lse=None,
+                  return_lse: bool = False, ws=None):
+    """Attention of one token per request, q (B,Hq,D), over lens (B) int32 keys
+    of k_cache and v_cache (pages, page, Hkv, D) found through table (B,W)
+    int32: softmax(softcap(scale q.k) + key_bias) v, with scale 1/sqrt(D) by
+    default. Returns out (B,Hq,D), and with return_lse (or lse given) the
+    natural log of the softmax's sum, (B,Hq) fp32."""
+    torch = _torch()
+    dt, dev = q.dtype, _first_device(q, "q")
+    code = dtype_code(dt)
+    sq = _rows(q, "q", dt, 3, dev)
+    B, Hq, D = q.shape
+    cache = _kv_cache(k_cache, v_cache, key_bias, dt, None, D, dev)
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"table must have shape {(B, 'W')}, got {tuple(table.shape)}")
+    st2 = _rows(table, "table", torch.int32, 2, dev)
+    width = table.shape[1]
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=dt, device=dev)
+    if lse is None and return_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    lib = load()
+    need = lib.fk_workspace_size_attn(code, B, Hq, cache.heads, D)
+    if need == 0:
+        raise ValueError(f"{Hq} query heads of {D} do not go with {cache.heads} cache heads")
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    st = lib.fk_paged_attn(
+        q.data_ptr(), _strides2(sq[0], sq[1]), code, B, Hq, ctypes.byref(cache), table.data_ptr(),
+        st2[0] if B > 1 else width, width, _on(lens, "lens", torch.int32, (B,), dev),
+        int(max_len), D ** -0.5 if scale is None else scale, softcap,
+        _on(out, "out", dt, (B, Hq, D), dev),
+        None if lse is None else _on(lse, "lse", torch.float32, (B, Hq), dev),
+        _on(ws, "ws", torch.uint8, ws.shape, dev), ws.numel(), _stream(q))
+    _check(st, "fk_paged_attn")
+    return out if lse is None else (out, lse)
 
 
 def fk_trace_begin(capacity: int) -> None:

@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfkmeans.so")
-SOURCES = ["norms.hip", "assign.hip", "assign_splitd.hip", "update.hip", "api.hip"]
+SOURCES = ["norms.hip", "assign.hip", "assign_splitd.hip", "update.hip", "api.hip",
+           "kvtables.hip", "qkrope.hip", "attn.hip", "api_kv.hip"]
 # The contrast baselines (materialised-distance assign, scatter-atomic
 # update) are a library of their own, linked against rocBLAS for the GEMM,
 # so the Lloyd library itself depends on nothing but the HIP runtime.

@@ -16,7 +16,9 @@
  *                centroids and the centre shift;
  *   - fk_lloyd : the loop over those steps with the tol test;
  *   - fk_lloyd_host: the same loop for points kept in host memory, streamed
- *                through the device in chunks every iteration.
+ *                through the device in chunks every iteration;
+ *   - fk_page_tables, fk_qk_norm_rope, fk_paged_attn: a paged key-value cache
+ *                for attention over keys and over the centres of their clusters.
  *
  * Sources (web pages describing flash-kmeans):
  *   [hysenlabs] "flash-kmeans and the return of exact K-Means on the GPU"
@@ -238,6 +240,121 @@ fk_status_t fk_lloyd_host(const void* x_host, fk_dtype_t dt, int64_t B, int64_t 
 
 /* Workspace bytes fk_lloyd_host needs; 0 for invalid arguments. */
 size_t fk_workspace_size_host(fk_dtype_t dt, int64_t B, int64_t chunk, int64_t d, int64_t K);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Paged key-value cache beside the clustering.
+ * The pages name sparse-attention routing and KV-cache compression as what
+ * clusters of keys are for ([hysenlabs] introduction, [paixiang] use cases,
+ * [iaemfoco] applications). The three calls below are the steps around the
+ * clustering of a layer's keys: fk_page_tables says where a step's tokens go,
+ * fk_qk_norm_rope makes their queries and keys and stores keys and values, and
+ * fk_paged_attn attends over what is stored, tokens as well as cluster centres
+ * (a centre that stands for n keys carries the bias log n). They run forward
+ * only, as every call of this library.
+ *
+ * A cache holds `pages` pages of `page` tokens, and in each token `heads` rows
+ * of `dim` elements for keys and for values. Slot s is token s % page of page
+ * s / page; pages * page < 2^31. Strides are in elements, between pages,
+ * tokens and heads, in that order, so any order of these axes can be used; the
+ * elements of a row are contiguous. key_bias (fp32, may be null) is one number
+ * per slot and head, added to the key's score; -inf takes the key out.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* key_bias;
+  int64_t pages, page, heads, dim;
+  int64_t k_stride[3], v_stride[3], bias_stride[3];
+} fk_kv_cache_t;
+
+/*
+ * Block tables, slots and positions of one step from request lengths.
+ * Request b holds len_old[b] tokens and gets len_new[b] more (a negative
+ * length counts as 0; old + new is cut off at width * page, what is beyond gets
+ * no page). With held = ceil(old / page) and need = ceil((old + new) / page):
+ *   cu_tokens (B+1) out: 0, then running sums of len_new;
+ *   cu_pages  (B+1) out: 0, then running sums of need - held, the pages taken
+ *             from free_pages in order of requests. cu_pages[B] > n_free says
+ *             that the list was too short;
+ *   lens      (B) out: old + new;
+ *   table     (B,width) out: entry j of row b is table_in[b,j] for j < held
+ *             (-1 past width_in), free_pages[cu_pages[b] + j - held] for held <=
+ *             j < need (-1 past the list), and -1 for j >= need;
+ *   slots, positions (tokens) out: the step's tokens in order of requests,
+ *             position old + i for token i of its request and slot
+ *             table[position / page] * page + position % page; slot -1 where
+ *             there is no page. Entries past the sum of len_new get slot -1
+ *             and position 0; tokens beyond `tokens` are not written.
+ * Everything is int32. table_in (B,width_in) may be null with width_in 0, and
+ * may be `table` itself if width_in == width; no other output may overlap an
+ * input. Sums of lengths or pages past 2^31 - 1 stop there. page >= 1,
+ * width >= 1, B, n_free, tokens >= 0.
+ */
+fk_status_t fk_page_tables(const int32_t* len_old, const int32_t* len_new,
+                           const int32_t* table_in, int64_t width_in, const int32_t* free_pages,
+                           int64_t n_free, int64_t B, int64_t page, int64_t width, int64_t tokens,
+                           int32_t* table, int32_t* lens, int32_t* cu_tokens, int32_t* cu_pages,
+                           int32_t* slots, int32_t* positions, hipStream_t stream);
+
+/*
+ * Queries and keys of T tokens: per-head RMS norm, then position rotation, and
+ * keys and values into their slots of the cache.
+ *   y = x / sqrt(mean(x^2) + eps) * weight         (weights given; else y = x)
+ *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)   for the pairs (a, b)
+ * of the first `rot` elements: (i, i + rot/2), or (2i, 2i+1) if interleaved.
+ * cos and sin of pair i at position p are rope[p, i] and rope[p, rot/2 + i].
+ * fp32 arithmetic, each result rounded once to dt.
+ *   q (T,Hq,D), k (T,Hkv,D), v (T,Hkv,D) dt in; *_stride: elements between
+ *             tokens and between heads; rows are contiguous.
+ *   q_weight, k_weight (D) dt in, both or neither null.
+ *   rope (max_pos,rot) fp32, positions (T) int32 in; unused with rot == 0. A
+ *             position outside [0,max_pos) is taken as the nearest inside.
+ *   q_out (T,Hq,D) dt out; k_out (T,Hkv,D) dt out, may be null.
+ *   slots (T) int32, cache (host struct): keys and values (and, where the cache
+ *             has one, a key_bias of 0) of token t go to slots[t]; a slot
+ *             outside the cache is skipped. Equal slots give either token's
+ *             rows. Both null, and v, to keep nothing.
+ * Outputs may not overlap inputs. rot even, 0 <= rot <= D; eps >= 0 and finite.
+ */
+fk_status_t fk_qk_norm_rope(const void* q, const int64_t q_stride[2], const void* k,
+                            const int64_t k_stride[2], const void* v, const int64_t v_stride[2],
+                            fk_dtype_t dt, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                            const void* q_weight, const void* k_weight, float eps,
+                            const float* rope, int64_t max_pos, int64_t rot, int32_t interleaved,
+                            const int32_t* positions, const int32_t* slots,
+                            const fk_kv_cache_t* cache, void* q_out, void* k_out,
+                            hipStream_t stream);
+
+/*
+ * Attention of one new token per request over its keys in the cache. Query
+ * head h reads cache head h / (Hq / cache->heads). Over j < min(lens[b],
+ * width * page), with key, value and bias at slot table[b, j / page] * page +
+ * j % page:
+ *   s_j = scale * q.k_j;  s_j = softcap * tanh(s_j / softcap) if softcap > 0;
+ *   s_j = s_j + key_bias_j;  out = sum_j e^(s_j - lse) v_j;  lse = log sum_j e^s_j
+ * Keys with bias -inf, or whose page is outside [0,pages), are left out, and
+ * nothing stored there reaches the result, NaN included. A request with
+ * nothing left gets out = 0 and lse = -inf. Scores, softmax statistics and sums
+ * are fp32; the result is rounded once.
+ *   q (B,Hq,D) dt in, q_stride: elements between requests and between heads.
+ *   table (B,width) int32 in, rows ld_table >= width apart; lens (B) int32 in.
+ *   max_len: no length is above it (0: not known). It only chooses how the work
+ *             is split; a longer request is still computed in full.
+ *   out (B,Hq,D) dt out; lse (B,Hq) fp32 out, may be null.
+ *   ws: fk_workspace_size_attn(dt, B, Hq, Hkv, D) bytes, 256-byte aligned.
+ * D <= 1024 (FK_ERR_UNSUPPORTED above). Same results on every run with the
+ * same arguments.
+ */
+fk_status_t fk_paged_attn(const void* q, const int64_t q_stride[2], fk_dtype_t dt, int64_t B,
+                          int64_t Hq, const fk_kv_cache_t* cache, const int32_t* table,
+                          int64_t ld_table, int64_t width, const int32_t* lens, int64_t max_len,
+                          float scale, float softcap, void* out, float* lse, void* ws,
+                          size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes fk_paged_attn needs (at least 256); 0 for invalid arguments. */
+size_t fk_workspace_size_attn(fk_dtype_t dt, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
 
 /*
  * Optional timing trace of fk_lloyd (process-wide, not thread-safe).
