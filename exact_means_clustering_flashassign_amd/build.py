@@ -28,7 +28,9 @@ ROCM_LIB = "/opt/rocm/lib"
 # MFMA accumulators live in VGPRs, which the argmax reads without AGPR copies.
 # assign_splitd.hip keeps the default (accumulators in AGPRs): its 256
 # accumulator registers per lane would not fit the VGPR file.
-FILE_FLAGS = {"assign.hip": ["-fno-honor-nans", "-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# attn.hip rescales its accumulators every step, so they live in VGPRs too.
+FILE_FLAGS = {"assign.hip": ["-fno-honor-nans", "-mllvm", "-amdgpu-mfma-vgpr-form"],
+              "attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 ARCH = "gfx950"
 
 FLAGS = [

@@ -101,15 +101,626 @@ hipError_t run_any(const AttnArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Matrix-core kernel: rows of at most 256 elements in whole 16-byte units
+// ---------------------------------------------------------------------------
+// One block works for up to 16 query heads of one cache head, so a key is read
+// once for all of them. With G query heads a key head, 16-bit caches give G
+// operations a byte: HBM is the bound, and the 16 columns of the matrix product
+// cost the same for any G up to 16.
+//
+// Lane 16 g + m of a wave. Scores are S^T = K Q^T with v_mfma 16x16: row =
+// key, column = query head, so lane (m, g) holds query head m's scores of keys
+// 4g..4g+3 of each 16-key tile. The values enter as O^T = V^T P^T, whose
+// contraction index is the key: the same lane must hold head m's
+// probabilities of some keys and, for row m of V^T, those keys' values. The
+// order of keys within a contraction is free, so slot 8g + j stands for key 4g + j
+// of the first (j < 4) or second (j >= 4) tile: the probabilities are used in the
+// lane that computed them, and the lane loads rows 4g + j of V itself, elements
+// VE m .. VE m + VE - 1 (16 lanes cover a row), picking tile t's element of
+// each row with byte permutes. Nothing goes through LDS but row addresses.
+constexpr int kHeadTile = 16;
+
+template <int DT, int DP> struct Shape {
+  static constexpr int tiles = DT == FK_F32 ? 1 : 2;        // 16-key tiles per step
+  static constexpr int keys = 16 * tiles;                   // keys per wave and step
+  static constexpr int unit = DT == FK_F32 ? 4 : 8;         // elements in 16 bytes
+  static constexpr int nc = DP / (4 * unit);                // 16-byte key loads per row and lane
+  static constexpr int ve = DP == 64 || DT == FK_F32 ? 4 : 8;   // elements per value load
+  static constexpr int nu = DP / (16 * ve);                 // value loads per row and lane
+  static constexpr int rows = 4 * tiles;                    // value rows per lane
+  static constexpr int ldo = DP + 4;                        // LDS row of merged results
+};
+
+// Loads by address: the address space is stated, so that they are global loads
+// and not generic ones, which the LDS counter would wait for too.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef const __attribute__((address_space(1))) u32x4* gptr16;
+typedef const __attribute__((address_space(1))) u32x2* gptr8;
+typedef const __attribute__((address_space(1))) int32_t* gptr_i32;
+typedef const __attribute__((address_space(1))) float* gptr_f32;
+
+__device__ __forceinline__ uint4 load16(uint64_t addr) {
+  return __builtin_bit_cast(uint4, *(gptr16)addr);
+}
+
+// Keys that do not count are read from here: zeros, whatever the cache holds.
+__device__ const uint4 zero_row[64] = {};
+
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery).
+struct FastDiv {
+  uint32_t mul, shift, d;
+};
+FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while (((uint64_t)1 << l) < d) ++l;
+  return {(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1), l, d};
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
+  return (__umulhi(n, f.mul) + n) >> f.shift;
+}
+
+// How the work is shared. Request b costs its steps of `keys` keys plus
+// kSegCost (a request's own share: queries, joining the waves, storing). The
+// requests' costs are laid end to end and cut into equal parts, one per block of
+// a cache head, so that a batch of any lengths fills the chip evenly. A request
+// inside one part is finished there; one that is cut leaves a partial
+// result per part, at most two a block (one that started before, one that goes
+// on), joined by attn_join_kernel.
+constexpr int kSegCost = 8;
+constexpr int kMinSteps = 8;      // steps worth a block of its own
+
+struct Plan {
+  int parts;            // blocks per (cache head, head tile); 0: one per request
+  int heads, tiles;     // cache heads, head tiles per cache head
+  int G;                // query heads per cache head
+  FastDiv page;
+  float* o;             // (parts, heads, tiles, 2, 16, D) partial sums
+  float* ml;            // (parts, heads, tiles, 2, 16, 2) their maximum and sum
+  int32_t* cover;       // (B, 2) first and last part of a request
+};
+
+__device__ __forceinline__ int len_of(const AttnArgs& a, int64_t b) {
+  const int64_t cap = a.width * a.cache.page;
+  const int n = a.lens[b];
+  return n <= 0 ? 0 : (n < cap ? n : (int)cap);
+}
+
+template <int DT> struct Mfma16;
+template <> struct Mfma16<FK_F16> {
+  __device__ static __forceinline__ floatx4_t run(uint4 a, uint4 b, floatx4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a),
+                                                  __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  }
+  typedef _Float16 T;
+};
+template <> struct Mfma16<FK_BF16> {
+  __device__ static __forceinline__ floatx4_t run(uint4 a, uint4 b, floatx4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  }
+  typedef __bf16 T;
+};
+// fp32: element j of the lanes' 16 bytes in turn, four k per product.
+template <> struct Mfma16<FK_F32> {
+  __device__ static __forceinline__ floatx4_t run(uint4 a, uint4 b, floatx4_t c) {
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, a.x),
+                                             __builtin_bit_cast(float, b.x), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, a.y),
+                                             __builtin_bit_cast(float, b.y), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, a.z),
+                                             __builtin_bit_cast(float, b.z), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, a.w),
+                                                __builtin_bit_cast(float, b.w), c, 0, 0, 0);
+  }
+};
+
+// fp16 probabilities are scaled by 2^14, so that one 2^-38 of the largest is
+// still a subnormal fp16 and a long tail of small ones is not lost.
+template <int DT> constexpr float kProbShift = DT == FK_F16 ? 14.f : 0.f;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
+}
+
+// State of one wave over a run of steps.
+template <int DT, int DP> struct Acc {
+  using S = Shape<DT, DP>;
+  float m, l;                          // of head m's keys; l: this lane's share
+  floatx4_t o[S::nu * S::ve];
+};
+
+// Row addresses and bias of one step's keys, per wave and parity.
+template <int DT, int DP> struct Rows {
+  static constexpr int n = Shape<DT, DP>::keys;
+  uint64_t k[n], v[n];
+  float bias[n];
+};
+
+template <int DT, int DP, bool EXTRA>
+__device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t b, int hk, int ht,
+                                       int len, int step, int end, Rows<DT, DP>* rows,
+                                       Acc<DT, DP>& acc) {
+  using S = Shape<DT, DP>;
+  const fk_kv_cache_t& c = a.cache;
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const int D = (int)c.dim;
+  constexpr int eb = Val<DT>::bytes;
+  acc.m = -INFINITY;
+  acc.l = 0.f;
+#pragma unroll
+  for (int i = 0; i < S::nu * S::ve; ++i) acc.o[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+  if (step >= end) return;
+
+  // Query fragments; heads past G and elements past D are zero. An element
+  // past D reads the key row's start instead, times a zero query.
+  uint4 q[S::nc];
+  uint32_t koff[S::nc], voff[S::nu];
+  const int head = ht * kHeadTile + m;
+  const char* qp = (const char*)a.q +
+                   (b * a.q_stride[0] + (int64_t)(hk * p.G + min(head, p.G - 1)) * a.q_stride[1]) * eb;
+#pragma unroll
+  for (int i = 0; i < S::nc; ++i) {
+    const int e = i * 4 * S::unit + g * S::unit;
+    koff[i] = e < D ? e * eb : 0;
+    q[i] = load16((uint64_t)(qp + koff[i]));
+    if (e >= D || head >= p.G) q[i] = make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < S::nu; ++i) {
+    const int e = i * 16 * S::ve + m * S::ve;
+    voff[i] = e < D ? e * eb : 0;
+  }
+
+  // Lane i < keys looks after key i of a step: table entry two steps ahead, bias
+  // one step ahead, addresses to LDS just before the step's loads.
+  const uint64_t table = (uint64_t)(a.table + b * a.ld_table);
+  const int kl = lane & (S::keys - 1);
+  const uint64_t kbase = (uint64_t)c.k + (uint64_t)hk * c.k_stride[2] * eb;
+  const uint64_t vbase = (uint64_t)c.v + (uint64_t)hk * c.v_stride[2] * eb;
+  const uint64_t zero = (uint64_t)zero_row;
+  const bool has_bias = EXTRA && c.key_bias && c.pages > 0;
+  const uint64_t bbase = (uint64_t)c.key_bias + (uint64_t)hk * c.bias_stride[2] * 4;
+  // (loads without branches: a key past the end reads the last one's entry)
+  auto entry = [&](int st) -> int32_t {             // page of key kl of step st, -1: none
+    const uint32_t key = (uint32_t)st * S::keys + kl;
+    const uint32_t at = min(key, (uint32_t)len - 1);
+    const int32_t pg = *(gptr_i32)(table + 4 * (uint64_t)div_by(at, p.page));
+    return st < end && key == at ? pg : -1;
+  };
+  auto bias_of = [&](int st, int32_t pg) -> float {
+    const bool live = (uint32_t)pg < (uint32_t)c.pages;
+    float bias = 0.f;
+    if (has_bias) {
+      const uint32_t key = (uint32_t)st * S::keys + kl;
+      const uint32_t tok = key - div_by(key, p.page) * p.page.d;
+      bias = *(gptr_f32)(bbase + (uint64_t)((live ? pg : 0) * c.bias_stride[0] + tok * c.bias_stride[1]) * 4);
+    }
+    return live ? bias : -INFINITY;
+  };
+  auto put_rows = [&](Rows<DT, DP>& r, int st, int32_t pg, float bias) {
+    const uint32_t key = (uint32_t)st * S::keys + kl;
+    const uint32_t tok = key - div_by(key, p.page) * p.page.d;
+    const bool live = bias != -INFINITY;
+    const uint64_t ka = kbase + (uint64_t)(pg * c.k_stride[0] + tok * c.k_stride[1]) * eb;
+    const uint64_t va = vbase + (uint64_t)(pg * c.v_stride[0] + tok * c.v_stride[1]) * eb;
+    // other lanes of the wave read these: keep the compiler's order
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    r.k[kl] = live ? ka : zero;
+    r.v[kl] = live ? va : zero;
+    r.bias[kl] = bias;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  };
+  uint4 kf[S::tiles][S::nc];
+  auto load_k = [&](const Rows<DT, DP>& r) {
+#pragma unroll
+    for (int s = 0; s < S::tiles; ++s) {
+      const uint64_t ad = r.k[16 * s + m];
+#pragma unroll
+      for (int i = 0; i < S::nc; ++i) kf[s][i] = load16(ad + koff[i]);
+    }
+  };
+  uint4 vf[S::rows][S::nu];            // ve == 4 and 16-bit: only .x and .y
+  auto load_v = [&](const Rows<DT, DP>& r) {
+#pragma unroll
+    for (int j = 0; j < S::rows; ++j) {
+      const uint64_t ad = r.v[16 * (j >> 2) + 4 * g + (j & 3)];
+#pragma unroll
+      for (int i = 0; i < S::nu; ++i) {
+        if constexpr (S::ve * eb == 16) {
+          vf[j][i] = load16(ad + voff[i]);
+        } else {
+          const u32x2 h = *(gptr8)(ad + voff[i]);
+          vf[j][i] = make_uint4(h.x, h.y, 0, 0);
+        }
+      }
+    }
+  };
+
+  int32_t pg1 = entry(step), pg2 = entry(step + kWaves);
+  put_rows(rows[0], step, pg1, bias_of(step, pg1));
+  float bias1 = bias_of(step + kWaves, pg2);
+  pg1 = pg2;
+  pg2 = entry(step + 2 * kWaves);
+  load_k(rows[0]);
+  load_v(rows[0]);
+  int par = 0;
+  for (; step < end; step += kWaves, par ^= 1) {
+    Rows<DT, DP>& now = rows[par];
+    Rows<DT, DP>& next = rows[par ^ 1];
+    put_rows(next, step + kWaves, pg1, bias1);
+    float s[S::tiles][4];
+#pragma unroll
+    for (int u = 0; u < S::tiles; ++u) {
+      floatx4_t x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < S::nc; ++i) x = Mfma16<DT>::run(kf[u][i], q[i], x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[u][i] = x[i];
+    }
+    load_k(next);
+    __builtin_amdgcn_sched_barrier(0);   // the next keys are on their way before the softmax
+    bias1 = bias_of(step + 2 * kWaves, pg2);
+    pg1 = pg2;
+    pg2 = entry(step + 3 * kWaves);
+
+    float top = acc.m;
+#pragma unroll
+    for (int u = 0; u < S::tiles; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // -inf where a key does not count: its score is 0 (a zero row)
+        const float x = s[u][i] * a.scale;
+        s[u][i] = (EXTRA ? capped(x, a.softcap) : x) + now.bias[16 * u + 4 * g + i];
+        top = fmaxf(top, s[u][i]);
+      }
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    // differences before the scaling by log2 e: a bias of the type's lowest
+    // value must not overflow; with nothing but -inf so far, subtract nothing
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float alpha = fast_exp2((acc.m - ref) * kLog2e);
+    acc.m = top;
+    float part = 0.f;
+#pragma unroll
+    for (int u = 0; u < S::tiles; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[u][i] = fast_exp2(fmaf(s[u][i] - ref, kLog2e, kProbShift<DT>));
+        part += s[u][i];
+      }
+    acc.l = fmaf(acc.l, alpha, part);
+#pragma unroll
+    for (int i = 0; i < S::nu * S::ve; ++i) acc.o[i] *= alpha;
+
+    if constexpr (DT == FK_F32) {
+#pragma unroll
+      for (int u = 0; u < S::nu; ++u)
+#pragma unroll
+        for (int t = 0; t < S::ve; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc.o[u * S::ve + t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                __builtin_bit_cast(float, word(vf[j][u], t)), s[0][j], acc.o[u * S::ve + t], 0, 0, 0);
+    } else {
+      // Probabilities as the sum of two 16-bit numbers: one alone would round
+      // each to 8 (bf16) or 11 bits, an error as large as the result's own
+      // rounding. The second product rides on matrix units that are idle anyway.
+      typedef typename Mfma16<DT>::T T;
+      typedef T T8 __attribute__((ext_vector_type(8)));
+      T8 hi, lo;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = s[j >> 2][j & 3];
+        hi[j] = (T)x;
+        lo[j] = (T)(x - (float)hi[j]);
+      }
+      const uint4 ph = __builtin_bit_cast(uint4, hi), pl = __builtin_bit_cast(uint4, lo);
+#pragma unroll
+      for (int u = 0; u < S::nu; ++u)
+#pragma unroll
+        for (int t = 0; t < S::ve; ++t) {
+          const uint32_t sel = t & 1 ? 0x07060302u : 0x05040100u;
+          uint4 vt;
+          vt.x = __builtin_amdgcn_perm(word(vf[1][u], t >> 1), word(vf[0][u], t >> 1), sel);
+          vt.y = __builtin_amdgcn_perm(word(vf[3][u], t >> 1), word(vf[2][u], t >> 1), sel);
+          vt.z = __builtin_amdgcn_perm(word(vf[5][u], t >> 1), word(vf[4][u], t >> 1), sel);
+          vt.w = __builtin_amdgcn_perm(word(vf[7][u], t >> 1), word(vf[6][u], t >> 1), sel);
+          acc.o[u * S::ve + t] = Mfma16<DT>::run(vt, ph, acc.o[u * S::ve + t]);
+          acc.o[u * S::ve + t] = Mfma16<DT>::run(vt, pl, acc.o[u * S::ve + t]);
+        }
+    }
+    load_v(next);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  acc.l += __shfl_xor(acc.l, 16, 64);
+  acc.l += __shfl_xor(acc.l, 32, 64);
+}
+
+// Where part `w` of the flattened costs starts: request and cost before it.
+// Every block finds out by itself: thread i adds up requests [i n, (i + 1) n).
+struct Start {
+  int64_t total, lo, hi;     // all costs; this part's range
+  int64_t b, before;         // request that holds lo, cost of those before it
+  int parts;                 // parts in use
+};
+
+template <int KEYS>
+__device__ __forceinline__ int64_t cost_of(const AttnArgs& a, int64_t b) {
+  return kSegCost + (len_of(a, b) + KEYS - 1) / KEYS;
+}
+
+template <int KEYS>
+__device__ __forceinline__ Start find_start(const AttnArgs& a, const Plan& p, int w) {
+  __shared__ int64_t wave_tot[kWaves];
+  __shared__ int64_t found[2];
+  const int64_t n = (a.B + kWaves * 64 - 1) / (kWaves * 64);
+  const int64_t b0 = threadIdx.x * n, b1 = b0 + n < a.B ? b0 + n : a.B;
+  int64_t mine = 0;
+  for (int64_t b = b0; b < b1; ++b) mine += cost_of<KEYS>(a, b);
+  int64_t incl = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t o = __shfl_up(incl, off, 64);
+    if ((int)(threadIdx.x & 63) >= off) incl += o;
+  }
+  if ((threadIdx.x & 63) == 63) wave_tot[threadIdx.x >> 6] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    if (i < (int)(threadIdx.x >> 6)) before += wave_tot[i];
+    total += wave_tot[i];
+  }
+  Start st;
+  st.total = total;
+  const int64_t most = total / (kMinSteps + kSegCost);
+  st.parts = (int)(most < 1 ? 1 : (most < p.parts ? most : p.parts));
+  st.lo = w < st.parts ? total * w / st.parts : total;
+  st.hi = w < st.parts ? total * (w + 1) / st.parts : total;
+  if (st.lo >= before && st.lo < before + mine) {
+    int64_t b = b0, at = before;
+    for (int64_t c = cost_of<KEYS>(a, b); at + c <= st.lo; c = cost_of<KEYS>(a, b)) at += c, ++b;
+    found[0] = b;
+    found[1] = at;
+  }
+  __syncthreads();
+  st.b = found[0];
+  st.before = found[1];
+  return st;
+}
+
+// Scale and sum of `n` partial results (m_i, l_i) of one head.
+__device__ __forceinline__ float join_factor(float m, float l, float top) {
+  return l == 0.f ? 0.f : fast_exp2((m - top) * kLog2e);
+}
+
+template <int DT>
+__device__ __forceinline__ void store4(void* out, int64_t at, const float* x) {
+  if constexpr (DT == FK_F32) {
+    *(float4*)((float*)out + at) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+    typedef typename Mfma16<DT>::T T;
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    T4 v = {(T)x[0], (T)x[1], (T)x[2], (T)x[3]};
+    *(T4*)((T*)out + at) = v;
+  }
+}
+
+template <int DT, int DP, bool EXTRA>
+__global__ __launch_bounds__(kWaves * 64) void attn_mfma_kernel(AttnArgs a, Plan p) {
+  using S = Shape<DT, DP>;
+  __shared__ Rows<DT, DP> rows[kWaves][2];
+  __shared__ float so[kWaves][kHeadTile][S::ldo];
+  __shared__ float sm[kWaves][kHeadTile], sl[kWaves][kHeadTile];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
+  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
+  const int ht = (int)(id % p.tiles), hk = (int)((id / p.tiles) % p.heads);
+  const int64_t part = id / ((int64_t)p.tiles * p.heads);
+  const int nh = min(kHeadTile, p.G - ht * kHeadTile);
+  const int D = (int)a.cache.dim;
+
+  Start st;
+  if (p.parts > 0) {
+    st = find_start<S::keys>(a, p, (int)part);
+    if (st.lo >= st.hi) return;
+  } else {
+    st.lo = 0, st.hi = 1, st.b = part, st.before = 0;
+  }
+  for (int64_t b = st.b, at = st.before; at < st.hi;) {
+    const int len = len_of(a, b);
+    const int steps = (len + S::keys - 1) / S::keys;
+    int t0 = 0, t1 = steps;
+    if (p.parts > 0) {
+      const int64_t first = at + kSegCost;
+      t0 = (int)max((int64_t)0, min(st.lo - first, (int64_t)steps));
+      t1 = (int)max((int64_t)0, min(st.hi - first, (int64_t)steps));
+    }
+    const bool starts = at >= st.lo;           // the request begins in this part
+    if (t0 < t1 || (steps == 0 && starts)) {
+      Acc<DT, DP> acc;
+      attend<DT, DP, EXTRA>(a, p, b, hk, ht, len, t0 + w, t1, rows[w], acc);
+      __syncthreads();                         // the last request's results are out
+      if (m < nh) {
+        if (g == 0) sm[w][m] = acc.m, sl[w][m] = acc.l;
+#pragma unroll
+        for (int u = 0; u < S::nu; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int t = 0; t < S::ve; ++t)
+              so[w][m][u * 16 * S::ve + S::ve * (4 * g + i) + t] = acc.o[u * S::ve + t][i];
+      }
+      __syncthreads();
+      const bool whole = t0 == 0 && t1 == steps;
+      const int slot = t0 == 0 ? 1 : 0;
+      const int64_t ps = (((part * p.heads + hk) * p.tiles + ht) * 2 + slot) * kHeadTile;
+      for (int i = threadIdx.x; i < nh * (DP / 4); i += kWaves * 64) {
+        const int h = i / (DP / 4), e = (i - h * (DP / 4)) * 4;
+        float top = sm[0][h];
+#pragma unroll
+        for (int k = 1; k < kWaves; ++k) top = fmaxf(top, sm[k][h]);
+        float x[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k) {
+          const float f = join_factor(sm[k][h], sl[k][h], top);
+          l = fmaf(f, sl[k][h], l);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = fmaf(f, so[k][h][e + j], x[j]);
+        }
+        if (e >= D) continue;
+        if (whole) {
+          const int64_t row = b * a.Hq + hk * p.G + ht * kHeadTile + h;
+          const float r = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] *= r;
+          store4<DT>(a.out, row * D + e, x);
+          if (e == 0 && a.lse)
+            a.lse[row] = l == 0.f ? -INFINITY : top + (logf(l) - kProbShift<DT> * kLn2);
+        } else {
+          *(float4*)(p.o + (ps + h) * D + e) = make_float4(x[0], x[1], x[2], x[3]);
+          if (e == 0) p.ml[(ps + h) * 2] = top, p.ml[(ps + h) * 2 + 1] = l;
+        }
+      }
+      if (p.parts > 0 && hk == 0 && ht == 0 && threadIdx.x == 0) {
+        if (t0 == 0) p.cover[2 * b] = (int32_t)part;
+        if (t1 == steps) p.cover[2 * b + 1] = (int32_t)part;
+      }
+    }
+    if (p.parts == 0) break;
+    at += kSegCost + steps;
+    ++b;
+  }
+}
+
+// Joins the partial results of a request that was cut: slot 1 of its first part,
+// slot 0 of the others. One block per (request, query head).
+template <int DT>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p) {
+  __shared__ float red[256][4];
+  __shared__ float redl[256];
+  const int64_t b = blockIdx.x / a.Hq;
+  const int h = (int)(blockIdx.x - b * a.Hq);
+  const int first = p.cover[2 * b], last = p.cover[2 * b + 1];
+  if (first == last) return;
+  const int hk = h / p.G, ht = (h % p.G) / kHeadTile, hr = (h % p.G) % kHeadTile;
+  const int D = (int)a.cache.dim, n = last - first + 1;
+  auto row = [&](int i) {
+    const int64_t part = first + i;
+    return (((part * p.heads + hk) * p.tiles + ht) * 2 + (i == 0 ? 1 : 0)) * kHeadTile + hr;
+  };
+  float top = -INFINITY;
+  for (int i = threadIdx.x & 63; i < n; i += 64) top = fmaxf(top, p.ml[row(i) * 2]);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+  // threads: D / 4 columns by as many groups of partial results as fit
+  const int cols = D / 4, groups = 256 / cols;
+  const int grp = threadIdx.x / cols, e = (threadIdx.x - grp * cols) * 4;
+  float x[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+  if (grp < groups)
+    for (int i = grp; i < n; i += groups) {
+      const int64_t r = row(i);
+      const float pl = p.ml[r * 2 + 1], f = join_factor(p.ml[r * 2], pl, top);
+      const float4 v = *(const float4*)(p.o + r * D + e);
+      l = fmaf(f, pl, l);
+      x[0] = fmaf(f, v.x, x[0]);
+      x[1] = fmaf(f, v.y, x[1]);
+      x[2] = fmaf(f, v.z, x[2]);
+      x[3] = fmaf(f, v.w, x[3]);
+    }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) red[threadIdx.x][j] = x[j];
+  redl[threadIdx.x] = l;
+  __syncthreads();
+  if ((int)threadIdx.x >= cols) return;
+  for (int k = 1; k < groups; ++k) {
+    l += redl[threadIdx.x + k * cols];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] += red[threadIdx.x + k * cols][j];
+  }
+  const float r = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] *= r;
+  const int64_t orow = b * a.Hq + h;
+  store4<DT>(a.out, orow * D + e, x);
+  if (e == 0 && a.lse)
+    a.lse[orow] = l == 0.f ? -INFINITY : top + (logf(l) - kProbShift<DT> * kLn2);
+}
+
+// Rows the matrix-core kernel can load: whole, aligned 16-byte units.
+bool aligned16(const AttnArgs& a, int eb) {
+  const fk_kv_cache_t& c = a.cache;
+  const int64_t s[] = {a.q_stride[0], a.q_stride[1], c.k_stride[0], c.k_stride[1], c.k_stride[2],
+                       c.v_stride[0], c.v_stride[1], c.v_stride[2], c.dim};
+  for (int64_t v : s)
+    if (v * eb % 16) return false;
+  return !(((uintptr_t)a.q | (uintptr_t)c.k | (uintptr_t)c.v | (uintptr_t)a.out) & 15);
+}
+
+constexpr int64_t kMaxBlocks = 1024;      // parts * heads * tiles of one call at most this or heads * tiles
+
+int64_t head_tiles(int64_t G) { return (G + kHeadTile - 1) / kHeadTile; }
+
+// Parts per (cache head, head tile): the chip's blocks shared out.
+int64_t parts_of(int64_t units) { return units >= kMaxBlocks ? 1 : kMaxBlocks / units; }
+
+template <int DT, int DP>
+hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
+  Plan p{};
+  p.heads = (int)a.cache.heads;
+  p.G = (int)(a.Hq / a.cache.heads);
+  p.tiles = (int)head_tiles(p.G);
+  p.page = fast_div((uint32_t)a.cache.page);
+  const int64_t units = (int64_t)p.heads * p.tiles;
+  const int64_t most = a.max_len > 0 && a.max_len < a.width * a.cache.page ? a.max_len : a.width * a.cache.page;
+  const bool cut = most > 512;
+  p.parts = cut ? (int)parts_of(units) : 0;
+  if (cut) {
+    const int64_t slots = units * p.parts * 2 * kHeadTile;
+    char* w = (char*)ws;
+    p.o = (float*)w;
+    p.ml = (float*)(w + slots * a.cache.dim * 4);
+    p.cover = (int32_t*)(w + slots * a.cache.dim * 4 + slots * 8);
+  }
+  const int64_t blocks = units * (cut ? p.parts : a.B);
+  if (blocks > 0x7FFFFFFF || a.B * a.Hq > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const auto kernel = a.softcap > 0.f || a.cache.key_bias ? attn_mfma_kernel<DT, DP, true>
+                                                          : attn_mfma_kernel<DT, DP, false>;
+  kernel<<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !cut) return e;
+  attn_join_kernel<DT><<<(unsigned)(a.B * a.Hq), 256, 0, s>>>(a, p);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t run(const AttnArgs& a, void* ws, hipStream_t s) {
+  const int64_t D = a.cache.dim;
+  if (D > 256 || !aligned16(a, Val<DT>::bytes)) return run_any<DT>(a, s);
+  return D <= 64 ? run_mfma<DT, 64>(a, ws, s)
+         : D <= 128 ? run_mfma<DT, 128>(a, ws, s)
+                    : run_mfma<DT, 256>(a, ws, s);
+}
+
 }  // namespace
 
-size_t attn_ws_bytes(int64_t, int64_t, int64_t, int64_t) { return 256; }
+size_t attn_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+  if (D > 256) return 256;
+  const int64_t units = Hkv * head_tiles(Hq / Hkv);
+  const size_t slots = (size_t)units * parts_of(units) * 2 * kHeadTile;
+  return slots * D * 4 + slots * 8 + (size_t)B * 8;
+}
 
-hipError_t launch_paged_attn(const AttnArgs& a, int dt, void*, hipStream_t s) {
+hipError_t launch_paged_attn(const AttnArgs& a, int dt, void* ws, hipStream_t s) {
   if (a.B == 0) return hipSuccess;
-  return dt == FK_F32 ? run_any<FK_F32>(a, s)
-         : dt == FK_F16 ? run_any<FK_F16>(a, s)
-                        : run_any<FK_BF16>(a, s);
+  return dt == FK_F32   ? run<FK_F32>(a, ws, s)
+         : dt == FK_F16 ? run<FK_F16>(a, ws, s)
+                        : run<FK_BF16>(a, ws, s);
 }
 
 }  // namespace fk

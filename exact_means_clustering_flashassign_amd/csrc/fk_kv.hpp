@@ -10,16 +10,19 @@ namespace fk {
 template <int DT> struct Val;
 template <> struct Val<FK_F32> {
   using type = float;
+  static constexpr int bytes = 4;
   __device__ static __forceinline__ float get(const float* p) { return *p; }
   __device__ static __forceinline__ void put(float* p, float f) { *p = f; }
 };
 template <> struct Val<FK_F16> {
   using type = uint16_t;
+  static constexpr int bytes = 2;
   __device__ static __forceinline__ float get(const uint16_t* p) { return f16_bits_to_f32(*p); }
   __device__ static __forceinline__ void put(uint16_t* p, float f) { *p = f32_to_f16_bits(f); }
 };
 template <> struct Val<FK_BF16> {
   using type = uint16_t;
+  static constexpr int bytes = 2;
   __device__ static __forceinline__ float get(const uint16_t* p) { return bf16_bits_to_f32(*p); }
   __device__ static __forceinline__ void put(uint16_t* p, float f) {
     // the integer rounding would carry a NaN's payload into infinity
