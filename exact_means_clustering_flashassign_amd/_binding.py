@@ -7,7 +7,9 @@ current stream. Nothing here computes: a missing or broken library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from typing import Optional, Tuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -313,60 +315,79 @@ def fk_lloyd_host(x_host, init, max_iter: int, tol: float, chunk: int, ids=None,
 
 # ---------------------------------------------------------------------------
 # paged key-value cache
+# These run once per layer and generated token, where a few microseconds of
+# argument handling show: attributes are read once, structures and strides are
+# packed as bytes, and the words of an error are only made when there is one.
 # ---------------------------------------------------------------------------
-_strides2 = ctypes.c_int64 * 2
+_pack2 = struct.Struct("2q").pack
+_pack_cache = struct.Struct("3P4q9q").pack      # the layout of fk_kv_cache_t
 
 
-def _on(t, name, dtype, shape, dev):
-    """Checks of a contiguous device tensor on `dev`; its address."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _raw_stream(index: int) -> int:
+    return _torch_c()._cuda_getCurrentRawStream(index)
+
+
+@functools.lru_cache(None)
+def _torch_c():
+    return _torch()._C
+
+
+@functools.lru_cache(None)
+def _codes():
+    torch = _torch()
+    return {torch.float32: FK_F32, torch.float16: FK_F16, torch.bfloat16: FK_BF16}
+
+
+def _gpu_index(t, name) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    return index
+
+
+def _on(t, name, dtype, shape, index):
+    """Checks of a contiguous tensor on device `index`; its address."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"cuda:{index}, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on "
+                         f"{t.device}")
     return t.data_ptr()
 
 
-def _rows(t, name, dtype, dims, dev):
-    """Checks of a strided device tensor with contiguous rows, for the forward-only calls."""
-    if t.dim() != dims or t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name} must be a {dims}-dimensional {dtype} tensor on {dev}, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
-    if t.requires_grad:
-        raise ValueError(f"{name} requires grad: the call has no backward pass, detach it first")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"the elements of {name}'s rows must be contiguous")
-    return t.stride()
+def _rows(t, name, dtype, dims, index):
+    """Checks of a tensor with contiguous rows, for the forward-only calls; its strides."""
+    s = t.stride()
+    if len(s) != dims or t.dtype is not dtype or t.get_device() != index or t.requires_grad or \
+            (s[-1] != 1 and t.shape[-1] > 1):
+        if t.requires_grad:
+            raise ValueError(f"{name} requires grad: the call has no backward pass, detach it first")
+        raise ValueError(f"{name} must be a {dims}-dimensional {dtype} tensor with contiguous rows "
+                         f"on cuda:{index}, got {t.dtype} {tuple(t.shape)} strides {s} on "
+                         f"{t.device}")
+    return s
 
 
-def _first_device(t, name):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    return t.device
-
-
-def _kv_cache(k_cache, v_cache, key_bias, dtype, heads, dim, dev):
-    """fk_kv_cache_t of (pages, page, heads, dim) tensors in any axis order of memory."""
-    sk = _rows(k_cache, "k_cache", dtype, 4, dev)
-    sv = _rows(v_cache, "v_cache", dtype, 4, dev)
+def _kv_cache(k_cache, v_cache, key_bias, dtype, heads, dim, index):
+    """fk_kv_cache_t (as bytes) of (pages, page, heads, dim) tensors in any axis order of
+    memory, and its number of heads."""
+    sk = _rows(k_cache, "k_cache", dtype, 4, index)
+    sv = _rows(v_cache, "v_cache", dtype, 4, index)
     shape = k_cache.shape
-    if v_cache.shape != shape:
-        raise ValueError(f"v_cache must have k_cache's shape {tuple(shape)}, got "
-                         f"{tuple(v_cache.shape)}")
-    if shape[3] != dim or (heads is not None and shape[2] != heads):
-        raise ValueError(f"k_cache {tuple(shape)} does not hold {heads} heads of {dim} elements")
-    c = fk_kv_cache_t(k_cache.data_ptr(), v_cache.data_ptr(), None, *shape, sk[:3], sv[:3])
+    if v_cache.shape != shape or shape[3] != dim or (heads and shape[2] != heads):
+        raise ValueError(f"k_cache and v_cache must have shape (pages, page, {heads or 'heads'}, "
+                         f"{dim}), got {tuple(shape)} and {tuple(v_cache.shape)}")
+    bp, sb = None, (0, 0, 0)
     if key_bias is not None:
-        sb = _rows(key_bias.unsqueeze(-1), "key_bias", _torch().float32, 4, dev)
-        if key_bias.shape != shape[:3]:
-            raise ValueError(f"key_bias must have shape {tuple(shape[:3])}, got "
-                             f"{tuple(key_bias.shape)}")
-        c.key_bias = key_bias.data_ptr()
-        c.bias_stride[:] = sb[:3]
-    return c
+        sb = key_bias.stride()
+        if key_bias.shape != shape[:3] or key_bias.dtype is not _torch().float32 or \
+                key_bias.get_device() != index or key_bias.requires_grad:
+            raise ValueError(f"key_bias must be float32 of shape {tuple(shape[:3])} on "
+                             f"cuda:{index} without grad, got {key_bias.dtype} "
+                             f"{tuple(key_bias.shape)} on {key_bias.device}")
+        bp = key_bias.data_ptr()
+    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), bp or 0, *shape, *sk[:3], *sv[:3],
+                       *sb), shape[2]
 
 
 def fk_page_tables(len_old, len_new, free_pages, page: int, width: int, tokens: int, table=None,
@@ -375,32 +396,36 @@ def fk_page_tables(len_old, len_new, free_pages, page: int, width: int, tokens: 
     len_new (B) more, pages taken from free_pages (F) in order; table (B,W)
     holds the pages they have (None: none). All int32 on the GPU. Returns
     (table (B,width), lens (B), cu_tokens (B+1), cu_pages (B+1), slots (tokens),
-    positions (tokens)); `out`: those six tensors, to write into."""
+    positions (tokens)), views of one buffer; `out`: those six tensors, to
+    write into."""
     torch = _torch()
-    i32, dev = torch.int32, _first_device(len_old, "len_old")
-    if len_old.dim() != 1 or free_pages.dim() != 1:
-        raise ValueError("len_old and free_pages must be one-dimensional")
-    B, width, tokens = len_old.shape[0], int(width), int(tokens)
-    shapes = ((B, width), (B,), (B + 1,), (B + 1,), (tokens,), (tokens,))
+    i32, index = torch.int32, _gpu_index(len_old, "len_old")
+    B = len_old.numel()
+    p_old = _on(len_old, "len_old", i32, (B,), index)
+    p_new = _on(len_new, "len_new", i32, (B,), index)
+    n_free = free_pages.numel()
+    p_free = _on(free_pages, "free_pages", i32, (n_free,), index)
+    p_in, width_in = None, 0
+    if table is not None:
+        width_in = table.shape[-1]
+        p_in = _on(table, "table", i32, (B, width_in), index)
     if out is None:
         if width < 1 or tokens < 0:
             raise ValueError("width must be at least 1 and tokens non-negative")
-        out = tuple(torch.empty(s, dtype=i32, device=dev) for s in shapes)
-    names = ("table", "lens", "cu_tokens", "cu_pages", "slots", "positions")
-    if len(out) != 6:
-        raise ValueError("out must hold " + ", ".join(names))
-    width_in, tin = 0, None
-    if table is not None:
-        if table.dim() != 2:
-            raise ValueError("table must be two-dimensional")
-        width_in = table.shape[1]
-        tin = _on(table, "table", i32, (B, width_in), dev)
-    st = load().fk_page_tables(
-        _on(len_old, "len_old", i32, (B,), dev), _on(len_new, "len_new", i32, (B,), dev), tin,
-        width_in, _on(free_pages, "free_pages", i32, free_pages.shape, dev), free_pages.shape[0],
-        B, int(page), width, tokens,
-        *(_on(t, "out " + n, i32, s, dev) for t, n, s in zip(out, names, shapes)),
-        _stream(len_old))
+        n = B * width
+        buf = torch.empty(n + 3 * B + 2 + 2 * tokens, dtype=i32, device=len_old.device)
+        o = buf.split_with_sizes((n, B, B + 1, B + 1, tokens, tokens))
+        out = (o[0].view(B, width), *o[1:])
+        p = buf.data_ptr()
+        n, B4, T4 = 4 * n, 4 * B, 4 * tokens
+        ps = (p, p + n, p + n + B4, p + n + 2 * B4 + 4, p + n + 3 * B4 + 8, p + n + 3 * B4 + 8 + T4)
+    else:
+        if len(out) != 6:
+            raise ValueError("out must hold table, lens, cu_tokens, cu_pages, slots, positions")
+        shapes = ((B, width), (B,), (B + 1,), (B + 1,), (tokens,), (tokens,))
+        ps = [_on(t, f"out[{i}]", i32, s, index) for i, (t, s) in enumerate(zip(out, shapes))]
+    st = load().fk_page_tables(p_old, p_new, p_in, width_in, p_free, n_free, B, page, width,
+                               tokens, *ps, _raw_stream(index))
     _check(st, "fk_page_tables")
     return tuple(out)
 
@@ -415,54 +440,62 @@ def fk_qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-
     (pages, page, Hkv, D), with a key_bias (pages, page, Hkv) of 0. Returns
     (q_out, k_out); k_out is None with a cache unless given."""
     torch = _torch()
-    dt, dev = q.dtype, _first_device(q, "q")
-    code = dtype_code(dt)
-    sq, sk = _rows(q, "q", dt, 3, dev), _rows(k, "k", dt, 3, dev)
+    dt, index = q.dtype, _gpu_index(q, "q")
+    code = _codes().get(dt)
+    if code is None:
+        code = dtype_code(dt)            # says what is supported
+    sq, sk = _rows(q, "q", dt, 3, index), _rows(k, "k", dt, 3, index)
     T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    if k.shape != (T, Hkv, D):
-        raise ValueError(f"k must have shape {(T, 'Hkv', D)}, got {tuple(k.shape)}")
-    cache = vp = sv = sp = None
+    ks = k.shape
+    Hkv = ks[1]
+    if ks != (T, Hkv, D):
+        raise ValueError(f"k must have shape {(T, 'Hkv', D)}, got {tuple(ks)}")
+    cache = vp = sv = sp = p_ko = None
     if slots is not None:
         if v is None or k_cache is None or v_cache is None:
             raise ValueError("slots need v, k_cache and v_cache")
-        sv = _rows(v, "v", dt, 3, dev)
-        if v.shape != k.shape:
-            raise ValueError(f"v must have k's shape {tuple(k.shape)}, got {tuple(v.shape)}")
-        vp, sv = v.data_ptr(), _strides2(sv[0], sv[1])
-        sp = _on(slots, "slots", torch.int32, (T,), dev)
-        cache = ctypes.byref(_kv_cache(k_cache, v_cache, key_bias, dt, Hkv, D, dev))
+        sv = _rows(v, "v", dt, 3, index)
+        if v.shape != ks:
+            raise ValueError(f"v must have k's shape {tuple(ks)}, got {tuple(v.shape)}")
+        vp, sv = v.data_ptr(), _pack2(sv[0], sv[1])
+        sp = _on(slots, "slots", torch.int32, (T,), index)
+        cache = _kv_cache(k_cache, v_cache, key_bias, dt, Hkv, D, index)[0]
     elif v is not None or k_cache is not None or v_cache is not None or key_bias is not None:
         raise ValueError("v and the cache need slots")
     elif k_out is None:
-        k_out = torch.empty((T, Hkv, D), dtype=dt, device=dev)
+        k_out = torch.empty((T, Hkv, D), dtype=dt, device=q.device)
+    if k_out is not None:
+        p_ko = _on(k_out, "k_out", dt, (T, Hkv, D), index)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+        q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
+    p_qw = p_kw = rp = pp = None
+    if q_weight is not None:
+        p_qw = _on(q_weight, "q_weight", dt, (D,), index)
+        p_kw = _on(k_weight, "k_weight", dt, (D,), index)
     rot = max_pos = 0
-    rp = pp = None
     if rope is not None:
         if rope.dim() != 2 or positions is None:
             raise ValueError("rope must be (max_pos, rot), with positions")
         max_pos, rot = rope.shape
-        rp = _on(rope, "rope", torch.float32, (max_pos, rot), dev)
-        pp = _on(positions, "positions", torch.int32, (T,), dev)
+        rp = _on(rope, "rope", torch.float32, (max_pos, rot), index)
+        pp = _on(positions, "positions", torch.int32, (T,), index)
     st = load().fk_qk_norm_rope(
-        q.data_ptr(), _strides2(sq[0], sq[1]), k.data_ptr(), _strides2(sk[0], sk[1]), vp, sv,
-        code, T, Hq, Hkv, D,
-        None if q_weight is None else _on(q_weight, "q_weight", dt, (D,), dev),
-        None if k_weight is None else _on(k_weight, "k_weight", dt, (D,), dev), eps,
-        rp, max_pos, rot, bool(interleaved), pp, sp, cache,
-        _on(q_out, "q_out", dt, (T, Hq, D), dev),
-        None if k_out is None else _on(k_out, "k_out", dt, (T, Hkv, D), dev), _stream(q))
+        q.data_ptr(), _pack2(sq[0], sq[1]), k.data_ptr(), _pack2(sk[0], sk[1]), vp, sv, code, T,
+        Hq, Hkv, D, p_qw, p_kw, eps, rp, max_pos, rot, interleaved, pp, sp, cache,
+        _on(q_out, "q_out", dt, (T, Hq, D), index), p_ko, _raw_stream(index))
     _check(st, "fk_qk_norm_rope")
     return q_out, k_out
 
 
-def fk_workspace_size_attn(dtype, B: int, Hq: int, Hkv: int, D: int) -> int:
-    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+@functools.lru_cache(256)
+def _attn_ws(code, B, Hq, Hkv, D):
     return int(load().fk_workspace_size_attn(code, B, Hq, Hkv, D))
+
+
+def fk_workspace_size_attn(dtype, B: int, Hq: int, Hkv: int, D: int) -> int:
+    return _attn_ws(dtype if isinstance(dtype, int) else dtype_code(dtype), B, Hq, Hkv, D)
 
 
 def fk_paged_attn(q, k_cache, v_cache, table, lens, scale: Optional[float] = None,
@@ -474,32 +507,43 @@ def fk_paged_attn(q, k_cache, v_cache, table, lens, scale: Optional[float] = Non
     default. Returns out (B,Hq,D), and with return_lse (or lse given) the
     natural log of the softmax's sum, (B,Hq) fp32."""
     torch = _torch()
-    dt, dev = q.dtype, _first_device(q, "q")
-    code = dtype_code(dt)
-    sq = _rows(q, "q", dt, 3, dev)
+    dt, index = q.dtype, _gpu_index(q, "q")
+    code = _codes().get(dt)
+    if code is None:
+        code = dtype_code(dt)            # says what is supported
+    sq = _rows(q, "q", dt, 3, index)
     B, Hq, D = q.shape
-    cache = _kv_cache(k_cache, v_cache, key_bias, dt, None, D, dev)
-    if table.dim() != 2 or table.shape[0] != B:
-        raise ValueError(f"table must have shape {(B, 'W')}, got {tuple(table.shape)}")
-    st2 = _rows(table, "table", torch.int32, 2, dev)
-    width = table.shape[1]
+    cache, heads = _kv_cache(k_cache, v_cache, key_bias, dt, 0, D, index)
+    st2 = _rows(table, "table", torch.int32, 2, index)
+    rows, width = table.shape
+    if rows != B:
+        raise ValueError(f"table must have {B} rows, got {tuple(table.shape)}")
+    p_lens = _on(lens, "lens", torch.int32, (B,), index)
+    need = _attn_ws(code, B, Hq, heads, D)
+    if need == 0:
+        raise ValueError(f"{Hq} query heads of {D} do not go with {heads} cache heads")
+    dev = q.device
     if out is None:
         out = torch.empty((B, Hq, D), dtype=dt, device=dev)
-    if lse is None and return_lse:
+        p_out = out.data_ptr()
+    else:
+        p_out = _on(out, "out", dt, (B, Hq, D), index)
+    p_lse = None
+    if lse is not None:
+        p_lse = _on(lse, "lse", torch.float32, (B, Hq), index)
+    elif return_lse:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-    lib = load()
-    need = lib.fk_workspace_size_attn(code, B, Hq, cache.heads, D)
-    if need == 0:
-        raise ValueError(f"{Hq} query heads of {D} do not go with {cache.heads} cache heads")
+        p_lse = lse.data_ptr()
     if ws is None:
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    st = lib.fk_paged_attn(
-        q.data_ptr(), _strides2(sq[0], sq[1]), code, B, Hq, ctypes.byref(cache), table.data_ptr(),
-        st2[0] if B > 1 else width, width, _on(lens, "lens", torch.int32, (B,), dev),
-        int(max_len), D ** -0.5 if scale is None else scale, softcap,
-        _on(out, "out", dt, (B, Hq, D), dev),
-        None if lse is None else _on(lse, "lse", torch.float32, (B, Hq), dev),
-        _on(ws, "ws", torch.uint8, ws.shape, dev), ws.numel(), _stream(q))
+        p_ws = ws.data_ptr()
+    else:
+        need = ws.numel()
+        p_ws = _on(ws, "ws", torch.uint8, (need,), index)
+    st = load().fk_paged_attn(
+        q.data_ptr(), _pack2(sq[0], sq[1]), code, B, Hq, cache, table.data_ptr(),
+        st2[0] if B > 1 else width, width, p_lens, max_len, D ** -0.5 if scale is None else scale,
+        softcap, p_out, p_lse, p_ws, need, _raw_stream(index))
     _check(st, "fk_paged_attn")
     return out if lse is None else (out, lse)
 

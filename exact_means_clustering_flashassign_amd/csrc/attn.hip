@@ -120,6 +120,7 @@ hipError_t run_any(const AttnArgs& a, hipStream_t s) {
 // VE m .. VE m + VE - 1 (16 lanes cover a row), picking tile t's element of
 // each row with byte permutes. Nothing goes through LDS but row addresses.
 constexpr int kHeadTile = 16;
+constexpr int kMaxBlocks = 1024;   // blocks of a call over all parts, unless its heads alone are more
 
 template <int DT, int DP> struct Shape {
   static constexpr int tiles = DT == FK_F32 ? 1 : 2;        // 16-key tiles per step
@@ -168,8 +169,14 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
 // inside one part is finished there; one that is cut leaves a partial
 // result per part, at most two a block (one that started before, one that goes
 // on), joined by attn_join_kernel.
-constexpr int kSegCost = 8;
-constexpr int kMinSteps = 8;      // steps worth a block of its own
+#ifndef SEGC
+#define SEGC 8
+#endif
+#ifndef MINC
+#define MINC 8
+#endif
+constexpr int kSegCost = SEGC;
+constexpr int kMinCost = MINC;      // least cost worth a block of its own
 
 struct Plan {
   int parts;            // blocks per (cache head, head tile); 0: one per request
@@ -479,7 +486,7 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, const Plan& p, in
   }
   Start st;
   st.total = total;
-  const int64_t most = total / (kMinSteps + kSegCost);
+  const int64_t most = total / kMinCost;
   st.parts = (int)(most < 1 ? 1 : (most < p.parts ? most : p.parts));
   st.lo = w < st.parts ? total * w / st.parts : total;
   st.hi = w < st.parts ? total * (w + 1) / st.parts : total;
@@ -512,8 +519,14 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const float* x) {
   }
 }
 
+// Blocks a CU holds (registers): the parts of a call are as many as the chip holds at once.
+#ifndef BPC128
+#define BPC128 2
+#endif
+template <int DP> constexpr int kBlocksPerCu = DP == 64 ? 3 : (DP == 128 ? BPC128 : 1);
+
 template <int DT, int DP, bool EXTRA>
-__global__ __launch_bounds__(kWaves * 64) void attn_mfma_kernel(AttnArgs a, Plan p) {
+__global__ __launch_bounds__(kWaves * 64, kBlocksPerCu<DP>) void attn_mfma_kernel(AttnArgs a, Plan p) {
   using S = Shape<DT, DP>;
   __shared__ Rows<DT, DP> rows[kWaves][2];
   __shared__ float so[kWaves][kHeadTile][S::ldo];
@@ -602,6 +615,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_mfma_kernel(AttnArgs a, Plan
 // slot 0 of the others. One block per (request, query head).
 template <int DT>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p) {
+  __shared__ float fac[kMaxBlocks], part_l[kMaxBlocks];
   __shared__ float red[256][4];
   __shared__ float redl[256];
   const int64_t b = blockIdx.x / a.Hq;
@@ -614,25 +628,33 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Plan p) {
     const int64_t part = first + i;
     return (((part * p.heads + hk) * p.tiles + ht) * 2 + (i == 0 ? 1 : 0)) * kHeadTile + hr;
   };
+  // every thread: maximum over all parts; factors and the sum of the parts' sums
   float top = -INFINITY;
   for (int i = threadIdx.x & 63; i < n; i += 64) top = fmaxf(top, p.ml[row(i) * 2]);
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const float2 ml = *(const float2*)(p.ml + row(i) * 2);
+    fac[i] = join_factor(ml.x, ml.y, top);
+    part_l[i] = ml.y;
+  }
+  __syncthreads();
   // threads: D / 4 columns by as many groups of partial results as fit
   const int cols = D / 4, groups = 256 / cols;
   const int grp = threadIdx.x / cols, e = (threadIdx.x - grp * cols) * 4;
   float x[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-  if (grp < groups)
+  if (grp < groups) {
+#pragma unroll 4
     for (int i = grp; i < n; i += groups) {
-      const int64_t r = row(i);
-      const float pl = p.ml[r * 2 + 1], f = join_factor(p.ml[r * 2], pl, top);
-      const float4 v = *(const float4*)(p.o + r * D + e);
-      l = fmaf(f, pl, l);
+      const float f = fac[i];
+      const float4 v = *(const float4*)(p.o + row(i) * D + e);
+      l = fmaf(f, part_l[i], l);
       x[0] = fmaf(f, v.x, x[0]);
       x[1] = fmaf(f, v.y, x[1]);
       x[2] = fmaf(f, v.z, x[2]);
       x[3] = fmaf(f, v.w, x[3]);
     }
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) red[threadIdx.x][j] = x[j];
   redl[threadIdx.x] = l;
@@ -662,12 +684,10 @@ bool aligned16(const AttnArgs& a, int eb) {
   return !(((uintptr_t)a.q | (uintptr_t)c.k | (uintptr_t)c.v | (uintptr_t)a.out) & 15);
 }
 
-constexpr int64_t kMaxBlocks = 1024;      // parts * heads * tiles of one call at most this or heads * tiles
-
 int64_t head_tiles(int64_t G) { return (G + kHeadTile - 1) / kHeadTile; }
 
-// Parts per (cache head, head tile): the chip's blocks shared out.
-int64_t parts_of(int64_t units) { return units >= kMaxBlocks ? 1 : kMaxBlocks / units; }
+// Parts per (cache head, head tile): `blocks` shared out.
+int64_t parts_of(int64_t blocks, int64_t units) { return units >= blocks ? 1 : blocks / units; }
 
 template <int DT, int DP>
 hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
@@ -679,7 +699,8 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   const int64_t units = (int64_t)p.heads * p.tiles;
   const int64_t most = a.max_len > 0 && a.max_len < a.width * a.cache.page ? a.max_len : a.width * a.cache.page;
   const bool cut = most > 512;
-  p.parts = cut ? (int)parts_of(units) : 0;
+  const int64_t resident = (int64_t)device_cus() * kBlocksPerCu<DP>;
+  p.parts = cut ? (int)parts_of(resident < kMaxBlocks ? resident : kMaxBlocks, units) : 0;
   if (cut) {
     const int64_t slots = units * p.parts * 2 * kHeadTile;
     char* w = (char*)ws;
@@ -712,7 +733,7 @@ hipError_t run(const AttnArgs& a, void* ws, hipStream_t s) {
 size_t attn_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   if (D > 256) return 256;
   const int64_t units = Hkv * head_tiles(Hq / Hkv);
-  const size_t slots = (size_t)units * parts_of(units) * 2 * kHeadTile;
+  const size_t slots = (size_t)units * parts_of(kMaxBlocks, units) * 2 * kHeadTile;
   return slots * D * 4 + slots * 8 + (size_t)B * 8;
 }
 
