@@ -149,19 +149,6 @@ __device__ __forceinline__ uint4 load16(uint64_t addr) {
 // Keys that do not count are read from here: zeros, whatever the cache holds.
 __device__ const uint4 zero_row[64] = {};
 
-// n / d for n < 2^31 by a multiplication (Granlund and Montgomery).
-struct FastDiv {
-  uint32_t mul, shift, d;
-};
-FastDiv fast_div(uint32_t d) {
-  uint32_t l = 0;
-  while (((uint64_t)1 << l) < d) ++l;
-  return {(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1), l, d};
-}
-__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
-  return (__umulhi(n, f.mul) + n) >> f.shift;
-}
-
 // How the work is shared. Request b costs its steps of `keys` keys plus
 // kSegCost (a request's own share: queries, joining the waves, storing). The
 // requests' costs are laid end to end and cut into equal parts, one per block of
@@ -200,14 +187,12 @@ template <> struct Mfma16<FK_F16> {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a),
                                                   __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
   }
-  typedef _Float16 T;
 };
 template <> struct Mfma16<FK_BF16> {
   __device__ static __forceinline__ floatx4_t run(uint4 a, uint4 b, floatx4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
   }
-  typedef __bf16 T;
 };
 // fp32: element j of the lanes' 16 bytes in turn, four k per product.
 template <> struct Mfma16<FK_F32> {
@@ -418,7 +403,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
       // Probabilities as the sum of two 16-bit numbers: one alone would round
       // each to 8 (bf16) or 11 bits, an error as large as the result's own
       // rounding. The second product rides on matrix units that are idle anyway.
-      typedef typename Mfma16<DT>::T T;
+      typedef typename Val<DT>::arith T;
       typedef T T8 __attribute__((ext_vector_type(8)));
       T8 hi, lo;
 #pragma unroll
@@ -512,7 +497,7 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const float* x) {
   if constexpr (DT == FK_F32) {
     *(float4*)((float*)out + at) = make_float4(x[0], x[1], x[2], x[3]);
   } else {
-    typedef typename Mfma16<DT>::T T;
+    typedef typename Val<DT>::arith T;
     typedef T T4 __attribute__((ext_vector_type(4)));
     T4 v = {(T)x[0], (T)x[1], (T)x[2], (T)x[3]};
     *(T4*)((T*)out + at) = v;

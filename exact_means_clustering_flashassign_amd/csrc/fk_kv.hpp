@@ -10,18 +10,21 @@ namespace fk {
 template <int DT> struct Val;
 template <> struct Val<FK_F32> {
   using type = float;
+  using arith = float;      // the type as the compiler's conversions know it
   static constexpr int bytes = 4;
   __device__ static __forceinline__ float get(const float* p) { return *p; }
   __device__ static __forceinline__ void put(float* p, float f) { *p = f; }
 };
 template <> struct Val<FK_F16> {
   using type = uint16_t;
+  using arith = _Float16;
   static constexpr int bytes = 2;
   __device__ static __forceinline__ float get(const uint16_t* p) { return f16_bits_to_f32(*p); }
   __device__ static __forceinline__ void put(uint16_t* p, float f) { *p = f32_to_f16_bits(f); }
 };
 template <> struct Val<FK_BF16> {
   using type = uint16_t;
+  using arith = __bf16;
   static constexpr int bytes = 2;
   __device__ static __forceinline__ float get(const uint16_t* p) { return bf16_bits_to_f32(*p); }
   __device__ static __forceinline__ void put(uint16_t* p, float f) {
@@ -29,6 +32,19 @@ template <> struct Val<FK_BF16> {
     *p = f == f ? f32_to_bf16_bits(f) : (uint16_t)0x7FC0;
   }
 };
+
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery's method).
+struct FastDiv {
+  uint32_t mul, shift, d;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while (((uint64_t)1 << l) < d) ++l;
+  return {(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1), l, d};
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
+  return (__umulhi(n, f.mul) + n) >> f.shift;
+}
 
 struct TablesArgs {
   const int32_t *len_old, *len_new, *table_in, *free_pages;

@@ -84,11 +84,216 @@ __global__ __launch_bounds__(kWaves * 64) void rope_any_kernel(RopeArgs a, int64
   }
 }
 
+// ---------------------------------------------------------------------------
+// Rows in whole VE-element units (16 or 8 bytes)
+// ---------------------------------------------------------------------------
+// Memory-bound: each element is read and written once. A lane holds two units of
+// a row, for pairs (i, i + rot/2) the two halves of VE pairs, so a pair is never
+// split between lanes; L lanes make a row and the wave takes 64 / L rows a pass.
+// A wave stays with one token: its cosines, sines and both weights are loaded
+// once and serve all rows it takes.
+struct RopePlan {
+  int units, hp, rem;        // units a row; pairs of units that rotate; others, two by two
+  int L, rp;                 // lanes a row (a power of two), rows a pass
+  int rows, passes;          // rows a token, passes a token
+  int ppw, wpt;              // passes a wave, waves a token
+  FastDiv page;
+};
+
+template <int DT, int VE> struct Unit {
+  typedef typename Val<DT>::arith T;
+  typedef T vec __attribute__((ext_vector_type(VE)));
+};
+
+template <int DT, int VE, bool INTER>
+__global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopePlan p,
+                                                               int64_t waves) {
+  typedef typename Unit<DT, VE>::T T;
+  typedef typename Unit<DT, VE>::vec V;
+  const int lane = threadIdx.x & 63;
+  const int64_t wave =
+      (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (wave >= waves) return;
+  const int64_t t = wave / p.wpt;
+  const int pass0 = (int)(wave - t * p.wpt) * p.ppw;
+  const int pass1 = min(pass0 + p.ppw, p.passes);
+
+  // this lane's units of every row it meets
+  const int j = lane & (p.L - 1), sub = lane / p.L;
+  const bool turn = j < p.hp;
+  const int ua = turn ? j : j + p.hp;
+  const int ub = turn ? j + p.hp : ua + p.rem;
+  const bool va = j < p.hp + p.rem, vb = va && ub < p.units;
+  const int ea = va ? ua * VE : 0, eb = vb ? ub * VE : 0;
+
+  const int half = (int)(a.rot >> 1);
+  float cs[VE] = {}, sn[VE] = {};
+  bool on[VE];               // pair i of this lane rotates
+#pragma unroll
+  for (int i = 0; i < VE; ++i) on[i] = !INTER && turn;
+  if (half) {
+    const int64_t pos = clamp_pos(a.positions[t], a.max_pos);
+    const float* row = a.rope + pos * a.rot;
+    if (INTER) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {         // first the pairs of unit a, then those of b
+        const int pr = (i < VE / 2 ? ea / 2 + i : eb / 2 + i - VE / 2);
+        on[i] = (i < VE / 2 ? va : vb) && pr < half;
+        if (on[i]) cs[i] = row[pr], sn[i] = row[half + pr];
+      }
+    } else if (turn) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) cs[i] = row[ea + i], sn[i] = row[half + ea + i];
+    }
+  }
+  const bool norm = a.q_weight != nullptr;
+  V wqa = {}, wqb = {}, wka = {}, wkb = {};
+  if (norm) {
+    const T *wq = (const T*)a.q_weight, *wk = (const T*)a.k_weight;
+    wqa = *(const V*)(wq + ea), wqb = *(const V*)(wq + eb);
+    wka = *(const V*)(wk + ea), wkb = *(const V*)(wk + eb);
+  }
+  bool slot_ok = false;
+  int64_t kslot = 0, vslot = 0, bslot = 0;
+  if (a.cache.k) {
+    const int32_t slot = __builtin_amdgcn_readfirstlane(a.slots[t]);
+    slot_ok = slot >= 0 && slot < a.cache.pages * a.cache.page;
+    if (slot_ok) {
+      const int64_t page = div_by(slot, p.page), tok = slot - page * p.page.d;
+      kslot = page * a.cache.k_stride[0] + tok * a.cache.k_stride[1];
+      vslot = page * a.cache.v_stride[0] + tok * a.cache.v_stride[1];
+      bslot = page * a.cache.bias_stride[0] + tok * a.cache.bias_stride[1];
+    }
+  }
+
+  struct Row {
+    V a, b;
+    int kind, h;             // 0 query, 1 key, 2 value, 3 none
+  };
+  auto load = [&](int pass) {
+    Row x;
+    const int r = pass * p.rp + sub;
+    x.kind = r < a.Hq ? 0 : (r < a.Hq + a.Hkv ? 1 : 2);
+    x.h = r - (x.kind == 0 ? 0 : (x.kind == 1 ? (int)a.Hq : (int)(a.Hq + a.Hkv)));
+    if (pass >= pass1 || r >= p.rows || !va) x.kind = 3;
+    x.a = V{}, x.b = V{};
+    if (x.kind == 3) return x;
+    const T* src = x.kind == 0   ? (const T*)a.q + t * a.q_stride[0] + x.h * a.q_stride[1]
+                   : x.kind == 1 ? (const T*)a.k + t * a.k_stride[0] + x.h * a.k_stride[1]
+                                 : (const T*)a.v + t * a.v_stride[0] + x.h * a.v_stride[1];
+    x.a = *(const V*)(src + ea);
+    if (vb) x.b = *(const V*)(src + eb);
+    return x;
+  };
+
+  Row next = load(pass0);
+  for (int pass = pass0; pass < pass1; ++pass) {
+    const Row x = next;
+    next = load(pass + 1);
+    float fa[VE], fb[VE];
+#pragma unroll
+    for (int i = 0; i < VE; ++i) fa[i] = (float)x.a[i], fb[i] = (float)x.b[i];
+    if (norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < VE; ++i) ss = fmaf(fa[i], fa[i], fmaf(fb[i], fb[i], ss));
+      for (int off = p.L >> 1; off >= 1; off >>= 1) ss += __shfl_xor(ss, off, 64);
+      const float r = 1.f / sqrtf(ss / (float)a.D + a.eps);
+      const V wa = x.kind == 0 ? wqa : wka, wb = x.kind == 0 ? wqb : wkb;
+#pragma unroll
+      for (int i = 0; i < VE; ++i) fa[i] = fa[i] * r * (float)wa[i], fb[i] = fb[i] * r * (float)wb[i];
+    }
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      // pair i: elements 2i, 2i+1 of a then b, or element i of both
+      float* e0 = !INTER ? &fa[i] : (i < VE / 2 ? &fa[2 * i] : &fb[2 * i - VE]);
+      float* e1 = !INTER ? &fb[i] : e0 + 1;
+      const float u = *e0, w = *e1;
+      *e0 = on[i] ? u * cs[i] - w * sn[i] : u;
+      *e1 = on[i] ? w * cs[i] + u * sn[i] : w;
+    }
+    if (x.kind == 3) continue;
+    V ya, yb;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) ya[i] = (T)fa[i], yb[i] = (T)fb[i];
+    T *y0 = nullptr, *y1 = nullptr;
+    if (x.kind == 0) {
+      y0 = (T*)a.q_out + (t * a.Hq + x.h) * a.D;
+    } else if (x.kind == 1) {
+      if (a.k_out) y0 = (T*)a.k_out + (t * a.Hkv + x.h) * a.D;
+      if (slot_ok) y1 = (T*)a.cache.k + kslot + x.h * a.cache.k_stride[2];
+      if (slot_ok && a.cache.key_bias && j == 0)
+        a.cache.key_bias[bslot + x.h * a.cache.bias_stride[2]] = 0.f;
+    } else {
+      ya = x.a, yb = x.b;                    // values as they are
+      if (slot_ok) y1 = (T*)a.cache.v + vslot + x.h * a.cache.v_stride[2];
+    }
+    if (y0) {
+      *(V*)(y0 + ea) = ya;
+      if (vb) *(V*)(y0 + eb) = yb;
+    }
+    if (y1) {
+      *(V*)(y1 + ea) = ya;
+      if (vb) *(V*)(y1 + eb) = yb;
+    }
+  }
+}
+
+// Whether every row starts at a multiple of `bytes` and holds whole units of it,
+// with rotated pairs either side by side or whole units apart.
+bool in_units(const RopeArgs& a, int eb, int bytes) {
+  const fk_kv_cache_t& c = a.cache;
+  int64_t s = a.D | a.q_stride[0] | a.q_stride[1] | a.k_stride[0] | a.k_stride[1];
+  uintptr_t p = (uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.q_out | (uintptr_t)a.k_out |
+                (uintptr_t)a.q_weight | (uintptr_t)a.k_weight;
+  if (c.k) {
+    s |= a.v_stride[0] | a.v_stride[1];
+    for (int i = 0; i < 3; ++i) s |= c.k_stride[i] | c.v_stride[i];
+    p |= (uintptr_t)a.v | (uintptr_t)c.k | (uintptr_t)c.v;
+  }
+  if (!a.interleaved) s |= a.rot / 2;
+  return s * eb % bytes == 0 && p % bytes == 0;     // powers of two: a bit below shows in the or
+}
+
+template <int DT, int VE>
+hipError_t run_vec(const RopeArgs& a, hipStream_t s) {
+  RopePlan p{};
+  p.units = (int)(a.D / VE);
+  p.hp = a.interleaved ? 0 : (int)(a.rot / 2 / VE);
+  p.rem = (p.units - 2 * p.hp + 1) / 2;
+  p.L = 1;
+  while (p.L < p.hp + p.rem) p.L *= 2;
+  p.rp = 64 / p.L;
+  const int64_t rows = a.Hq + a.Hkv * (a.cache.k ? 2 : 1);
+  if (rows > 1 << 30) return hipErrorInvalidConfiguration;
+  p.rows = (int)rows;
+  p.passes = (p.rows + p.rp - 1) / p.rp;
+  // A wave takes several passes once there are waves enough for every CU's slots.
+  const int64_t all = a.T * p.passes, want = (int64_t)device_cus() * 32;
+  p.ppw = (int)(all / want < 1 ? 1 : (all / want < p.passes ? all / want : p.passes));
+  p.wpt = (p.passes + p.ppw - 1) / p.ppw;
+  p.page = fast_div(a.cache.k ? (uint32_t)a.cache.page : 1);
+  const int64_t waves = a.T * p.wpt, blocks = (waves + kWaves - 1) / kWaves;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const auto kernel =
+      a.interleaved ? rope_vec_kernel<DT, VE, true> : rope_vec_kernel<DT, VE, false>;
+  kernel<<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, p, waves);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_qk_norm_rope(const RopeArgs& a, int dt, hipStream_t s) {
   const int64_t rows = a.T * (a.Hq + a.Hkv * (a.cache.k ? 2 : 1));
   if (rows == 0) return hipSuccess;
+  // 64 lanes of two units are the longest row
+  if (dt == FK_F32) {
+    if (a.D <= 512 && in_units(a, 4, 16)) return run_vec<FK_F32, 4>(a, s);
+  } else if (a.D <= 1024 && in_units(a, 2, 16)) {
+    return dt == FK_F16 ? run_vec<FK_F16, 8>(a, s) : run_vec<FK_BF16, 8>(a, s);
+  } else if (a.D <= 512 && in_units(a, 2, 8)) {
+    return dt == FK_F16 ? run_vec<FK_F16, 4>(a, s) : run_vec<FK_BF16, 4>(a, s);
+  }
   const int64_t blocks = (rows + kWaves - 1) / kWaves;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   const auto kernel = dt == FK_F32   ? rope_any_kernel<FK_F32>
