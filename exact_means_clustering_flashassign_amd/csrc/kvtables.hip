@@ -2,121 +2,189 @@
 //
 // Two running sums over the requests carry everything: new tokens (which
 // request a token of the step belongs to) and pages taken from the free list
-// (which free page an entry gets). tables_scan_kernel writes both; in
-// tables_fill_kernel every table entry and every token is then independent.
+// (which free page an entry gets). With them every table entry and every token is
+// independent. Up to kOwnScan requests, every block forms both sums for itself
+// in LDS (8 bytes a request from L2) and one launch does it all: the call is a
+// few microseconds of latency, and a second launch would add as much again.
+// Beyond that one block writes the sums first and the others read them.
 #include "fk_kv.hpp"
 
 namespace fk {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kOwnScan = 2048;
+constexpr int kPer = kOwnScan / kThreads;     // requests a thread sums, each round
+constexpr int kRun = 256;                     // entries or tokens a wave takes at a time
 
-struct Need {
-  int64_t old, len, held, need;   // held and need in pages
+struct Geometry {
+  FastDiv page;
+  int32_t cap;            // tokens that a row of pages holds, at most 2^31 - 1
+  int64_t row_items, items;
+  int32_t token_items;
 };
 
-__device__ __forceinline__ Need need_of(const TablesArgs& a, int64_t b) {
-  Need n;
-  const int32_t o = a.len_old[b], w = a.len_new[b];
-  n.old = o > 0 ? o : 0;
-  n.len = n.old + (w > 0 ? w : 0);
-  n.held = min((n.old + a.page - 1) / a.page, a.width);
-  n.need = min((n.len + a.page - 1) / a.page, a.width);
-  return n;
-}
+struct Need {
+  int32_t old, fresh;     // tokens held and new
+  int32_t held, need;     // pages of the old tokens and of all, at most a row
+};
 
 __device__ __forceinline__ int32_t to_i32(int64_t v) {
   return (int32_t)(v < 0x7FFFFFFF ? v : 0x7FFFFFFF);
 }
-
-// One block: running sums over the requests, kThreads at a time.
-__global__ __launch_bounds__(kThreads) void tables_scan_kernel(TablesArgs a) {
-  __shared__ int64_t part[2][kThreads];
-  int64_t base_t = 0, base_p = 0;
-  if (threadIdx.x == 0) a.cu_tokens[0] = a.cu_pages[0] = 0;
-  for (int64_t b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int64_t b = b0 + threadIdx.x;
-    int64_t t = 0, p = 0;
-    if (b < a.B) {
-      const Need n = need_of(a, b);
-      t = n.len - n.old;
-      p = n.need - n.held;
-      a.lens[b] = to_i32(n.len);
-    }
-    part[0][threadIdx.x] = t;
-    part[1][threadIdx.x] = p;
-    for (int off = 1; off < kThreads; off <<= 1) {
-      __syncthreads();
-      int64_t ut = 0, up = 0;
-      if ((int)threadIdx.x >= off) {
-        ut = part[0][threadIdx.x - off];
-        up = part[1][threadIdx.x - off];
-      }
-      __syncthreads();
-      part[0][threadIdx.x] += ut;
-      part[1][threadIdx.x] += up;
-    }
-    __syncthreads();
-    if (b < a.B) {
-      a.cu_tokens[b + 1] = to_i32(base_t + part[0][threadIdx.x]);
-      a.cu_pages[b + 1] = to_i32(base_p + part[1][threadIdx.x]);
-    }
-    base_t += part[0][kThreads - 1];
-    base_p += part[1][kThreads - 1];
-    __syncthreads();
-  }
+__device__ __forceinline__ int32_t pages_of(int32_t tokens, const Geometry& g) {
+  const int32_t n = min(tokens, g.cap);
+  return n > 0 ? (int32_t)div_by(n - 1, g.page) + 1 : 0;
+}
+__device__ __forceinline__ Need need_of(const TablesArgs& a, const Geometry& g, int64_t b) {
+  Need n;
+  n.old = max(a.len_old[b], 0);
+  n.fresh = max(a.len_new[b], 0);
+  n.held = pages_of(n.old, g);
+  n.need = pages_of(to_i32((int64_t)n.old + n.fresh), g);
+  return n;
 }
 
-// Physical page of entry j of request b: kept, from the free list, or -1.
+// Running sums of kOwnScan requests from b0 on, on top of *base (tokens, pages):
+// cu_t[i], cu_p[i] = sums before request b0 + i, capped; *base moves on.
+struct Sums {
+  int64_t t, p;
+};
+__device__ __forceinline__ Sums wave_scan(Sums v) {       // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t t = __shfl_up(v.t, off, 64), p = __shfl_up(v.p, off, 64);
+    if (lane >= off) v.t += t, v.p += p;
+  }
+  return v;
+}
+__device__ __forceinline__ Sums scan_requests(const TablesArgs& a, const Geometry& g, int64_t b0,
+                                              Sums base, int32_t* cu_t, int32_t* cu_p) {
+  __shared__ Sums tot[kWaves];
+  const int64_t first = b0 + (int64_t)threadIdx.x * kPer;
+  Sums own[kPer], mine{0, 0};
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    own[i] = Sums{0, 0};
+    if (first + i < a.B) {
+      const Need n = need_of(a, g, first + i);
+      own[i] = Sums{n.fresh, n.need - n.held};
+    }
+    mine.t += own[i].t, mine.p += own[i].p;
+  }
+  const Sums incl = wave_scan(mine);
+  const int w = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 63) tot[w] = incl;
+  __syncthreads();
+  Sums at{base.t + incl.t - mine.t, base.p + incl.p - mine.p}, end = base;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    if (i < w) at.t += tot[i].t, at.p += tot[i].p;
+    end.t += tot[i].t, end.p += tot[i].p;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (first + i < a.B) cu_t[threadIdx.x * kPer + i] = to_i32(at.t), cu_p[threadIdx.x * kPer + i] = to_i32(at.p);
+    at.t += own[i].t, at.p += own[i].p;
+  }
+  __syncthreads();
+  return end;
+}
+
+// Page of entry j of a request: kept, from the free list at `taken`, or -1.
 __device__ __forceinline__ int32_t entry_of(const TablesArgs& a, int64_t b, const Need& n,
-                                            int64_t j) {
+                                            int32_t taken, int32_t j) {
   if (j < n.held) return j < a.width_in ? a.table_in[b * a.width_in + j] : -1;
   if (j >= n.need) return -1;
-  const int64_t f = (int64_t)a.cu_pages[b] + (j - n.held);
+  const int64_t f = (int64_t)taken + (j - n.held);
   return f < a.n_free ? a.free_pages[f] : -1;
 }
 
-__global__ __launch_bounds__(kThreads) void tables_fill_kernel(TablesArgs a) {
-  const int64_t entries = a.B * a.width, all = entries + a.tokens;
-  const int64_t step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += step) {
-    if (i < entries) {
-      const int64_t b = i / a.width, j = i - b * a.width;
-      a.table[i] = entry_of(a, b, need_of(a, b), j);
+__global__ __launch_bounds__(kThreads) void tables_scan_kernel(TablesArgs a, Geometry g) {
+  Sums base{0, 0};
+  for (int64_t b0 = 0; b0 < a.B; b0 += kOwnScan)
+    base = scan_requests(a, g, b0, base, a.cu_tokens + b0, a.cu_pages + b0);
+  if (threadIdx.x == 0) a.cu_tokens[a.B] = to_i32(base.t), a.cu_pages[a.B] = to_i32(base.p);
+}
+
+// A wave takes kRun entries of one row, or kRun tokens, at a time.
+template <bool OWN>
+__global__ __launch_bounds__(kThreads) void tables_fill_kernel(TablesArgs a, Geometry g) {
+  __shared__ int32_t lds_t[OWN ? kOwnScan : 1], lds_p[OWN ? kOwnScan : 1];
+  const int32_t *cu_t = a.cu_tokens, *cu_p = a.cu_pages;
+  int32_t total;
+  if (OWN) {
+    const Sums end = scan_requests(a, g, 0, Sums{0, 0}, lds_t, lds_p);
+    cu_t = lds_t, cu_p = lds_p;
+    total = to_i32(end.t);
+    if (blockIdx.x == 0) {
+      for (int b = threadIdx.x; b < a.B; b += kThreads) a.cu_tokens[b] = lds_t[b], a.cu_pages[b] = lds_p[b];
+      if (threadIdx.x == 0) a.cu_tokens[a.B] = total, a.cu_pages[a.B] = to_i32(end.p);
+    }
+  } else {
+    total = a.cu_tokens[a.B];
+  }
+  const int lane = threadIdx.x & 63;
+  const int64_t wave = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int64_t it = wave; it < g.items; it += (int64_t)gridDim.x * kWaves) {
+    if (it >= g.token_items) {
+      const int64_t r = it - g.token_items, b = r / g.row_items, c = r - b * g.row_items;
+      const Need n = need_of(a, g, b);
+      const int32_t taken = cu_p[b];
+      if (c == 0 && lane == 0) a.lens[b] = to_i32((int64_t)n.old + n.fresh);
+#pragma unroll
+      for (int k = 0; k < kRun / 64; ++k) {
+        const int64_t j = c * kRun + k * 64 + lane;
+        if (j < a.width) a.table[b * a.width + j] = entry_of(a, b, n, taken, (int32_t)j);
+      }
       continue;
     }
-    const int64_t t = i - entries;
-    int32_t slot = -1;
-    int64_t pos = 0;
-    if (a.B > 0 && t < a.cu_tokens[a.B]) {
-      int64_t lo = 0, hi = a.B;             // the request with cu[lo] <= t < cu[lo + 1]
-      while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (a.cu_tokens[mid] <= t) lo = mid; else hi = mid;
+#pragma unroll
+    for (int k = 0; k < kRun / 64; ++k) {
+      const int64_t t = it * kRun + k * 64 + lane;
+      if (t >= a.tokens) continue;
+      int32_t slot = -1, pos = 0;
+      if (t < total) {
+        int64_t lo = 0, hi = a.B;             // the last request with sum before it <= t
+        while (hi - lo > 1) {
+          const int64_t mid = (lo + hi) >> 1;
+          if (cu_t[mid] <= t) lo = mid; else hi = mid;
+        }
+        const Need n = need_of(a, g, lo);
+        pos = to_i32((int64_t)n.old + (t - cu_t[lo]));
+        const int32_t j = (int32_t)div_by(pos, g.page);
+        if (j < n.need) {
+          const int32_t pg = entry_of(a, lo, n, cu_p[lo], j);
+          if (pg >= 0) slot = to_i32((int64_t)pg * a.page + (pos - j * (int32_t)a.page));
+        }
       }
-      const Need n = need_of(a, lo);
-      pos = n.old + (t - a.cu_tokens[lo]);
-      const int64_t j = pos / a.page;
-      if (j < n.need) {
-        const int32_t pg = entry_of(a, lo, n, j);
-        if (pg >= 0) slot = to_i32((int64_t)pg * a.page + pos % a.page);
-      }
+      a.slots[t] = slot;
+      a.positions[t] = pos;
     }
-    a.slots[t] = slot;
-    a.positions[t] = to_i32(pos);
   }
 }
 
 }  // namespace
 
 hipError_t launch_page_tables(const TablesArgs& a, hipStream_t s) {
-  tables_scan_kernel<<<1, kThreads, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
+  Geometry g;
+  g.page = fast_div((uint32_t)a.page);
+  const int64_t cap = a.page * a.width;
+  g.cap = (int32_t)(cap < 0x7FFFFFFF ? cap : 0x7FFFFFFF);
+  g.token_items = (int32_t)((a.tokens + kRun - 1) / kRun);
+  g.row_items = (a.width + kRun - 1) / kRun;
+  g.items = g.token_items + a.B * g.row_items;
+  const int64_t need = (g.items + kWaves - 1) / kWaves, most = (int64_t)device_cus() * 8;
+  const unsigned blocks = (unsigned)(need < 1 ? 1 : (need < most ? need : most));
+  if (a.B <= kOwnScan) {
+    tables_fill_kernel<true><<<blocks, kThreads, 0, s>>>(a, g);
+    return hipGetLastError();
+  }
+  tables_scan_kernel<<<1, kThreads, 0, s>>>(a, g);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t all = a.B * a.width + a.tokens;
-  if (all == 0) return hipSuccess;
-  const int64_t blocks = (all + kThreads - 1) / kThreads;
-  tables_fill_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), kThreads, 0, s>>>(a);
+  tables_fill_kernel<false><<<blocks, kThreads, 0, s>>>(a, g);
   return hipGetLastError();
 }
 
