@@ -14,7 +14,6 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kOwnScan = 2048;
-constexpr int kPer = kOwnScan / kThreads;     // requests a thread sums, each round
 constexpr int kRun = 256;                     // entries or tokens a wave takes at a time
 
 struct Geometry {
@@ -45,51 +44,68 @@ __device__ __forceinline__ Need need_of(const TablesArgs& a, const Geometry& g, 
   return n;
 }
 
-// Running sums of kOwnScan requests from b0 on, on top of *base (tokens, pages):
-// cu_t[i], cu_p[i] = sums before request b0 + i, capped; *base moves on.
+// Running sums of up to kOwnScan requests from b0 on, on top of `base`:
+// cu_t[i], cu_p[i] = sums before request b0 + i. 32-bit sums that stay at 2^32 - 1 once they
+// get there (such an addition is associative) and are stored as at most 2^31 - 1.
 struct Sums {
-  int64_t t, p;
+  uint32_t t, p;
 };
+__device__ __forceinline__ Sums operator+(Sums a, Sums b) {
+  return Sums{__builtin_elementwise_add_sat(a.t, b.t), __builtin_elementwise_add_sat(a.p, b.p)};
+}
+__device__ __forceinline__ int32_t stored(uint32_t v) { return (int32_t)min(v, 0x7FFFFFFFu); }
+
 __device__ __forceinline__ Sums wave_scan(Sums v) {       // inclusive
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const int64_t t = __shfl_up(v.t, off, 64), p = __shfl_up(v.p, off, 64);
-    if (lane >= off) v.t += t, v.p += p;
+    const Sums u{__shfl_up(v.t, off, 64), __shfl_up(v.p, off, 64)};
+    if (lane >= off) v = v + u;
   }
   return v;
 }
 __device__ __forceinline__ Sums scan_requests(const TablesArgs& a, const Geometry& g, int64_t b0,
                                               Sums base, int32_t* cu_t, int32_t* cu_p) {
   __shared__ Sums tot[kWaves];
-  const int64_t first = b0 + (int64_t)threadIdx.x * kPer;
-  Sums own[kPer], mine{0, 0};
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    own[i] = Sums{0, 0};
-    if (first + i < a.B) {
-      const Need n = need_of(a, g, first + i);
-      own[i] = Sums{n.fresh, n.need - n.held};
-    }
-    mine.t += own[i].t, mine.p += own[i].p;
+  // thread i sums requests b0 + i n .. b0 + (i + 1) n - 1
+  const int count = (int)min((int64_t)kOwnScan, a.B - b0);
+  const int n = (count + kThreads - 1) / kThreads, first = threadIdx.x * n;
+  const int past = min(first + n, count);
+  Sums mine{0, 0};
+  for (int i = first; i < past; ++i) {
+    const Need r = need_of(a, g, b0 + i);
+    cu_t[i] = r.fresh, cu_p[i] = r.need - r.held;
+    mine = mine + Sums{(uint32_t)r.fresh, (uint32_t)(r.need - r.held)};
   }
   const Sums incl = wave_scan(mine);
-  const int w = threadIdx.x >> 6;
-  if ((threadIdx.x & 63) == 63) tot[w] = incl;
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (lane == 63) tot[w] = incl;
+  Sums before{__shfl_up(incl.t, 1, 64), __shfl_up(incl.p, 1, 64)};
+  if (lane == 0) before = Sums{0, 0};
   __syncthreads();
-  Sums at{base.t + incl.t - mine.t, base.p + incl.p - mine.p}, end = base;
+  Sums at = base, end = base;
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) {
-    if (i < w) at.t += tot[i].t, at.p += tot[i].p;
-    end.t += tot[i].t, end.p += tot[i].p;
+    if (i < w) at = at + tot[i];
+    end = end + tot[i];
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (first + i < a.B) cu_t[threadIdx.x * kPer + i] = to_i32(at.t), cu_p[threadIdx.x * kPer + i] = to_i32(at.p);
-    at.t += own[i].t, at.p += own[i].p;
+  at = at + before;
+  for (int i = first; i < past; ++i) {
+    const Sums own{(uint32_t)cu_t[i], (uint32_t)cu_p[i]};
+    cu_t[i] = stored(at.t), cu_p[i] = stored(at.p);
+    at = at + own;
   }
   __syncthreads();
   return end;
+}
+
+// The last request in [lo, hi) whose sum before it is <= t; cu[lo] <= t.
+__device__ __forceinline__ int64_t request_of(const int32_t* cu, int64_t lo, int64_t hi, int64_t t) {
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
 }
 
 // Page of entry j of a request: kept, from the free list at `taken`, or -1.
@@ -105,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void tables_scan_kernel(TablesArgs a, Geo
   Sums base{0, 0};
   for (int64_t b0 = 0; b0 < a.B; b0 += kOwnScan)
     base = scan_requests(a, g, b0, base, a.cu_tokens + b0, a.cu_pages + b0);
-  if (threadIdx.x == 0) a.cu_tokens[a.B] = to_i32(base.t), a.cu_pages[a.B] = to_i32(base.p);
+  if (threadIdx.x == 0) a.cu_tokens[a.B] = stored(base.t), a.cu_pages[a.B] = stored(base.p);
 }
 
 // A wave takes kRun entries of one row, or kRun tokens, at a time.
@@ -117,10 +133,10 @@ __global__ __launch_bounds__(kThreads) void tables_fill_kernel(TablesArgs a, Geo
   if (OWN) {
     const Sums end = scan_requests(a, g, 0, Sums{0, 0}, lds_t, lds_p);
     cu_t = lds_t, cu_p = lds_p;
-    total = to_i32(end.t);
+    total = stored(end.t);
     if (blockIdx.x == 0) {
       for (int b = threadIdx.x; b < a.B; b += kThreads) a.cu_tokens[b] = lds_t[b], a.cu_pages[b] = lds_p[b];
-      if (threadIdx.x == 0) a.cu_tokens[a.B] = total, a.cu_pages[a.B] = to_i32(end.p);
+      if (threadIdx.x == 0) a.cu_tokens[a.B] = total, a.cu_pages[a.B] = stored(end.p);
     }
   } else {
     total = a.cu_tokens[a.B];
@@ -140,17 +156,20 @@ __global__ __launch_bounds__(kThreads) void tables_fill_kernel(TablesArgs a, Geo
       }
       continue;
     }
+    // the run's first and last request once, each token's between them
+    const int64_t t0 = it * kRun, t1 = min(t0 + kRun, (int64_t)total);
+    int64_t b0 = 0, b1 = 1;
+    if (t0 < t1) {
+      b0 = request_of(cu_t, 0, a.B, t0);
+      b1 = request_of(cu_t, b0, a.B, t1 - 1) + 1;
+    }
 #pragma unroll
     for (int k = 0; k < kRun / 64; ++k) {
-      const int64_t t = it * kRun + k * 64 + lane;
+      const int64_t t = t0 + k * 64 + lane;
       if (t >= a.tokens) continue;
       int32_t slot = -1, pos = 0;
       if (t < total) {
-        int64_t lo = 0, hi = a.B;             // the last request with sum before it <= t
-        while (hi - lo > 1) {
-          const int64_t mid = (lo + hi) >> 1;
-          if (cu_t[mid] <= t) lo = mid; else hi = mid;
-        }
+        const int64_t lo = request_of(cu_t, b0, b1, t);
         const Need n = need_of(a, g, lo);
         pos = to_i32((int64_t)n.old + (t - cu_t[lo]));
         const int32_t j = (int32_t)div_by(pos, g.page);
@@ -175,7 +194,7 @@ hipError_t launch_page_tables(const TablesArgs& a, hipStream_t s) {
   g.token_items = (int32_t)((a.tokens + kRun - 1) / kRun);
   g.row_items = (a.width + kRun - 1) / kRun;
   g.items = g.token_items + a.B * g.row_items;
-  const int64_t need = (g.items + kWaves - 1) / kWaves, most = (int64_t)device_cus() * 8;
+  const int64_t need = (g.items + kWaves - 1) / kWaves, most = (int64_t)device_cus() * 4;
   const unsigned blocks = (unsigned)(need < 1 ? 1 : (need < most ? need : most));
   if (a.B <= kOwnScan) {
     tables_fill_kernel<true><<<blocks, kThreads, 0, s>>>(a, g);
