@@ -12,10 +12,22 @@ namespace {
 
 constexpr int kWaves = 4;
 
-__device__ __forceinline__ float capped(float s, float cap) {
-  if (!(cap > 0.f)) return s;
-  // tanh(x) = 1 - 2 / (e^(2x) + 1): saturates to +-1 without overflowing to NaN
-  return cap * (1.f - 2.f / (__expf(2.f * (s / cap)) + 1.f));
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// cap * tanh(s / cap) to a few units in the last place of its own size (scores of a few
+// units under a cap of tens must not carry the cap's rounding): below 1 the
+// quotient of Lambert's continued fraction cut after six terms (4e-10 off at 1), above
+// it (e^2x - 1) / (e^2x + 1), where the difference loses nothing.
+__device__ __forceinline__ float capped(float s, float cap, float inv_cap) {
+  const float x = fminf(fmaxf(s * inv_cap, -20.f), 20.f), y = x * x;
+  const float e = fast_exp2(x * (2.f * kLog2e));
+  const bool small = y < 1.f;
+  const float num = small ? x * fmaf(fmaf(21.f, y, 1260.f), y, 10395.f) : e - 1.f;
+  const float den = small ? fmaf(fmaf(y + 210.f, y, 4725.f), y, 10395.f) : e + 1.f;
+  const float r = cap * (num * __builtin_amdgcn_rcpf(den));
+  return s == s ? r : s;     // the clamp drops a NaN
 }
 
 // Any size, stride and alignment. One block per (request, query head); a wave
@@ -55,7 +67,9 @@ __global__ __launch_bounds__(kWaves * 64) void attn_any_kernel(AttnArgs a) {
       const int e = lane + 64 * i;
       if (e < D) s = fmaf(qf[i], Val<DT>::get(k + e), s);
     }
-    s = capped(wave_sum(s) * a.scale, a.softcap) + bias;
+    s = wave_sum(s) * a.scale;
+    if (a.softcap > 0.f) s = capped(s, a.softcap, 1.f / a.softcap);
+    s += bias;
     const float mn = fmaxf(m, s);
     const float alpha = m == -INFINITY ? 0.f : __expf(m - mn);
     const float p = s == -INFINITY ? 0.f : __expf(s - mn);   // a NaN score stays one
@@ -120,14 +134,14 @@ hipError_t run_any(const AttnArgs& a, hipStream_t s) {
 // VE m .. VE m + VE - 1 (16 lanes cover a row), picking tile t's element of
 // each row with byte permutes. Nothing goes through LDS but row addresses.
 constexpr int kHeadTile = 16;
-constexpr int kMaxBlocks = 1024;   // blocks of a call over all parts, unless its heads alone are more
+constexpr int kMaxCus = 256;
 
 template <int DT, int DP> struct Shape {
   static constexpr int tiles = DT == FK_F32 ? 1 : 2;        // 16-key tiles per step
   static constexpr int keys = 16 * tiles;                   // keys per wave and step
   static constexpr int unit = DT == FK_F32 ? 4 : 8;         // elements in 16 bytes
   static constexpr int nc = DP / (4 * unit);                // 16-byte key loads per row and lane
-  static constexpr int ve = DP == 64 || DT == FK_F32 ? 4 : 8;   // elements per value load
+  static constexpr int ve = DP / 16 < unit ? DP / 16 : unit;    // elements per value load
   static constexpr int nu = DP / (16 * ve);                 // value loads per row and lane
   static constexpr int rows = 4 * tiles;                    // value rows per lane
   static constexpr int ldo = DP + 4;                        // LDS row of merged results
@@ -139,6 +153,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef const __attribute__((address_space(1))) u32x4* gptr16;
 typedef const __attribute__((address_space(1))) u32x2* gptr8;
+typedef const __attribute__((address_space(1))) uint32_t* gptr4;
 typedef const __attribute__((address_space(1))) int32_t* gptr_i32;
 typedef const __attribute__((address_space(1))) float* gptr_f32;
 
@@ -146,36 +161,38 @@ __device__ __forceinline__ uint4 load16(uint64_t addr) {
   return __builtin_bit_cast(uint4, *(gptr16)addr);
 }
 
-// Keys and values are read once: marked so, they do not push out of L2 what others
-// will read again (long_b32 815 -> 779 us, one_131072 112 -> 106 us).
-__device__ __forceinline__ uint4 stream16(uint64_t addr) {
-  return __builtin_bit_cast(uint4, __builtin_nontemporal_load((gptr16)addr));
-}
-__device__ __forceinline__ uint4 stream8(uint64_t addr) {
-  const u32x2 h = __builtin_nontemporal_load((gptr8)addr);
-  return make_uint4(h.x, h.y, 0, 0);
+// A load of n = 16, 8 or 4 bytes into the first words. STREAM: bytes that no one else
+// reads are marked so and do not push out of L2 what others will read again.
+template <int n, bool STREAM> __device__ __forceinline__ uint4 load_row(uint64_t addr) {
+  if constexpr (n == 16) {
+    return __builtin_bit_cast(uint4, STREAM ? __builtin_nontemporal_load((gptr16)addr) : *(gptr16)addr);
+  } else if constexpr (n == 8) {
+    const u32x2 h = STREAM ? __builtin_nontemporal_load((gptr8)addr) : *(gptr8)addr;
+    return make_uint4(h.x, h.y, 0, 0);
+  } else {
+    return make_uint4(STREAM ? __builtin_nontemporal_load((gptr4)addr) : *(gptr4)addr, 0, 0, 0);
+  }
 }
 
 // Keys that do not count are read from here: zeros, whatever the cache holds.
 __device__ const uint4 zero_row[64] = {};
 
 // How the work is shared. Request b costs its steps of `keys` keys plus
-// kSegCost (a request's own share: queries, joining the waves, storing). The
+// one step of each of its waves (queries, first loads, joining, storing). The
 // requests' costs are laid end to end and cut into equal parts, one per block of
 // a cache head, so that a batch of any lengths fills the chip evenly. A request
 // inside one part is finished there; one that is cut leaves a partial
 // result per part, at most two a block (one that started before, one that goes
 // on), joined by attn_join_kernel.
-constexpr int kSegCost = 8;
-constexpr int kMinCost = 8;       // least cost worth a block of its own
 
 struct Plan {
-  int parts;            // blocks per (cache head, head tile); 0: one per request
+  int parts;            // blocks per (cache head, head tile); 0: a team per request
+  int team;             // waves that share a request's steps: 4, 2 or 1
   int heads, tiles;     // cache heads, head tiles per cache head
-  int G;                // query heads per cache head
+  int G, hr;            // query heads per cache head; of them per tile, at most
   FastDiv page;
-  float* o;             // (parts, heads, tiles, 2, 16, D) partial sums
-  float* ml;            // (parts, heads, tiles, 2, 16, 2) their maximum and sum
+  float* o;             // (parts, heads, tiles, 2, hr, D) partial sums
+  float* ml;            // (parts, heads, tiles, 2, hr, 2) their maximum and sum
   int32_t* cover;       // (B, 2) first and last part of a request
 };
 
@@ -215,10 +232,6 @@ template <> struct Mfma16<FK_F32> {
 // fp16 probabilities are scaled by 2^14, so that one 2^-38 of the largest is
 // still a subnormal fp16 and a long tail of small ones is not lost.
 template <int DT> constexpr float kProbShift = DT == FK_F16 ? 14.f : 0.f;
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-
-__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
@@ -238,14 +251,15 @@ template <int DT, int DP> struct Rows {
   float bias[n];
 };
 
-template <int DT, int DP, bool EXTRA>
+template <int DT, int DP, bool EXTRA, bool EXACT>
 __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t b, int hk, int ht,
-                                       int len, int step, int end, Rows<DT, DP>* rows,
+                                       int len, int step, int stride, int end,
+                                       Rows<DT, DP>* rows,
                                        Acc<DT, DP>& acc) {
   using S = Shape<DT, DP>;
   const fk_kv_cache_t& c = a.cache;
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-  const int D = (int)c.dim;
+  const int D = EXACT ? DP : (int)c.dim;
   constexpr int eb = Val<DT>::bytes;
   acc.m = -INFINITY;
   acc.l = 0.f;
@@ -280,6 +294,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
   const uint64_t kbase = (uint64_t)c.k + (uint64_t)hk * c.k_stride[2] * eb;
   const uint64_t vbase = (uint64_t)c.v + (uint64_t)hk * c.v_stride[2] * eb;
   const uint64_t zero = (uint64_t)zero_row;
+  const bool cap = EXTRA && a.softcap > 0.f;
+  const float inv_cap = cap ? 1.f / a.softcap : 0.f;
   const bool has_bias = EXTRA && c.key_bias && c.pages > 0;
   const uint64_t bbase = (uint64_t)c.key_bias + (uint64_t)hk * c.bias_stride[2] * 4;
   // (loads without branches: a key past the end reads the last one's entry)
@@ -318,37 +334,31 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
     for (int s = 0; s < S::tiles; ++s) {
       const uint64_t ad = r.k[16 * s + m];
 #pragma unroll
-      for (int i = 0; i < S::nc; ++i) kf[s][i] = stream16(ad + koff[i]);
+      for (int i = 0; i < S::nc; ++i) kf[s][i] = load_row<16, EXACT>(ad + koff[i]);
     }
   };
-  uint4 vf[S::rows][S::nu];            // ve == 4 and 16-bit: only .x and .y
+  uint4 vf[S::rows][S::nu];            // a load of fewer bytes fills the first words
   auto load_v = [&](const Rows<DT, DP>& r) {
 #pragma unroll
     for (int j = 0; j < S::rows; ++j) {
       const uint64_t ad = r.v[16 * (j >> 2) + 4 * g + (j & 3)];
 #pragma unroll
-      for (int i = 0; i < S::nu; ++i) {
-        if constexpr (S::ve * eb == 16) {
-          vf[j][i] = stream16(ad + voff[i]);
-        } else {
-          vf[j][i] = stream8(ad + voff[i]);
-        }
-      }
+      for (int i = 0; i < S::nu; ++i) vf[j][i] = load_row<S::ve * eb, EXACT>(ad + voff[i]);
     }
   };
 
-  int32_t pg1 = entry(step), pg2 = entry(step + kWaves);
+  int32_t pg1 = entry(step), pg2 = entry(step + stride);
   put_rows(rows[0], step, pg1, bias_of(step, pg1));
-  float bias1 = bias_of(step + kWaves, pg2);
+  float bias1 = bias_of(step + stride, pg2);
   pg1 = pg2;
-  pg2 = entry(step + 2 * kWaves);
+  pg2 = entry(step + 2 * stride);
   load_k(rows[0]);
   load_v(rows[0]);
   int par = 0;
-  for (; step < end; step += kWaves, par ^= 1) {
+  for (; step < end; step += stride, par ^= 1) {
     Rows<DT, DP>& now = rows[par];
     Rows<DT, DP>& next = rows[par ^ 1];
-    put_rows(next, step + kWaves, pg1, bias1);
+    put_rows(next, step + stride, pg1, bias1);
     float s[S::tiles][4];
 #pragma unroll
     for (int u = 0; u < S::tiles; ++u) {
@@ -360,9 +370,9 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
     }
     load_k(next);
     __builtin_amdgcn_sched_barrier(0);   // the next keys are on their way before the softmax
-    bias1 = bias_of(step + 2 * kWaves, pg2);
+    bias1 = bias_of(step + 2 * stride, pg2);
     pg1 = pg2;
-    pg2 = entry(step + 3 * kWaves);
+    pg2 = entry(step + 3 * stride);
 
     float top = acc.m;
 #pragma unroll
@@ -370,8 +380,9 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // -inf where a key does not count: its score is 0 (a zero row)
-        const float x = s[u][i] * a.scale;
-        s[u][i] = (EXTRA ? capped(x, a.softcap) : x) + now.bias[16 * u + 4 * g + i];
+        float x = s[u][i] * a.scale;
+        if (cap) x = capped(x, a.softcap, inv_cap);
+        s[u][i] = x + now.bias[16 * u + 4 * g + i];
         top = fmaxf(top, s[u][i]);
       }
     top = fmaxf(top, __shfl_xor(top, 16, 64));
@@ -395,40 +406,47 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
 
     if constexpr (DT == FK_F32) {
 #pragma unroll
-      for (int u = 0; u < S::nu; ++u)
+      for (int y = 0; y < S::tiles; ++y)
 #pragma unroll
-        for (int t = 0; t < S::ve; ++t)
+        for (int u = 0; u < S::nu; ++u)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc.o[u * S::ve + t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                __builtin_bit_cast(float, word(vf[j][u], t)), s[0][j], acc.o[u * S::ve + t], 0, 0, 0);
+          for (int t = 0; t < S::ve; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc.o[u * S::ve + t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                  __builtin_bit_cast(float, word(vf[4 * y + j][u], t)), s[y][j],
+                  acc.o[u * S::ve + t], 0, 0, 0);
     } else {
       // Probabilities as the sum of two 16-bit numbers: one alone would round
       // each to 8 (bf16) or 11 bits, an error as large as the result's own
       // rounding. The second product rides on matrix units that are idle anyway.
       typedef typename Val<DT>::arith T;
       typedef T T8 __attribute__((ext_vector_type(8)));
-      T8 hi, lo;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = s[j >> 2][j & 3];
-        hi[j] = (T)x;
-        lo[j] = (T)(x - (float)hi[j]);
-      }
-      const uint4 ph = __builtin_bit_cast(uint4, hi), pl = __builtin_bit_cast(uint4, lo);
+      for (int y = 0; y < S::tiles / 2; ++y) {
+        T8 hi, lo;
 #pragma unroll
-      for (int u = 0; u < S::nu; ++u)
-#pragma unroll
-        for (int t = 0; t < S::ve; ++t) {
-          const uint32_t sel = t & 1 ? 0x07060302u : 0x05040100u;
-          uint4 vt;
-          vt.x = __builtin_amdgcn_perm(word(vf[1][u], t >> 1), word(vf[0][u], t >> 1), sel);
-          vt.y = __builtin_amdgcn_perm(word(vf[3][u], t >> 1), word(vf[2][u], t >> 1), sel);
-          vt.z = __builtin_amdgcn_perm(word(vf[5][u], t >> 1), word(vf[4][u], t >> 1), sel);
-          vt.w = __builtin_amdgcn_perm(word(vf[7][u], t >> 1), word(vf[6][u], t >> 1), sel);
-          acc.o[u * S::ve + t] = Mfma16<DT>::run(vt, ph, acc.o[u * S::ve + t]);
-          acc.o[u * S::ve + t] = Mfma16<DT>::run(vt, pl, acc.o[u * S::ve + t]);
+        for (int j = 0; j < 8; ++j) {
+          const float x = s[2 * y + (j >> 2)][j & 3];
+          hi[j] = (T)x;
+          lo[j] = (T)(x - (float)hi[j]);
         }
+        const uint4 ph = __builtin_bit_cast(uint4, hi), pl = __builtin_bit_cast(uint4, lo);
+        auto pick = [&](int j, int u, int t) {       // element t of rows j (low half) and j + 1
+          return __builtin_amdgcn_perm(word(vf[8 * y + j + 1][u], t >> 1),
+                                       word(vf[8 * y + j][u], t >> 1),
+                                       t & 1 ? 0x07060302u : 0x05040100u);
+        };
+#pragma unroll
+        for (int u = 0; u < S::nu; ++u)
+#pragma unroll
+          for (int t = 0; t < S::ve; ++t) {
+            const uint4 vt = make_uint4(pick(0, u, t), pick(2, u, t), pick(4, u, t), pick(6, u, t));
+            floatx4_t& o = acc.o[u * S::ve + t];
+            o = Mfma16<DT>::run(vt, ph, o);
+            o = Mfma16<DT>::run(vt, pl, o);
+          }
+      }
     }
     load_v(next);
     __builtin_amdgcn_sched_barrier(0);
@@ -446,8 +464,8 @@ struct Start {
 };
 
 template <int KEYS>
-__device__ __forceinline__ int64_t cost_of(const AttnArgs& a, int64_t b) {
-  return kSegCost + (len_of(a, b) + KEYS - 1) / KEYS;
+__device__ __forceinline__ int64_t cost_of(const AttnArgs& a, const Plan& p, int64_t b) {
+  return p.team + (len_of(a, b) + KEYS - 1) / KEYS;
 }
 
 template <int KEYS>
@@ -457,7 +475,7 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, const Plan& p, in
   const int64_t n = (a.B + kWaves * 64 - 1) / (kWaves * 64);
   const int64_t b0 = threadIdx.x * n, b1 = b0 + n < a.B ? b0 + n : a.B;
   int64_t mine = 0;
-  for (int64_t b = b0; b < b1; ++b) mine += cost_of<KEYS>(a, b);
+  for (int64_t b = b0; b < b1; ++b) mine += cost_of<KEYS>(a, p, b);
   int64_t incl = mine;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
@@ -474,13 +492,13 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, const Plan& p, in
   }
   Start st;
   st.total = total;
-  const int64_t most = total / kMinCost;
+  const int64_t most = total / (2 * p.team);     // less is not worth a part of its own
   st.parts = (int)(most < 1 ? 1 : (most < p.parts ? most : p.parts));
   st.lo = w < st.parts ? total * w / st.parts : total;
   st.hi = w < st.parts ? total * (w + 1) / st.parts : total;
   if (st.lo >= before && st.lo < before + mine) {
     int64_t b = b0, at = before;
-    for (int64_t c = cost_of<KEYS>(a, b); at + c <= st.lo; c = cost_of<KEYS>(a, b)) at += c, ++b;
+    for (int64_t c = cost_of<KEYS>(a, p, b); at + c <= st.lo; c = cost_of<KEYS>(a, p, b)) at += c, ++b;
     found[0] = b;
     found[1] = at;
   }
@@ -509,19 +527,21 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const float* x) {
 
 // Waves a SIMD holds (registers) and with them blocks a CU: the parts of a call are as
 // many as the chip holds at once.
-template <int DP> constexpr int kWavesPerSimd = DP == 64 ? 3 : (DP == 128 ? 2 : 1);
-template <int DP> constexpr int kBlocksPerCu = kWavesPerSimd<DP> * 4 / kWaves;
+template <int DP> constexpr int kWavesPerSimd = DP <= 64 ? 3 : (DP == 128 ? 2 : 1);
+constexpr int kMaxParts = kMaxCus * 3;
 
-template <int DT, int DP, bool EXTRA>
+template <int DT, int DP, bool EXTRA, bool EXACT>
 __global__ __launch_bounds__(kWaves * 64, kWavesPerSimd<DP>) void attn_mfma_kernel(AttnArgs a, Plan p) {
   using S = Shape<DT, DP>;
   __shared__ Rows<DT, DP> rows[kWaves][2];
   __shared__ float so[kWaves][kHeadTile][S::ldo];
   __shared__ float sm[kWaves][kHeadTile], sl[kWaves][kHeadTile];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
-  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
-  const int ht = (int)(id % p.tiles), hk = (int)((id / p.tiles) % p.heads);
-  const int64_t part = id / ((int64_t)p.tiles * p.heads);
+  // Waves k0 .. k1 - 1 of this block are one team; its teams take neighbouring heads.
+  const int k0 = w / p.team * p.team, k1 = k0 + p.team, teams = kWaves / p.team;
+  const int64_t unit = xcd_remap(blockIdx.x, gridDim.x) * teams + w / p.team;
+  const int ht = (int)(unit % p.tiles), hk = (int)((unit / p.tiles) % p.heads);
+  const int64_t part = unit / ((int64_t)p.tiles * p.heads);
   const int nh = min(kHeadTile, p.G - ht * kHeadTile);
   const int D = (int)a.cache.dim;
 
@@ -532,19 +552,20 @@ __global__ __launch_bounds__(kWaves * 64, kWavesPerSimd<DP>) void attn_mfma_kern
   } else {
     st.lo = 0, st.hi = 1, st.b = part, st.before = 0;
   }
+  const bool idle = p.parts == 0 && part >= a.B;     // a wave past the last request
   for (int64_t b = st.b, at = st.before; at < st.hi;) {
-    const int len = len_of(a, b);
+    const int len = idle ? 0 : len_of(a, b);
     const int steps = (len + S::keys - 1) / S::keys;
     int t0 = 0, t1 = steps;
     if (p.parts > 0) {
-      const int64_t first = at + kSegCost;
+      const int64_t first = at + p.team;
       t0 = (int)max((int64_t)0, min(st.lo - first, (int64_t)steps));
       t1 = (int)max((int64_t)0, min(st.hi - first, (int64_t)steps));
     }
     const bool starts = at >= st.lo;           // the request begins in this part
     if (t0 < t1 || (steps == 0 && starts)) {
       Acc<DT, DP> acc;
-      attend<DT, DP, EXTRA>(a, p, b, hk, ht, len, t0 + w, t1, rows[w], acc);
+      attend<DT, DP, EXTRA, EXACT>(a, p, b, hk, ht, len, t0 + w - k0, p.team, t1, rows[w], acc);
       __syncthreads();                         // the last request's results are out
       if (m < nh) {
         if (g == 0) sm[w][m] = acc.m, sl[w][m] = acc.l;
@@ -559,15 +580,13 @@ __global__ __launch_bounds__(kWaves * 64, kWavesPerSimd<DP>) void attn_mfma_kern
       __syncthreads();
       const bool whole = t0 == 0 && t1 == steps;
       const int slot = t0 == 0 ? 1 : 0;
-      const int64_t ps = (((part * p.heads + hk) * p.tiles + ht) * 2 + slot) * kHeadTile;
-      for (int i = threadIdx.x; i < nh * (DP / 4); i += kWaves * 64) {
+      const int64_t ps = (((part * p.heads + hk) * p.tiles + ht) * 2 + slot) * p.hr;
+      for (int i = threadIdx.x - k0 * 64; i < nh * (DP / 4) && !idle; i += p.team * 64) {
         const int h = i / (DP / 4), e = (i - h * (DP / 4)) * 4;
-        float top = sm[0][h];
-#pragma unroll
-        for (int k = 1; k < kWaves; ++k) top = fmaxf(top, sm[k][h]);
+        float top = -INFINITY;
+        for (int k = k0; k < k1; ++k) top = fmaxf(top, sm[k][h]);
         float x[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-#pragma unroll
-        for (int k = 0; k < kWaves; ++k) {
+        for (int k = k0; k < k1; ++k) {
           const float f = join_factor(sm[k][h], sl[k][h], top);
           l = fmaf(f, sl[k][h], l);
 #pragma unroll
@@ -593,7 +612,7 @@ __global__ __launch_bounds__(kWaves * 64, kWavesPerSimd<DP>) void attn_mfma_kern
       }
     }
     if (p.parts == 0) break;
-    at += kSegCost + steps;
+    at += p.team + steps;
     ++b;
   }
 }
@@ -604,7 +623,7 @@ constexpr int kJoin = 256;        // threads of the joining block
 // slot 0 of the others. One block per (request, query head).
 template <int DT>
 __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Plan p) {
-  __shared__ float fac[kMaxBlocks], part_l[kMaxBlocks];
+  __shared__ float fac[kMaxParts], part_l[kMaxParts];
   __shared__ float red[kJoin][4];
   __shared__ float redl[kJoin];
   const int64_t b = blockIdx.x / a.Hq;
@@ -615,7 +634,7 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Plan p) {
   const int D = (int)a.cache.dim, n = last - first + 1;
   auto row = [&](int i) {
     const int64_t part = first + i;
-    return (((part * p.heads + hk) * p.tiles + ht) * 2 + (i == 0 ? 1 : 0)) * kHeadTile + hr;
+    return (((part * p.heads + hk) * p.tiles + ht) * 2 + (i == 0 ? 1 : 0)) * p.hr + hr;
   };
   // every thread: maximum over all parts; factors and the sum of the parts' sums
   float top = -INFINITY;
@@ -678,29 +697,60 @@ int64_t head_tiles(int64_t G) { return (G + kHeadTile - 1) / kHeadTile; }
 // Parts per (cache head, head tile): `blocks` shared out.
 int64_t parts_of(int64_t blocks, int64_t units) { return units >= blocks ? 1 : blocks / units; }
 
+// Blocks the chip holds at once for rows of D elements.
+int64_t blocks_of(int64_t D) {
+  const int64_t cus = device_cus() < kMaxCus ? device_cus() : kMaxCus;
+  return cus * (D <= 64 ? kWavesPerSimd<64> : (D <= 128 ? kWavesPerSimd<128> : kWavesPerSimd<256>)) * 4 / kWaves;
+}
+
+// Waves a head when requests are cut: the block's waves take as many neighbouring
+// heads as divide them evenly.
+int team_of(int64_t units) { return units % 4 == 0 ? 1 : (units % 2 == 0 ? 2 : 4); }
+
 template <int DT, int DP>
 hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   Plan p{};
   p.heads = (int)a.cache.heads;
   p.G = (int)(a.Hq / a.cache.heads);
   p.tiles = (int)head_tiles(p.G);
+  p.hr = p.G < kHeadTile ? p.G : kHeadTile;
   p.page = fast_div((uint32_t)a.cache.page);
   const int64_t units = (int64_t)p.heads * p.tiles;
   const int64_t most = a.max_len > 0 && a.max_len < a.width * a.cache.page ? a.max_len : a.width * a.cache.page;
   const bool cut = most > 512;
-  const int64_t resident = (int64_t)device_cus() * kBlocksPerCu<DP>;
-  p.parts = cut ? (int)parts_of(resident < kMaxBlocks ? resident : kMaxBlocks, units) : 0;
+  const int64_t resident = blocks_of(DP);
   if (cut) {
-    const int64_t slots = units * p.parts * 2 * kHeadTile;
+    // Where there are steps enough for every wave of the chip, a block's waves take
+    // neighbouring heads, whose rows lie side by side in the cache, instead of one
+    // head's steps in turn: the block reads 4 rows' length in one piece (long_b32: 774 us
+    // with 1 head a block, 697 with 2, 670 with 4). With fewer steps the waves share them
+    // and join in LDS, not through memory.
+    const int64_t steps = units * a.B * ((most + Shape<DT, DP>::keys - 1) / Shape<DT, DP>::keys);
+    p.team = steps >= 4 * kWaves * resident ? team_of(units) : kWaves;
+    const int64_t groups = units * p.team / kWaves;       // blocks that make one part
+    p.parts = (int)parts_of(resident, groups);
+    const int64_t slots = units * p.parts * 2 * p.hr;
     char* w = (char*)ws;
     p.o = (float*)w;
     p.ml = (float*)(w + slots * a.cache.dim * 4);
     p.cover = (int32_t*)(w + slots * a.cache.dim * 4 + slots * 8);
+  } else {
+    // One wave each where that alone fills the chip, or where a second wave would
+    // find nothing to do.
+    p.team = most <= Shape<DT, DP>::keys || units * a.B >= kWaves * resident ? 1 : kWaves;
   }
-  const int64_t blocks = units * (cut ? p.parts : a.B);
+  const int64_t blocks = (units * (cut ? p.parts : a.B) * p.team + kWaves - 1) / kWaves;
   if (blocks > 0x7FFFFFFF || a.B * a.Hq > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const auto kernel = a.softcap > 0.f || a.cache.key_bias ? attn_mfma_kernel<DT, DP, true>
-                                                          : attn_mfma_kernel<DT, DP, false>;
+  // EXACT: rows fill their lanes and whole 128-byte lines, and no other wave reads them.
+  const auto aligned = [](uintptr_t base, const int64_t* s) {
+    return !((base | (uintptr_t)((s[0] | s[1] | s[2]) * Val<DT>::bytes)) & 127);
+  };
+  const bool exact = a.cache.dim == DP && p.tiles == 1 && DP * Val<DT>::bytes % 128 == 0 &&
+                     aligned((uintptr_t)a.cache.k, a.cache.k_stride) &&
+                     aligned((uintptr_t)a.cache.v, a.cache.v_stride);
+  const bool extra = a.softcap > 0.f || a.cache.key_bias;
+  const auto kernel = exact ? (extra ? attn_mfma_kernel<DT, DP, true, true> : attn_mfma_kernel<DT, DP, false, true>)
+                            : (extra ? attn_mfma_kernel<DT, DP, true, false> : attn_mfma_kernel<DT, DP, false, false>);
   kernel<<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !cut) return e;
@@ -712,7 +762,8 @@ template <int DT>
 hipError_t run(const AttnArgs& a, void* ws, hipStream_t s) {
   const int64_t D = a.cache.dim;
   if (D > 256 || !aligned16(a, Val<DT>::bytes)) return run_any<DT>(a, s);
-  return D <= 64 ? run_mfma<DT, 64>(a, ws, s)
+  return D <= 32 ? run_mfma<DT, 32>(a, ws, s)
+         : D <= 64 ? run_mfma<DT, 64>(a, ws, s)
          : D <= 128 ? run_mfma<DT, 128>(a, ws, s)
                     : run_mfma<DT, 256>(a, ws, s);
 }
@@ -721,8 +772,11 @@ hipError_t run(const AttnArgs& a, void* ws, hipStream_t s) {
 
 size_t attn_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   if (D > 256) return 256;
-  const int64_t units = Hkv * head_tiles(Hq / Hkv);
-  const size_t slots = (size_t)units * parts_of(kMaxBlocks, units) * 2 * kHeadTile;
+  // sized for the largest chip: a pure function of the shape
+  const int64_t G = Hq / Hkv, units = Hkv * head_tiles(G);
+  const int64_t most = kMaxCus * (D <= 64 ? kWavesPerSimd<64> : (D <= 128 ? kWavesPerSimd<128> : kWavesPerSimd<256>));
+  const int64_t groups = units * team_of(units) / kWaves;
+  const size_t slots = (size_t)units * parts_of(most, groups) * 2 * (G < kHeadTile ? G : kHeadTile);
   return slots * D * 4 + slots * 8 + (size_t)B * 8;
 }
 

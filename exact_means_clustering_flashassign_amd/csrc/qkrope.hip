@@ -126,6 +126,28 @@ __global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopeP
   const bool va = j < p.hp + p.rem, vb = va && ub < p.units;
   const int ea = va ? ua * VE : 0, eb = vb ? ub * VE : 0;
 
+  struct Row {
+    V a, b;
+    int kind, h;             // 0 query, 1 key, 2 value, 3 none
+  };
+  auto load = [&](int pass) {
+    Row x;
+    const int r = pass * p.rp + sub;
+    x.kind = r < a.Hq ? 0 : (r < a.Hq + a.Hkv ? 1 : 2);
+    x.h = r - (x.kind == 0 ? 0 : (x.kind == 1 ? (int)a.Hq : (int)(a.Hq + a.Hkv)));
+    if (pass >= pass1 || r >= p.rows || !va) x.kind = 3;
+    x.a = V{}, x.b = V{};
+    if (x.kind == 3) return x;
+    const T* src = x.kind == 0   ? (const T*)a.q + t * a.q_stride[0] + x.h * a.q_stride[1]
+                   : x.kind == 1 ? (const T*)a.k + t * a.k_stride[0] + x.h * a.k_stride[1]
+                                 : (const T*)a.v + t * a.v_stride[0] + x.h * a.v_stride[1];
+    x.a = *(const V*)(src + ea);
+    if (vb) x.b = *(const V*)(src + eb);
+    return x;
+  };
+
+  Row next = load(pass0);      // on its way before anything is waited for
+
   const int half = (int)(a.rot >> 1);
   float cs[VE] = {}, sn[VE] = {};
   bool on[VE];               // pair i of this lane rotates
@@ -166,27 +188,6 @@ __global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopeP
     }
   }
 
-  struct Row {
-    V a, b;
-    int kind, h;             // 0 query, 1 key, 2 value, 3 none
-  };
-  auto load = [&](int pass) {
-    Row x;
-    const int r = pass * p.rp + sub;
-    x.kind = r < a.Hq ? 0 : (r < a.Hq + a.Hkv ? 1 : 2);
-    x.h = r - (x.kind == 0 ? 0 : (x.kind == 1 ? (int)a.Hq : (int)(a.Hq + a.Hkv)));
-    if (pass >= pass1 || r >= p.rows || !va) x.kind = 3;
-    x.a = V{}, x.b = V{};
-    if (x.kind == 3) return x;
-    const T* src = x.kind == 0   ? (const T*)a.q + t * a.q_stride[0] + x.h * a.q_stride[1]
-                   : x.kind == 1 ? (const T*)a.k + t * a.k_stride[0] + x.h * a.k_stride[1]
-                                 : (const T*)a.v + t * a.v_stride[0] + x.h * a.v_stride[1];
-    x.a = *(const V*)(src + ea);
-    if (vb) x.b = *(const V*)(src + eb);
-    return x;
-  };
-
-  Row next = load(pass0);
   for (int pass = pass0; pass < pass1; ++pass) {
     const Row x = next;
     next = load(pass + 1);
