@@ -85,7 +85,7 @@ __global__ __launch_bounds__(kWaves * 64) void rope_any_kernel(RopeArgs a, int64
 }
 
 // ---------------------------------------------------------------------------
-// Rows in whole VE-element units (16 or 8 bytes)
+// Rows in whole VE-element units (16, 8 or 4 bytes)
 // ---------------------------------------------------------------------------
 // Memory-bound: each element is read and written once. A lane holds two units of
 // a row, for pairs (i, i + rot/2) the two halves of VE pairs, so a pair is never
@@ -97,7 +97,7 @@ struct RopePlan {
   int L, rp;                 // lanes a row (a power of two), rows a pass
   int rows, passes;          // rows a token, passes a token
   int ppw, wpt;              // passes a wave, waves a token
-  FastDiv page;
+  FastDiv page, per;         // tokens a page, rows a token
 };
 
 template <int DT, int VE> struct Unit {
@@ -105,7 +105,9 @@ template <int DT, int VE> struct Unit {
   typedef T vec __attribute__((ext_vector_type(VE)));
 };
 
-template <int DT, int VE, bool INTER>
+// FLAT: rows of all tokens end to end, each lane with its own token. Takes the
+// tokens whose rows would leave lanes of their own wave idle.
+template <int DT, int VE, bool INTER, bool FLAT>
 __global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopePlan p,
                                                                int64_t waves) {
   typedef typename Unit<DT, VE>::T T;
@@ -114,9 +116,6 @@ __global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopeP
   const int64_t wave =
       (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (wave >= waves) return;
-  const int64_t t = wave / p.wpt;
-  const int pass0 = (int)(wave - t * p.wpt) * p.ppw;
-  const int pass1 = min(pass0 + p.ppw, p.passes);
 
   // this lane's units of every row it meets
   const int j = lane & (p.L - 1), sub = lane / p.L;
@@ -126,16 +125,31 @@ __global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopeP
   const bool va = j < p.hp + p.rem, vb = va && ub < p.units;
   const int ea = va ? ua * VE : 0, eb = vb ? ub * VE : 0;
 
+  // its token, and the passes over the token's rows
+  int64_t t;
+  int pass0 = 0, pass1 = 1, row0 = sub;
+  bool live = va;
+  if constexpr (FLAT) {
+    const uint32_t row = (uint32_t)wave * p.rp + sub;     // T * rows < 2^31
+    live = va && row < (uint32_t)a.T * p.rows;
+    t = live ? div_by(row, p.per) : 0;
+    row0 = live ? row - (uint32_t)t * p.rows : 0;
+  } else {
+    t = wave / p.wpt;
+    pass0 = (int)(wave - t * p.wpt) * p.ppw;
+    pass1 = min(pass0 + p.ppw, p.passes);
+  }
+
   struct Row {
     V a, b;
     int kind, h;             // 0 query, 1 key, 2 value, 3 none
   };
   auto load = [&](int pass) {
     Row x;
-    const int r = pass * p.rp + sub;
+    const int r = pass * p.rp + row0;
     x.kind = r < a.Hq ? 0 : (r < a.Hq + a.Hkv ? 1 : 2);
     x.h = r - (x.kind == 0 ? 0 : (x.kind == 1 ? (int)a.Hq : (int)(a.Hq + a.Hkv)));
-    if (pass >= pass1 || r >= p.rows || !va) x.kind = 3;
+    if (pass >= pass1 || r >= p.rows || !live) x.kind = 3;
     x.a = V{}, x.b = V{};
     if (x.kind == 3) return x;
     const T* src = x.kind == 0   ? (const T*)a.q + t * a.q_stride[0] + x.h * a.q_stride[1]
@@ -145,7 +159,6 @@ __global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopeP
     if (vb) x.b = *(const V*)(src + eb);
     return x;
   };
-
   Row next = load(pass0);      // on its way before anything is waited for
 
   const int half = (int)(a.rot >> 1);
@@ -178,7 +191,7 @@ __global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopeP
   bool slot_ok = false;
   int64_t kslot = 0, vslot = 0, bslot = 0;
   if (a.cache.k) {
-    const int32_t slot = __builtin_amdgcn_readfirstlane(a.slots[t]);
+    const int32_t slot = FLAT ? a.slots[t] : __builtin_amdgcn_readfirstlane(a.slots[t]);
     slot_ok = slot >= 0 && slot < a.cache.pages * a.cache.page;
     if (slot_ok) {
       const int64_t page = div_by(slot, p.page), tok = slot - page * p.page.d;
@@ -274,10 +287,17 @@ hipError_t run_vec(const RopeArgs& a, hipStream_t s) {
   p.ppw = (int)(all / want < 1 ? 1 : (all / want < p.passes ? all / want : p.passes));
   p.wpt = (p.passes + p.ppw - 1) / p.ppw;
   p.page = fast_div(a.cache.k ? (uint32_t)a.cache.page : 1);
-  const int64_t waves = a.T * p.wpt, blocks = (waves + kWaves - 1) / kWaves;
+  p.per = fast_div((uint32_t)p.rows);
+  // Tokens of one pass, or that leave a quarter of their passes' lanes idle, go end to
+  // end (60000 tokens of 3 rows: 51 -> 26 us; of 10 rows in two passes: 47 -> 41); with more
+  // rows the wave that stays with its token is faster (48 rows: 356 us, end to end 406).
+  const bool flat = (p.passes == 1 || 4 * p.rows < 3 * p.passes * p.rp) &&
+                    a.T * p.rows < 0x7FFFFFFF - 64;
+  const int64_t waves = flat ? (a.T * p.rows + p.rp - 1) / p.rp : a.T * p.wpt;
+  const int64_t blocks = (waves + kWaves - 1) / kWaves;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const auto kernel =
-      a.interleaved ? rope_vec_kernel<DT, VE, true> : rope_vec_kernel<DT, VE, false>;
+  const auto kernel = a.interleaved ? (flat ? rope_vec_kernel<DT, VE, true, true> : rope_vec_kernel<DT, VE, true, false>)
+                                    : (flat ? rope_vec_kernel<DT, VE, false, true> : rope_vec_kernel<DT, VE, false, false>);
   kernel<<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, p, waves);
   return hipGetLastError();
 }
@@ -287,13 +307,16 @@ hipError_t run_vec(const RopeArgs& a, hipStream_t s) {
 hipError_t launch_qk_norm_rope(const RopeArgs& a, int dt, hipStream_t s) {
   const int64_t rows = a.T * (a.Hq + a.Hkv * (a.cache.k ? 2 : 1));
   if (rows == 0) return hipSuccess;
-  // 64 lanes of two units are the longest row
+  // The widest units that the rows, and half the rotated part, are whole numbers of;
+  // 64 lanes of two units are the longest row.
   if (dt == FK_F32) {
     if (a.D <= 512 && in_units(a, 4, 16)) return run_vec<FK_F32, 4>(a, s);
-  } else if (a.D <= 1024 && in_units(a, 2, 16)) {
-    return dt == FK_F16 ? run_vec<FK_F16, 8>(a, s) : run_vec<FK_BF16, 8>(a, s);
-  } else if (a.D <= 512 && in_units(a, 2, 8)) {
-    return dt == FK_F16 ? run_vec<FK_F16, 4>(a, s) : run_vec<FK_BF16, 4>(a, s);
+    if (a.D <= 256 && in_units(a, 4, 8)) return run_vec<FK_F32, 2>(a, s);
+  } else {
+    const bool f16 = dt == FK_F16;
+    if (a.D <= 1024 && in_units(a, 2, 16)) return f16 ? run_vec<FK_F16, 8>(a, s) : run_vec<FK_BF16, 8>(a, s);
+    if (a.D <= 512 && in_units(a, 2, 8)) return f16 ? run_vec<FK_F16, 4>(a, s) : run_vec<FK_BF16, 4>(a, s);
+    if (a.D <= 256 && in_units(a, 2, 4)) return f16 ? run_vec<FK_F16, 2>(a, s) : run_vec<FK_BF16, 2>(a, s);
   }
   const int64_t blocks = (rows + kWaves - 1) / kWaves;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
