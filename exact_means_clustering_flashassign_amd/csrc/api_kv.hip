@@ -112,7 +112,7 @@ fk_status_t fk_qk_norm_rope(const void* q, const int64_t q_stride[2], const void
 size_t fk_workspace_size_attn(fk_dtype_t dt, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   if (!valid_dt(dt) || below(B, 0) || below(Hq, 1) || below(Hkv, 1) || Hq % Hkv || below(D, 1))
     return 0;
-  const size_t n = fk::attn_ws_bytes(B, Hq, Hkv, D);
+  const size_t n = fk::attn_ws_bytes(dt, B, Hq, Hkv, D);
   return n < 256 ? 256 : n;
 }
 

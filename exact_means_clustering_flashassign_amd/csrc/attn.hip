@@ -189,7 +189,7 @@ struct Plan {
   int parts;            // blocks per (cache head, head tile); 0: a team per request
   int team;             // waves that share a request's steps: 4, 2 or 1
   int heads, tiles;     // cache heads, head tiles per cache head
-  int G, hr;            // query heads per cache head; of them per tile, at most
+  int G, width, hr;     // query heads per cache head, per head tile, and per tile at most
   FastDiv page;
   float* o;             // (parts, heads, tiles, 2, hr, D) partial sums
   float* ml;            // (parts, heads, tiles, 2, hr, 2) their maximum and sum
@@ -238,10 +238,10 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
 }
 
 // State of one wave over a run of steps.
-template <int DT, int DP> struct Acc {
+template <int DT, int DP, int HT> struct Acc {
   using S = Shape<DT, DP>;
-  float m, l;                          // of head m's keys; l: this lane's share
-  floatx4_t o[S::nu * S::ve];
+  float m[HT], l[HT];                  // of lane m's head of each tile; l: this lane's share
+  floatx4_t o[HT][S::nu * S::ve];
 };
 
 // Row addresses and bias of one step's keys, per wave and parity.
@@ -251,35 +251,44 @@ template <int DT, int DP> struct Rows {
   float bias[n];
 };
 
-template <int DT, int DP, bool EXTRA, bool EXACT>
+template <int DT, int DP, int HT, bool EXTRA, bool EXACT>
 __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t b, int hk, int ht,
                                        int len, int step, int stride, int end,
                                        Rows<DT, DP>* rows,
-                                       Acc<DT, DP>& acc) {
+                                       Acc<DT, DP, HT>& acc) {
   using S = Shape<DT, DP>;
   const fk_kv_cache_t& c = a.cache;
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const int D = EXACT ? DP : (int)c.dim;
   constexpr int eb = Val<DT>::bytes;
-  acc.m = -INFINITY;
-  acc.l = 0.f;
 #pragma unroll
-  for (int i = 0; i < S::nu * S::ve; ++i) acc.o[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+  for (int h = 0; h < HT; ++h) {
+    acc.m[h] = -INFINITY;
+    acc.l[h] = 0.f;
+#pragma unroll
+    for (int i = 0; i < S::nu * S::ve; ++i) acc.o[h][i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+  }
   if (step >= end) return;
 
   // Query fragments; heads past G and elements past D are zero. An element
   // past D reads the key row's start instead, times a zero query.
-  uint4 q[S::nc];
+  uint4 q[HT][S::nc];
   uint32_t koff[S::nc], voff[S::nu];
-  const int head = ht * kHeadTile + m;
-  const char* qp = (const char*)a.q +
-                   (b * a.q_stride[0] + (int64_t)(hk * p.G + min(head, p.G - 1)) * a.q_stride[1]) * eb;
 #pragma unroll
   for (int i = 0; i < S::nc; ++i) {
     const int e = i * 4 * S::unit + g * S::unit;
     koff[i] = e < D ? e * eb : 0;
-    q[i] = load16((uint64_t)(qp + koff[i]));
-    if (e >= D || head >= p.G) q[i] = make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int h = 0; h < HT; ++h) {
+    const int head = (ht * HT + h) * kHeadTile + m;
+    const char* qp = (const char*)a.q + (b * a.q_stride[0] +
+                                         (int64_t)(hk * p.G + min(head, p.G - 1)) * a.q_stride[1]) * eb;
+#pragma unroll
+    for (int i = 0; i < S::nc; ++i) {
+      q[h][i] = load16((uint64_t)(qp + koff[i]));
+      if (i * 4 * S::unit + g * S::unit >= D || head >= p.G) q[h][i] = make_uint4(0, 0, 0, 0);
+    }
   }
 #pragma unroll
   for (int i = 0; i < S::nu; ++i) {
@@ -359,50 +368,55 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
     Rows<DT, DP>& now = rows[par];
     Rows<DT, DP>& next = rows[par ^ 1];
     put_rows(next, step + stride, pg1, bias1);
-    float s[S::tiles][4];
+    float s[HT][S::tiles][4];
 #pragma unroll
-    for (int u = 0; u < S::tiles; ++u) {
-      floatx4_t x = {0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < HT; ++h)
 #pragma unroll
-      for (int i = 0; i < S::nc; ++i) x = Mfma16<DT>::run(kf[u][i], q[i], x);
+      for (int u = 0; u < S::tiles; ++u) {
+        floatx4_t x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[u][i] = x[i];
-    }
+        for (int i = 0; i < S::nc; ++i) x = Mfma16<DT>::run(kf[u][i], q[h][i], x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[h][u][i] = x[i];
+      }
     load_k(next);
     __builtin_amdgcn_sched_barrier(0);   // the next keys are on their way before the softmax
     bias1 = bias_of(step + 2 * stride, pg2);
     pg1 = pg2;
     pg2 = entry(step + 3 * stride);
 
-    float top = acc.m;
 #pragma unroll
-    for (int u = 0; u < S::tiles; ++u)
+    for (int h = 0; h < HT; ++h) {
+      float top = acc.m[h];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // -inf where a key does not count: its score is 0 (a zero row)
-        float x = s[u][i] * a.scale;
-        if (cap) x = capped(x, a.softcap, inv_cap);
-        s[u][i] = x + now.bias[16 * u + 4 * g + i];
-        top = fmaxf(top, s[u][i]);
-      }
-    top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    // differences before the scaling by log2 e: a bias of the type's lowest
-    // value must not overflow; with nothing but -inf so far, subtract nothing
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float alpha = fast_exp2((acc.m - ref) * kLog2e);
-    acc.m = top;
-    float part = 0.f;
+      for (int u = 0; u < S::tiles; ++u)
 #pragma unroll
-    for (int u = 0; u < S::tiles; ++u)
+        for (int i = 0; i < 4; ++i) {
+          // -inf where a key does not count: its score is 0 (a zero row)
+          float x = s[h][u][i] * a.scale;
+          if (cap) x = capped(x, a.softcap, inv_cap);
+          s[h][u][i] = x + now.bias[16 * u + 4 * g + i];
+          top = fmaxf(top, s[h][u][i]);
+        }
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      // differences before the scaling by log2 e: a bias of the type's lowest
+      // value must not overflow; with nothing but -inf so far, subtract nothing
+      const float ref = top == -INFINITY ? 0.f : top;
+      const float alpha = fast_exp2((acc.m[h] - ref) * kLog2e);
+      acc.m[h] = top;
+      float part = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[u][i] = fast_exp2(fmaf(s[u][i] - ref, kLog2e, kProbShift<DT>));
-        part += s[u][i];
-      }
-    acc.l = fmaf(acc.l, alpha, part);
+      for (int u = 0; u < S::tiles; ++u)
 #pragma unroll
-    for (int i = 0; i < S::nu * S::ve; ++i) acc.o[i] *= alpha;
+        for (int i = 0; i < 4; ++i) {
+          s[h][u][i] = fast_exp2(fmaf(s[h][u][i] - ref, kLog2e, kProbShift<DT>));
+          part += s[h][u][i];
+        }
+      acc.l[h] = fmaf(acc.l[h], alpha, part);
+#pragma unroll
+      for (int i = 0; i < S::nu * S::ve; ++i) acc.o[h][i] *= alpha;
+    }
 
     if constexpr (DT == FK_F32) {
 #pragma unroll
@@ -412,10 +426,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
 #pragma unroll
           for (int t = 0; t < S::ve; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              acc.o[u * S::ve + t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                  __builtin_bit_cast(float, word(vf[4 * y + j][u], t)), s[y][j],
-                  acc.o[u * S::ve + t], 0, 0, 0);
+            for (int j = 0; j < 4; ++j) {
+              floatx4_t& o = acc.o[0][u * S::ve + t];
+              o = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                  __builtin_bit_cast(float, word(vf[4 * y + j][u], t)), s[0][y][j], o, 0, 0, 0);
+            }
     } else {
       // Probabilities as the sum of two 16-bit numbers: one alone would round
       // each to 8 (bf16) or 11 bits, an error as large as the result's own
@@ -424,14 +439,18 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
       typedef T T8 __attribute__((ext_vector_type(8)));
 #pragma unroll
       for (int y = 0; y < S::tiles / 2; ++y) {
-        T8 hi, lo;
+        uint4 ph[HT], pl[HT];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x = s[2 * y + (j >> 2)][j & 3];
-          hi[j] = (T)x;
-          lo[j] = (T)(x - (float)hi[j]);
+        for (int h = 0; h < HT; ++h) {
+          T8 hi, lo;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float x = s[h][2 * y + (j >> 2)][j & 3];
+            hi[j] = (T)x;
+            lo[j] = (T)(x - (float)hi[j]);
+          }
+          ph[h] = __builtin_bit_cast(uint4, hi), pl[h] = __builtin_bit_cast(uint4, lo);
         }
-        const uint4 ph = __builtin_bit_cast(uint4, hi), pl = __builtin_bit_cast(uint4, lo);
         auto pick = [&](int j, int u, int t) {       // element t of rows j (low half) and j + 1
           return __builtin_amdgcn_perm(word(vf[8 * y + j + 1][u], t >> 1),
                                        word(vf[8 * y + j][u], t >> 1),
@@ -442,17 +461,23 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
 #pragma unroll
           for (int t = 0; t < S::ve; ++t) {
             const uint4 vt = make_uint4(pick(0, u, t), pick(2, u, t), pick(4, u, t), pick(6, u, t));
-            floatx4_t& o = acc.o[u * S::ve + t];
-            o = Mfma16<DT>::run(vt, ph, o);
-            o = Mfma16<DT>::run(vt, pl, o);
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+              floatx4_t& o = acc.o[h][u * S::ve + t];
+              o = Mfma16<DT>::run(vt, ph[h], o);
+              o = Mfma16<DT>::run(vt, pl[h], o);
+            }
           }
       }
     }
     load_v(next);
     __builtin_amdgcn_sched_barrier(0);
   }
-  acc.l += __shfl_xor(acc.l, 16, 64);
-  acc.l += __shfl_xor(acc.l, 32, 64);
+#pragma unroll
+  for (int h = 0; h < HT; ++h) {
+    acc.l[h] += __shfl_xor(acc.l[h], 16, 64);
+    acc.l[h] += __shfl_xor(acc.l[h], 32, 64);
+  }
 }
 
 // Where part `w` of the flattened costs starts: request and cost before it.
@@ -525,13 +550,16 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const float* x) {
   }
 }
 
-// Waves a SIMD holds (registers) and with them blocks a CU: the parts of a call are as
-// many as the chip holds at once.
-template <int DP> constexpr int kWavesPerSimd = DP <= 64 ? 3 : (DP == 128 ? 2 : 1);
+// Waves a SIMD holds (by their registers). The parts of a call are as many as the chip
+// holds blocks at once.
+constexpr int waves_per_simd(int64_t D, int64_t width) {
+  const bool two = width > kHeadTile;
+  return D <= 32 ? 3 : (D <= 64 ? (two ? 2 : 3) : (D <= 128 ? 2 : 1));
+}
 constexpr int kMaxParts = kMaxCus * 3;
 
-template <int DT, int DP, bool EXTRA, bool EXACT>
-__global__ __launch_bounds__(kWaves * 64, kWavesPerSimd<DP>) void attn_mfma_kernel(AttnArgs a, Plan p) {
+template <int DT, int DP, int HT, bool EXTRA, bool EXACT>
+__global__ __launch_bounds__(kWaves * 64, waves_per_simd(DP, HT * kHeadTile)) void attn_mfma_kernel(AttnArgs a, Plan p) {
   using S = Shape<DT, DP>;
   __shared__ Rows<DT, DP> rows[kWaves][2];
   __shared__ float so[kWaves][kHeadTile][S::ldo];
@@ -542,7 +570,6 @@ __global__ __launch_bounds__(kWaves * 64, kWavesPerSimd<DP>) void attn_mfma_kern
   const int64_t unit = xcd_remap(blockIdx.x, gridDim.x) * teams + w / p.team;
   const int ht = (int)(unit % p.tiles), hk = (int)((unit / p.tiles) % p.heads);
   const int64_t part = unit / ((int64_t)p.tiles * p.heads);
-  const int nh = min(kHeadTile, p.G - ht * kHeadTile);
   const int D = (int)a.cache.dim;
 
   Start st;
@@ -564,46 +591,52 @@ __global__ __launch_bounds__(kWaves * 64, kWavesPerSimd<DP>) void attn_mfma_kern
     }
     const bool starts = at >= st.lo;           // the request begins in this part
     if (t0 < t1 || (steps == 0 && starts)) {
-      Acc<DT, DP> acc;
-      attend<DT, DP, EXTRA, EXACT>(a, p, b, hk, ht, len, t0 + w - k0, p.team, t1, rows[w], acc);
-      __syncthreads();                         // the last request's results are out
-      if (m < nh) {
-        if (g == 0) sm[w][m] = acc.m, sl[w][m] = acc.l;
-#pragma unroll
-        for (int u = 0; u < S::nu; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int t = 0; t < S::ve; ++t)
-              so[w][m][u * 16 * S::ve + S::ve * (4 * g + i) + t] = acc.o[u * S::ve + t][i];
-      }
-      __syncthreads();
+      Acc<DT, DP, HT> acc;
+      attend<DT, DP, HT, EXTRA, EXACT>(a, p, b, hk, ht, len, t0 + w - k0, p.team, t1, rows[w], acc);
       const bool whole = t0 == 0 && t1 == steps;
       const int slot = t0 == 0 ? 1 : 0;
       const int64_t ps = (((part * p.heads + hk) * p.tiles + ht) * 2 + slot) * p.hr;
-      for (int i = threadIdx.x - k0 * 64; i < nh * (DP / 4) && !idle; i += p.team * 64) {
-        const int h = i / (DP / 4), e = (i - h * (DP / 4)) * 4;
-        float top = -INFINITY;
-        for (int k = k0; k < k1; ++k) top = fmaxf(top, sm[k][h]);
-        float x[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-        for (int k = k0; k < k1; ++k) {
-          const float f = join_factor(sm[k][h], sl[k][h], top);
-          l = fmaf(f, sl[k][h], l);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = fmaf(f, so[k][h][e + j], x[j]);
+      for (int h2 = 0; h2 < HT; ++h2) {
+        const int h0 = (ht * HT + h2) * kHeadTile;        // first head of this tile
+        const int nh = min(kHeadTile, p.G - h0);
+        __syncthreads();                       // the last results are out
+        if (m < nh) {
+          if (g == 0) sm[w][m] = acc.m[h2], sl[w][m] = acc.l[h2];
+#pragma unroll
+          for (int u = 0; u < S::nu; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int t = 0; t < S::ve; ++t)
+                so[w][m][u * 16 * S::ve + S::ve * (4 * g + i) + t] = acc.o[h2][u * S::ve + t][i];
         }
-        if (e >= D) continue;
-        if (whole) {
-          const int64_t row = b * a.Hq + hk * p.G + ht * kHeadTile + h;
-          const float r = l == 0.f ? 0.f : 1.f / l;
+        __syncthreads();
+        for (int i = threadIdx.x - k0 * 64; i < nh * (DP / 4) && !idle; i += p.team * 64) {
+          const int h = i / (DP / 4), e = (i - h * (DP / 4)) * 4;
+          float top = -INFINITY;
+          for (int k = k0; k < k1; ++k) top = fmaxf(top, sm[k][h]);
+          float x[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+          for (int k = k0; k < k1; ++k) {
+            const float f = join_factor(sm[k][h], sl[k][h], top);
+            l = fmaf(f, sl[k][h], l);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] *= r;
-          store4<DT>(a.out, row * D + e, x);
-          if (e == 0 && a.lse)
-            a.lse[row] = l == 0.f ? -INFINITY : top + (logf(l) - kProbShift<DT> * kLn2);
-        } else {
-          *(float4*)(p.o + (ps + h) * D + e) = make_float4(x[0], x[1], x[2], x[3]);
-          if (e == 0) p.ml[(ps + h) * 2] = top, p.ml[(ps + h) * 2 + 1] = l;
+            for (int j = 0; j < 4; ++j) x[j] = fmaf(f, so[k][h][e + j], x[j]);
+          }
+          if (e >= D) continue;
+          if (whole) {
+            const int64_t row = b * a.Hq + hk * p.G + h0 + h;
+            const float r = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] *= r;
+            store4<DT>(a.out, row * D + e, x);
+            if (e == 0 && a.lse)
+              a.lse[row] = l == 0.f ? -INFINITY : top + (logf(l) - kProbShift<DT> * kLn2);
+          } else {
+            const int64_t pr = ps + h2 * kHeadTile + h;
+            *(float4*)(p.o + pr * D + e) = make_float4(x[0], x[1], x[2], x[3]);
+            if (e == 0) p.ml[pr * 2] = top, p.ml[pr * 2 + 1] = l;
+          }
         }
       }
       if (p.parts > 0 && hk == 0 && ht == 0 && threadIdx.x == 0) {
@@ -630,7 +663,7 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Plan p) {
   const int h = (int)(blockIdx.x - b * a.Hq);
   const int first = p.cover[2 * b], last = p.cover[2 * b + 1];
   if (first == last) return;
-  const int hk = h / p.G, ht = (h % p.G) / kHeadTile, hr = (h % p.G) % kHeadTile;
+  const int hk = h / p.G, ht = (h % p.G) / p.width, hr = (h % p.G) % p.width;
   const int D = (int)a.cache.dim, n = last - first + 1;
   auto row = [&](int i) {
     const int64_t part = first + i;
@@ -692,41 +725,52 @@ bool aligned16(const AttnArgs& a, int eb) {
   return !(((uintptr_t)a.q | (uintptr_t)c.k | (uintptr_t)c.v | (uintptr_t)a.out) & 15);
 }
 
-int64_t head_tiles(int64_t G) { return (G + kHeadTile - 1) / kHeadTile; }
+// Query heads a wave serves at once: 32 where there are more than 16 and the registers
+// hold both tiles (16-bit rows of at most 128).
+int64_t tile_width(int dt, int64_t D, int64_t G) {
+  return G > kHeadTile && dt != FK_F32 && D <= 128 ? 2 * kHeadTile : kHeadTile;
+}
 
 // Parts per (cache head, head tile): `blocks` shared out.
 int64_t parts_of(int64_t blocks, int64_t units) { return units >= blocks ? 1 : blocks / units; }
 
-// Blocks the chip holds at once for rows of D elements.
-int64_t blocks_of(int64_t D) {
-  const int64_t cus = device_cus() < kMaxCus ? device_cus() : kMaxCus;
-  return cus * (D <= 64 ? kWavesPerSimd<64> : (D <= 128 ? kWavesPerSimd<128> : kWavesPerSimd<256>)) * 4 / kWaves;
+int64_t chip_blocks(int64_t cus, int64_t D, int64_t width) {
+  return (cus < kMaxCus ? cus : kMaxCus) * waves_per_simd(D, width) * 4 / kWaves;
 }
 
 // Waves a head when requests are cut: the block's waves take as many neighbouring
 // heads as divide them evenly.
 int team_of(int64_t units) { return units % 4 == 0 ? 1 : (units % 2 == 0 ? 2 : 4); }
 
-template <int DT, int DP>
+template <int DT, int DP, int HT>
 hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   Plan p{};
   p.heads = (int)a.cache.heads;
   p.G = (int)(a.Hq / a.cache.heads);
-  p.tiles = (int)head_tiles(p.G);
-  p.hr = p.G < kHeadTile ? p.G : kHeadTile;
+  p.width = HT * kHeadTile;
+  p.tiles = (p.G + p.width - 1) / p.width;
+  p.hr = p.G < p.width ? p.G : p.width;
   p.page = fast_div((uint32_t)a.cache.page);
   const int64_t units = (int64_t)p.heads * p.tiles;
-  const int64_t most = a.max_len > 0 && a.max_len < a.width * a.cache.page ? a.max_len : a.width * a.cache.page;
-  const bool cut = most > 512;
-  const int64_t resident = blocks_of(DP);
+  int64_t most = a.width * a.cache.page;                // keys of the longest request, at most
+  if (most > 0x7FFFFFFF) most = 0x7FFFFFFF;
+  if (a.max_len > 0 && a.max_len < most) most = a.max_len;
+  // Cutting costs a second launch and a trip through memory. Up to 512 keys a request is
+  // done faster whole (32 requests of 400 keys: 14.7 us, cut 21.4), unless there are
+  // many, whose lengths may differ: one wave each is best up to 8 steps, and beyond that
+  // cutting evens them out (256 requests up to 512 keys, spread over the logarithm: 35 us
+  // cut, 50 whole; all alike: 91 and 87).
+  const int64_t resident = chip_blocks(device_cus(), DP, p.width);
+  const bool many = units * a.B >= kWaves * resident;
+  const bool cut = most > 512 || (many && most > 8 * Shape<DT, DP>::keys);
   if (cut) {
     // Where there are steps enough for every wave of the chip, a block's waves take
     // neighbouring heads, whose rows lie side by side in the cache, instead of one
     // head's steps in turn: the block reads 4 rows' length in one piece (long_b32: 774 us
     // with 1 head a block, 697 with 2, 670 with 4). With fewer steps the waves share them
     // and join in LDS, not through memory.
-    const int64_t steps = units * a.B * ((most + Shape<DT, DP>::keys - 1) / Shape<DT, DP>::keys);
-    p.team = steps >= 4 * kWaves * resident ? team_of(units) : kWaves;
+    const double steps = (double)units * a.B * ((most + Shape<DT, DP>::keys - 1) / Shape<DT, DP>::keys);
+    p.team = steps >= 4.0 * kWaves * resident ? team_of(units) : kWaves;
     const int64_t groups = units * p.team / kWaves;       // blocks that make one part
     p.parts = (int)parts_of(resident, groups);
     const int64_t slots = units * p.parts * 2 * p.hr;
@@ -736,8 +780,8 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
     p.cover = (int32_t*)(w + slots * a.cache.dim * 4 + slots * 8);
   } else {
     // One wave each where that alone fills the chip, or where a second wave would
-    // find nothing to do.
-    p.team = most <= Shape<DT, DP>::keys || units * a.B >= kWaves * resident ? 1 : kWaves;
+    // find nothing to do (222 requests of 3 keys, 32 heads: 19 us, 40 with four waves).
+    p.team = many || most <= Shape<DT, DP>::keys ? 1 : kWaves;
   }
   const int64_t blocks = (units * (cut ? p.parts : a.B) * p.team + kWaves - 1) / kWaves;
   if (blocks > 0x7FFFFFFF || a.B * a.Hq > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
@@ -745,12 +789,17 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   const auto aligned = [](uintptr_t base, const int64_t* s) {
     return !((base | (uintptr_t)((s[0] | s[1] | s[2]) * Val<DT>::bytes)) & 127);
   };
-  const bool exact = a.cache.dim == DP && p.tiles == 1 && DP * Val<DT>::bytes % 128 == 0 &&
+  // Caches that the 256 MB last-level cache may still hold from the step before are read
+  // without the mark (4 requests of 512 keys: 10.4 us, marked 13.3).
+  const double bytes = 2.0 * a.B * most * a.cache.heads * DP * Val<DT>::bytes;
+  const bool exact = bytes >= (double)(128 << 20) && a.cache.dim == DP && p.tiles == 1 && DP * Val<DT>::bytes % 128 == 0 &&
                      aligned((uintptr_t)a.cache.k, a.cache.k_stride) &&
                      aligned((uintptr_t)a.cache.v, a.cache.v_stride);
   const bool extra = a.softcap > 0.f || a.cache.key_bias;
-  const auto kernel = exact ? (extra ? attn_mfma_kernel<DT, DP, true, true> : attn_mfma_kernel<DT, DP, false, true>)
-                            : (extra ? attn_mfma_kernel<DT, DP, true, false> : attn_mfma_kernel<DT, DP, false, false>);
+  const auto kernel = exact ? (extra ? attn_mfma_kernel<DT, DP, HT, true, true>
+                                     : attn_mfma_kernel<DT, DP, HT, false, true>)
+                            : (extra ? attn_mfma_kernel<DT, DP, HT, true, false>
+                                     : attn_mfma_kernel<DT, DP, HT, false, false>);
   kernel<<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !cut) return e;
@@ -762,21 +811,26 @@ template <int DT>
 hipError_t run(const AttnArgs& a, void* ws, hipStream_t s) {
   const int64_t D = a.cache.dim;
   if (D > 256 || !aligned16(a, Val<DT>::bytes)) return run_any<DT>(a, s);
-  return D <= 32 ? run_mfma<DT, 32>(a, ws, s)
-         : D <= 64 ? run_mfma<DT, 64>(a, ws, s)
-         : D <= 128 ? run_mfma<DT, 128>(a, ws, s)
-                    : run_mfma<DT, 256>(a, ws, s);
+  if constexpr (DT != FK_F32) {
+    if (tile_width(DT, D, a.Hq / a.cache.heads) > kHeadTile)
+      return D <= 32   ? run_mfma<DT, 32, 2>(a, ws, s)
+             : D <= 64 ? run_mfma<DT, 64, 2>(a, ws, s)
+                       : run_mfma<DT, 128, 2>(a, ws, s);
+  }
+  return D <= 32    ? run_mfma<DT, 32, 1>(a, ws, s)
+         : D <= 64  ? run_mfma<DT, 64, 1>(a, ws, s)
+         : D <= 128 ? run_mfma<DT, 128, 1>(a, ws, s)
+                    : run_mfma<DT, 256, 1>(a, ws, s);
 }
 
 }  // namespace
 
-size_t attn_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+size_t attn_ws_bytes(int dt, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   if (D > 256) return 256;
   // sized for the largest chip: a pure function of the shape
-  const int64_t G = Hq / Hkv, units = Hkv * head_tiles(G);
-  const int64_t most = kMaxCus * (D <= 64 ? kWavesPerSimd<64> : (D <= 128 ? kWavesPerSimd<128> : kWavesPerSimd<256>));
+  const int64_t G = Hq / Hkv, width = tile_width(dt, D, G), units = Hkv * ((G + width - 1) / width);
   const int64_t groups = units * team_of(units) / kWaves;
-  const size_t slots = (size_t)units * parts_of(most, groups) * 2 * (G < kHeadTile ? G : kHeadTile);
+  const size_t slots = (size_t)units * parts_of(chip_blocks(kMaxCus, D, width), groups) * 2 * (G < width ? G : width);
   return slots * D * 4 + slots * 8 + (size_t)B * 8;
 }
 

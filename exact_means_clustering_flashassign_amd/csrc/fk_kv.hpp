@@ -82,7 +82,7 @@ struct AttnArgs {
   float* lse;
 };
 constexpr int64_t kAttnMaxDim = 1024;
-size_t attn_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+size_t attn_ws_bytes(int dt, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
 hipError_t launch_paged_attn(const AttnArgs& a, int dt, void* ws, hipStream_t s);
 
 }  // namespace fk
