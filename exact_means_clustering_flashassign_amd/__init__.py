@@ -39,3 +39,4 @@ from ._binding import (  # noqa: F401
     workspace,
 )
 from .api import FlashKMeans, batch_kmeans_Euclid, random_init  # noqa: F401,E402
+from .kvcache import ClusteredKVCache  # noqa: F401,E402

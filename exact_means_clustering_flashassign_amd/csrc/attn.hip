@@ -30,13 +30,21 @@ __device__ __forceinline__ float capped(float s, float cap, float inv_cap) {
   return s == s ? r : s;     // the clamp drops a NaN
 }
 
-// Any size, stride and alignment. One block per (request, query head); a wave
-// takes every fourth key, a lane every 64th element of a row.
+// Scale of a partial result (m, l) under the common maximum.
+__device__ __forceinline__ float join_factor(float m, float l, float top) {
+  return l == 0.f ? 0.f : fast_exp2((m - top) * kLog2e);
+}
+
+// Any size, stride and alignment. One block per (request, query head, part of the
+// request's keys); a wave takes every fourth key, a lane every 64th element of a row. With
+// one part the result is final, else parts leave o (B,Hq,parts,D), ml (B,Hq,parts,2).
 template <int DT, int EPL>
-__global__ __launch_bounds__(kWaves * 64) void attn_any_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kWaves * 64) void attn_any_kernel(AttnArgs a, int parts, float* po,
+                                                               float* pml) {
   using E = typename Val<DT>::type;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t b = blockIdx.x / a.Hq, h = blockIdx.x - b * a.Hq;
+  const int64_t bh = blockIdx.x / parts, b = bh / a.Hq, h = bh - b * a.Hq;
+  const int part = (int)(blockIdx.x - bh * parts);
   const fk_kv_cache_t& c = a.cache;
   const int D = (int)c.dim;
   const int64_t hk = h / (a.Hq / c.heads);
@@ -50,8 +58,9 @@ __global__ __launch_bounds__(kWaves * 64) void attn_any_kernel(AttnArgs a) {
   }
   float m = -INFINITY, l = 0.f;
   const int64_t cap_len = a.width * c.page;
-  const int64_t len = a.lens[b] < cap_len ? a.lens[b] : cap_len;
-  for (int64_t j = w; j < len; j += kWaves) {
+  const int64_t len = a.lens[b] < 0 ? 0 : (a.lens[b] < cap_len ? a.lens[b] : cap_len);
+  const int64_t last = len * (part + 1) / parts;
+  for (int64_t j = len * part / parts + w; j < last; j += kWaves) {
     const int64_t page = a.table[b * a.ld_table + j / c.page], tok = j % c.page;
     if (page < 0 || page >= c.pages) continue;
     float bias = 0.f;
@@ -71,8 +80,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn_any_kernel(AttnArgs a) {
     if (a.softcap > 0.f) s = capped(s, a.softcap, 1.f / a.softcap);
     s += bias;
     const float mn = fmaxf(m, s);
-    const float alpha = m == -INFINITY ? 0.f : __expf(m - mn);
-    const float p = s == -INFINITY ? 0.f : __expf(s - mn);   // a NaN score stays one
+    const float alpha = m == -INFINITY ? 0.f : fast_exp2((m - mn) * kLog2e);
+    const float p = s == -INFINITY ? 0.f : fast_exp2((s - mn) * kLog2e);   // NaN stays NaN
     l = l * alpha + p;
     m = mn;
 #pragma unroll
@@ -90,29 +99,77 @@ __global__ __launch_bounds__(kWaves * 64) void attn_any_kernel(AttnArgs a) {
   for (int i = 1; i < kWaves; ++i) top = fmaxf(top, sm[i]);
   float f[kWaves], total = 0.f;
   for (int i = 0; i < kWaves; ++i) {
-    f[i] = sl[i] == 0.f ? 0.f : __expf(sm[i] - top);
+    f[i] = join_factor(sm[i], sl[i], top);
     total += f[i] * sl[i];
   }
   const bool any = total != 0.f;         // true for NaN: it has to reach the result
   for (int e = threadIdx.x; e < D; e += kWaves * 64) {
     float t = 0.f;
     for (int i = 0; i < kWaves; ++i) t += f[i] * so[i][e];
-    Val<DT>::put((E*)a.out + (b * a.Hq + h) * D + e, any ? t / total : 0.f);
+    if (parts > 1) {
+      po[(bh * parts + part) * D + e] = t;
+    } else {
+      Val<DT>::put((E*)a.out + bh * D + e, any ? t / total : 0.f);
+    }
   }
-  if (a.lse && threadIdx.x == 0) a.lse[b * a.Hq + h] = any ? top + logf(total) : -INFINITY;
+  if (threadIdx.x != 0) return;
+  if (parts > 1) pml[(bh * parts + part) * 2] = top, pml[(bh * parts + part) * 2 + 1] = total;
+  else if (a.lse) a.lse[bh] = any ? top + logf(total) : -INFINITY;
+}
+
+constexpr int kAnyParts = 64;
+
+// Joins the parts of one (request, query head).
+template <int DT>
+__global__ __launch_bounds__(kWaves * 64) void attn_any_join_kernel(AttnArgs a, int parts,
+                                                                    const float* po,
+                                                                    const float* pml) {
+  const int64_t bh = blockIdx.x;
+  const int D = (int)a.cache.dim;
+  const float* ml = pml + bh * parts * 2;
+  float top = -INFINITY, total = 0.f;
+  for (int i = 0; i < parts; ++i) top = fmaxf(top, ml[2 * i]);
+  for (int i = 0; i < parts; ++i) total = fmaf(join_factor(ml[2 * i], ml[2 * i + 1], top), ml[2 * i + 1], total);
+  const bool any = total != 0.f;
+  for (int e = threadIdx.x; e < D; e += kWaves * 64) {
+    float t = 0.f;
+    for (int i = 0; i < parts; ++i)
+      t = fmaf(join_factor(ml[2 * i], ml[2 * i + 1], top), po[(bh * parts + i) * D + e], t);
+    Val<DT>::put((typename Val<DT>::type*)a.out + bh * D + e, any ? t / total : 0.f);
+  }
+  if (a.lse && threadIdx.x == 0) a.lse[bh] = any ? top + logf(total) : -INFINITY;
+}
+
+// Parts of a request there: 2048 blocks over all, at most kAnyParts.
+int64_t any_parts(int64_t B, int64_t Hq) {
+  const int64_t n = B * Hq >= 2048 ? 1 : 2048 / (B * Hq > 0 ? B * Hq : 1);
+  return n < kAnyParts ? n : kAnyParts;
 }
 
 template <int DT>
-hipError_t run_any(const AttnArgs& a, hipStream_t s) {
-  const int64_t blocks = a.B * a.Hq;
+hipError_t run_any(const AttnArgs& a, int64_t most, void* ws, hipStream_t s) {
+  const int parts = most > 128 ? (int)any_parts(a.B, a.Hq) : 1;
+  const int64_t heads = a.B * a.Hq, blocks = heads * parts;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   const int64_t D = a.cache.dim;
+  float* po = (float*)ws;
+  float* pml = po + blocks * D;
   const auto kernel = D <= 64    ? attn_any_kernel<DT, 1>
                       : D <= 128 ? attn_any_kernel<DT, 2>
                       : D <= 256 ? attn_any_kernel<DT, 4>
                                  : attn_any_kernel<DT, 16>;
-  kernel<<<(unsigned)blocks, kWaves * 64, 0, s>>>(a);
+  kernel<<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, parts, po, pml);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || parts == 1) return e;
+  attn_any_join_kernel<DT><<<(unsigned)heads, kWaves * 64, 0, s>>>(a, parts, po, pml);
   return hipGetLastError();
+}
+
+// Keys of the longest request, at most: what the tables hold, or the caller's bound.
+int64_t longest(const AttnArgs& a) {
+  int64_t most = a.width * a.cache.page;
+  if (most > 0x7FFFFFFF) most = 0x7FFFFFFF;
+  return a.max_len > 0 && a.max_len < most ? a.max_len : most;
 }
 
 // ---------------------------------------------------------------------------
@@ -533,11 +590,6 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, const Plan& p, in
   return st;
 }
 
-// Scale and sum of `n` partial results (m_i, l_i) of one head.
-__device__ __forceinline__ float join_factor(float m, float l, float top) {
-  return l == 0.f ? 0.f : fast_exp2((m - top) * kLog2e);
-}
-
 template <int DT>
 __device__ __forceinline__ void store4(void* out, int64_t at, const float* x) {
   if constexpr (DT == FK_F32) {
@@ -752,9 +804,7 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   p.hr = p.G < p.width ? p.G : p.width;
   p.page = fast_div((uint32_t)a.cache.page);
   const int64_t units = (int64_t)p.heads * p.tiles;
-  int64_t most = a.width * a.cache.page;                // keys of the longest request, at most
-  if (most > 0x7FFFFFFF) most = 0x7FFFFFFF;
-  if (a.max_len > 0 && a.max_len < most) most = a.max_len;
+  const int64_t most = longest(a);
   // Cutting costs a second launch and a trip through memory. Up to 512 keys a request is
   // done faster whole (32 requests of 400 keys: 14.7 us, cut 21.4), unless there are
   // many, whose lengths may differ: one wave each is best up to 8 steps, and beyond that
@@ -810,7 +860,7 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
 template <int DT>
 hipError_t run(const AttnArgs& a, void* ws, hipStream_t s) {
   const int64_t D = a.cache.dim;
-  if (D > 256 || !aligned16(a, Val<DT>::bytes)) return run_any<DT>(a, s);
+  if (D > 256 || !aligned16(a, Val<DT>::bytes)) return run_any<DT>(a, longest(a), ws, s);
   if constexpr (DT != FK_F32) {
     if (tile_width(DT, D, a.Hq / a.cache.heads) > kHeadTile)
       return D <= 32   ? run_mfma<DT, 32, 2>(a, ws, s)
@@ -826,12 +876,15 @@ hipError_t run(const AttnArgs& a, void* ws, hipStream_t s) {
 }  // namespace
 
 size_t attn_ws_bytes(int dt, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
-  if (D > 256) return 256;
+  // either kernel may run: alignment is not known here
+  const size_t any = (size_t)(B * Hq * any_parts(B, Hq)) * (D + 2) * 4;
+  if (D > 256) return any;
   // sized for the largest chip: a pure function of the shape
   const int64_t G = Hq / Hkv, width = tile_width(dt, D, G), units = Hkv * ((G + width - 1) / width);
   const int64_t groups = units * team_of(units) / kWaves;
   const size_t slots = (size_t)units * parts_of(chip_blocks(kMaxCus, D, width), groups) * 2 * (G < width ? G : width);
-  return slots * D * 4 + slots * 8 + (size_t)B * 8;
+  const size_t cut = slots * D * 4 + slots * 8 + (size_t)B * 8;
+  return cut > any ? cut : any;
 }
 
 hipError_t launch_paged_attn(const AttnArgs& a, int dt, void* ws, hipStream_t s) {
