@@ -57,6 +57,8 @@ TABLES = [
     (1000, 1, 70, 64, 70000, 0, 40, 33),
     (1025, 64, 20, 20, 20000, 1, 700, 600),
     (5000, 16, 7, 7, 30000, 9, 60, 60),
+    (2048, 4, 9, 9, 30000, 3, 20, 12),     # the most whose sums every block forms for itself
+    (2049, 4, 9, 9, 30000, 3, 20, 12),
     (2, 16, 5000, 5000, 10000, 0, 40000, 38000),
 ]
 
@@ -139,6 +141,9 @@ ROPE = [
     (6, 2, 2, 64, 0, False, True, 5, "odd"),
     (4, 2, 1, 1000, 96, False, True, 2, "plain"),
     (300, 7, 1, 192, 64, False, True, 20, "packed"),
+    (2800, 32, 8, 128, 96, False, True, 16, "packed"),     # waves that take several passes
+    (9000, 4, 1, 32, 32, False, True, 0, "packed"),
+    (40, 12, 2, 200, 36, False, True, 16, "packed"),
 ]
 
 
@@ -252,6 +257,9 @@ ATTN = [
     (8, 8, 128, 16, [5000, 2049, 64], None, 0.0, "plain"),
     (8, 1, 128, 16, [20000], "log", 50.0, "plain"),
     (4, 1, 64, 256, [3, 9000, 0, 700, 0, 1], None, 0.0, "plain"),
+    (80, 2, 128, 16, [400, 33, 700], "log", 0.0, "plain"),     # 40 query heads a key head
+    (33, 1, 256, 16, [300, 1], None, 0.0, "plain"),
+    (24, 1, 32, 16, [600, 40], None, 15.0, "heads"),
 ]
 
 
@@ -351,6 +359,18 @@ def test_paged_attn(fk, case, dtype):
         _check_attn(got, want, dtype, case[2], case[6], f"max_len {hint}")
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("case", ATTN, ids=[f"{c[0]}x{c[1]}d{c[2]}p{c[3]}n{max(c[4])}{c[5] or ''}" for c in ATTN])
+def test_paged_attn_wide_tables(fk, case, dtype):
+    """Tables with room for 2^20 keys a request, most of it unused: the split and
+    the loads are those of large caches."""
+    torch = _torch()
+    args, want = _attn_case(case, dtype, seed=len(case[4]) * 100 + case[2])
+    table = args["table"]
+    args["table"] = torch.cat([table, table.new_full((table.shape[0], (1 << 20) // case[3]), -1)], 1)
+    _check_attn(fk.fk_paged_attn(**args), want, dtype, case[2], case[6])
+
+
 def test_paged_attn_many_ragged_requests(fk):
     rng = np.random.default_rng(5)
     lens = [int(n) for n in np.exp(rng.uniform(0, np.log(3000), 90))]
@@ -359,6 +379,12 @@ def test_paged_attn_many_ragged_requests(fk):
     args, want = _attn_case(case, "bf16", 6)
     _check_attn(fk.fk_paged_attn(**args), want, "bf16", 64, 0.0)
     _check_attn(fk.fk_paged_attn(max_len=max(lens), **args), want, "bf16", 64, 0.0)
+    # more requests than a block has threads, cut and whole
+    lens = [int(n) for n in np.exp(rng.uniform(0, np.log(600), 700))]
+    lens[::7] = [0] * len(lens[::7])
+    args, want = _attn_case((4, 4, 128, 8, lens, None, 0.0, "plain"), "f16", 7)
+    for hint in (0, 200, 32):
+        _check_attn(fk.fk_paged_attn(max_len=hint, **args), want, "f16", 128, 0.0)
 
 
 def test_paged_attn_same_bits_any_workspace_and_stream(fk):
