@@ -540,9 +540,14 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
 // Where part `w` of the flattened costs starts: request and cost before it.
 // Every block finds out by itself: thread i adds up requests [i n, (i + 1) n).
 struct Start {
-  int64_t total, lo, hi;     // all costs; this part's range
+  int64_t lo, hi;            // this part's range of costs
   int64_t b, before;         // request that holds lo, cost of those before it
-  int parts;                 // parts in use
+  __device__ __forceinline__ void cut(int64_t total, const Plan& p, int w) {
+    const int64_t most = total / (2 * p.team);     // less is not worth a part of its own
+    const int64_t parts = most < 1 ? 1 : (most < p.parts ? most : p.parts);
+    lo = w < parts ? total * w / parts : total;
+    hi = w < parts ? total * (w + 1) / parts : total;
+  }
 };
 
 template <int KEYS>
@@ -552,6 +557,23 @@ __device__ __forceinline__ int64_t cost_of(const AttnArgs& a, const Plan& p, int
 
 template <int KEYS>
 __device__ __forceinline__ Start find_start(const AttnArgs& a, const Plan& p, int w) {
+  Start st;
+  if (a.B <= 64) {
+    // a request a lane: every wave by itself, without barriers
+    const int lane = threadIdx.x & 63;
+    const uint32_t mine = lane < a.B ? (uint32_t)cost_of<KEYS>(a, p, lane) : 0;   // < 2^26 each
+    uint32_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const uint32_t o = __shfl_up(incl, off, 64);
+      if (lane >= off) incl += o;
+    }
+    st.cut(__shfl(incl, 63, 64), p, w);
+    const int b = __popcll(__ballot(incl <= st.lo));      // requests that end at or before lo
+    st.b = b;
+    st.before = b ? __shfl(incl, b - 1, 64) : 0;
+    return st;
+  }
   __shared__ int64_t wave_tot[kWaves];
   __shared__ int64_t found[2];
   const int64_t n = (a.B + kWaves * 64 - 1) / (kWaves * 64);
@@ -572,12 +594,7 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, const Plan& p, in
     if (i < (int)(threadIdx.x >> 6)) before += wave_tot[i];
     total += wave_tot[i];
   }
-  Start st;
-  st.total = total;
-  const int64_t most = total / (2 * p.team);     // less is not worth a part of its own
-  st.parts = (int)(most < 1 ? 1 : (most < p.parts ? most : p.parts));
-  st.lo = w < st.parts ? total * w / st.parts : total;
-  st.hi = w < st.parts ? total * (w + 1) / st.parts : total;
+  st.cut(total, p, w);
   if (st.lo >= before && st.lo < before + mine) {
     int64_t b = b0, at = before;
     for (int64_t c = cost_of<KEYS>(a, p, b); at + c <= st.lo; c = cost_of<KEYS>(a, p, b)) at += c, ++b;
@@ -702,19 +719,26 @@ __global__ __launch_bounds__(kWaves * 64, waves_per_simd(DP, HT * kHeadTile)) vo
   }
 }
 
-constexpr int kJoin = 256;        // threads of the joining block
+constexpr int kJoin = 256;        // threads of a joining block
 
 // Joins the partial results of a request that was cut: slot 1 of its first part,
-// slot 0 of the others. One block per (request, query head).
-template <int DT>
+// slot 0 of the others. R (request, query head) rows a block: one, or one a wave.
+template <int DT, int R>
 __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Plan p) {
-  __shared__ float fac[kMaxParts], part_l[kMaxParts];
-  __shared__ float red[kJoin][4];
-  __shared__ float redl[kJoin];
-  const int64_t b = blockIdx.x / a.Hq;
-  const int h = (int)(blockIdx.x - b * a.Hq);
+  constexpr int threads = kJoin / R;
+  __shared__ float fac[R][kMaxParts], part_l[R][kMaxParts];
+  __shared__ float red[kJoin][4], redl[kJoin];
+  const int me = R == 1 ? 0 : threadIdx.x / threads, tid = threadIdx.x - me * threads;
+  const int64_t out_row = (int64_t)blockIdx.x * R + me;
+  if (out_row >= a.B * a.Hq) return;
+  const int64_t b = out_row / a.Hq;
+  const int h = (int)(out_row - b * a.Hq);
   const int first = p.cover[2 * b], last = p.cover[2 * b + 1];
   if (first == last) return;
+  const auto sync = [] {
+    if constexpr (R == 1) __syncthreads();
+    else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");      // a row is one wave's
+  };
   const int hk = h / p.G, ht = (h % p.G) / p.width, hr = (h % p.G) % p.width;
   const int D = (int)a.cache.dim, n = last - first + 1;
   auto row = [&](int i) {
@@ -723,25 +747,25 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Plan p) {
   };
   // every thread: maximum over all parts; factors and the sum of the parts' sums
   float top = -INFINITY;
-  for (int i = threadIdx.x & 63; i < n; i += 64) top = fmaxf(top, p.ml[row(i) * 2]);
+  for (int i = tid & 63; i < n; i += 64) top = fmaxf(top, p.ml[row(i) * 2]);
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-  for (int i = threadIdx.x; i < n; i += kJoin) {
+  for (int i = tid; i < n; i += threads) {
     const float2 ml = *(const float2*)(p.ml + row(i) * 2);
-    fac[i] = join_factor(ml.x, ml.y, top);
-    part_l[i] = ml.y;
+    fac[me][i] = join_factor(ml.x, ml.y, top);
+    part_l[me][i] = ml.y;
   }
-  __syncthreads();
+  sync();
   // threads: D / 4 columns by as many groups of partial results as fit
-  const int cols = D / 4, groups = kJoin / cols;
-  const int grp = threadIdx.x / cols, e = (threadIdx.x - grp * cols) * 4;
+  const int cols = D / 4, groups = threads / cols;
+  const int grp = tid / cols, e = (tid - grp * cols) * 4;
   float x[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
   if (grp < groups) {
 #pragma unroll 4
     for (int i = grp; i < n; i += groups) {
-      const float f = fac[i];
+      const float f = fac[me][i];
       const float4 v = *(const float4*)(p.o + row(i) * D + e);
-      l = fmaf(f, part_l[i], l);
+      l = fmaf(f, part_l[me][i], l);
       x[0] = fmaf(f, v.x, x[0]);
       x[1] = fmaf(f, v.y, x[1]);
       x[2] = fmaf(f, v.z, x[2]);
@@ -751,8 +775,8 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Plan p) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) red[threadIdx.x][j] = x[j];
   redl[threadIdx.x] = l;
-  __syncthreads();
-  if ((int)threadIdx.x >= cols) return;
+  sync();
+  if (tid >= cols) return;
   for (int k = 1; k < groups; ++k) {
     l += redl[threadIdx.x + k * cols];
 #pragma unroll
@@ -761,10 +785,9 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Plan p) {
   const float r = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int j = 0; j < 4; ++j) x[j] *= r;
-  const int64_t orow = b * a.Hq + h;
-  store4<DT>(a.out, orow * D + e, x);
+  store4<DT>(a.out, out_row * D + e, x);
   if (e == 0 && a.lse)
-    a.lse[orow] = l == 0.f ? -INFINITY : top + (logf(l) - kProbShift<DT> * kLn2);
+    a.lse[out_row] = l == 0.f ? -INFINITY : top + (logf(l) - kProbShift<DT> * kLn2);
 }
 
 // Rows the matrix-core kernel can load: whole, aligned 16-byte units.
@@ -811,7 +834,7 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   // cutting evens them out (256 requests up to 512 keys, spread over the logarithm: 35 us
   // cut, 50 whole; all alike: 91 and 87).
   const int64_t resident = chip_blocks(device_cus(), DP, p.width);
-  const bool many = units * a.B >= kWaves * resident;
+  const bool many = units * a.B >= 2 * resident;
   const bool cut = most > 512 || (many && most > 8 * Shape<DT, DP>::keys);
   if (cut) {
     // Where there are steps enough for every wave of the chip, a block's waves take
@@ -853,7 +876,10 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   kernel<<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !cut) return e;
-  attn_join_kernel<DT><<<(unsigned)(a.B * a.Hq), kJoin, 0, s>>>(a, p);
+  // Many rows: most were not cut or have few parts, and a wave is enough for one.
+  const int64_t rows = a.B * a.Hq;
+  if (rows >= 8 * device_cus()) attn_join_kernel<DT, 4><<<(unsigned)((rows + 3) / 4), kJoin, 0, s>>>(a, p);
+  else attn_join_kernel<DT, 1><<<(unsigned)rows, kJoin, 0, s>>>(a, p);
   return hipGetLastError();
 }
 

@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kOwnScan = 2048;
-constexpr int kRun = 256;                     // entries or tokens a wave takes at a time
+constexpr int kRun = 256, kTokens = 64;       // entries and tokens a wave takes at a time
 
 struct Geometry {
   FastDiv page;
@@ -44,7 +44,7 @@ __device__ __forceinline__ Need need_of(const TablesArgs& a, const Geometry& g, 
   return n;
 }
 
-// Running sums of up to kOwnScan requests from b0 on, on top of `base`:
+// Running sums of up to `room` requests from b0 on, on top of `base`, in LDS:
 // cu_t[i], cu_p[i] = sums before request b0 + i. 32-bit sums that stay at 2^32 - 1 once they
 // get there (such an addition is associative) and are stored as at most 2^31 - 1.
 struct Sums {
@@ -64,19 +64,22 @@ __device__ __forceinline__ Sums wave_scan(Sums v) {       // inclusive
   }
   return v;
 }
+// kN threads, of which thread i sums requests b0 + i n .. b0 + (i + 1) n - 1.
+template <int kN>
 __device__ __forceinline__ Sums scan_requests(const TablesArgs& a, const Geometry& g, int64_t b0,
-                                              Sums base, int32_t* cu_t, int32_t* cu_p) {
-  __shared__ Sums tot[kWaves];
-  // thread i sums requests b0 + i n .. b0 + (i + 1) n - 1
-  const int count = (int)min((int64_t)kOwnScan, a.B - b0);
-  const int n = (count + kThreads - 1) / kThreads, first = threadIdx.x * n;
-  const int past = min(first + n, count);
-  Sums mine{0, 0};
-  for (int i = first; i < past; ++i) {
+                                              Sums base, int room, int32_t* cu_t, int32_t* cu_p) {
+  __shared__ Sums tot[kN / 64];
+  const int count = (int)min((int64_t)room, a.B - b0);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < count; i += kN) {
     const Need r = need_of(a, g, b0 + i);
     cu_t[i] = r.fresh, cu_p[i] = r.need - r.held;
-    mine = mine + Sums{(uint32_t)r.fresh, (uint32_t)(r.need - r.held)};
   }
+  __syncthreads();
+  const int n = (count + kN - 1) / kN, first = min((int)threadIdx.x * n, count);
+  const int past = min(first + n, count);
+  Sums mine{0, 0};
+  for (int i = first; i < past; ++i) mine = mine + Sums{(uint32_t)cu_t[i], (uint32_t)cu_p[i]};
   const Sums incl = wave_scan(mine);
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
   if (lane == 63) tot[w] = incl;
@@ -85,7 +88,7 @@ __device__ __forceinline__ Sums scan_requests(const TablesArgs& a, const Geometr
   __syncthreads();
   Sums at = base, end = base;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
+  for (int i = 0; i < kN / 64; ++i) {
     if (i < w) at = at + tot[i];
     end = end + tot[i];
   }
@@ -99,11 +102,39 @@ __device__ __forceinline__ Sums scan_requests(const TablesArgs& a, const Geometr
   return end;
 }
 
-// The last request in [lo, hi) whose sum before it is <= t; cu[lo] <= t.
-__device__ __forceinline__ int64_t request_of(const int32_t* cu, int64_t lo, int64_t hi, int64_t t) {
+// The last request whose sum before it is <= t, found by the whole wave: 64 probes at a
+// time, so that 4096 requests take two dependent reads.
+__device__ __forceinline__ int64_t request_of(const int32_t* cu, int64_t B, int64_t t) {
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, hi = B;                       // cu[lo] <= t, and cu[hi] > t or hi == B
   while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (cu[mid] <= t) lo = mid; else hi = mid;
+    const int64_t step = (hi - lo + 63) / 64, at = lo + (lane + 1) * step;
+    const int below = __popcll(__ballot(at < hi && cu[at] <= t));
+    lo += below * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// The same for each lane's own t, where request b is lane 0's and t does not fall from
+// lane to lane: among the next 64 requests by their sums in registers, else by halving.
+__device__ __forceinline__ int64_t lane_request_of(const int32_t* cu, int64_t B, int64_t b,
+                                                   int64_t t) {
+  const int lane = threadIdx.x & 63;
+  const int32_t c = b + lane < B ? cu[b + lane] : 0x7FFFFFFF;
+  const int32_t past = b + 64 < B ? cu[b + 64] : 0x7FFFFFFF;
+  int i = 0;                                  // the last of the 64 that is <= t
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    if (__shfl(c, i + off, 64) <= t) i += off;
+  }
+  int64_t lo = b + i;
+  if (b + 64 < B && past <= t) {
+    lo = b + 64;
+    for (int64_t hi = B; hi - lo > 1;) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (cu[mid] <= t) lo = mid; else hi = mid;
+    }
   }
   return lo;
 }
@@ -117,21 +148,28 @@ __device__ __forceinline__ int32_t entry_of(const TablesArgs& a, int64_t b, cons
   return f < a.n_free ? a.free_pages[f] : -1;
 }
 
-__global__ __launch_bounds__(kThreads) void tables_scan_kernel(TablesArgs a, Geometry g) {
+constexpr int kScanThreads = 1024, kScanRoom = 4096;
+
+__global__ __launch_bounds__(kScanThreads) void tables_scan_kernel(TablesArgs a, Geometry g) {
+  __shared__ int32_t lds_t[kScanRoom], lds_p[kScanRoom];
   Sums base{0, 0};
-  for (int64_t b0 = 0; b0 < a.B; b0 += kOwnScan)
-    base = scan_requests(a, g, b0, base, a.cu_tokens + b0, a.cu_pages + b0);
+  for (int64_t b0 = 0; b0 < a.B; b0 += kScanRoom) {
+    base = scan_requests<kScanThreads>(a, g, b0, base, kScanRoom, lds_t, lds_p);
+    for (int i = threadIdx.x; i < kScanRoom && b0 + i < a.B; i += kScanThreads)
+      a.cu_tokens[b0 + i] = lds_t[i], a.cu_pages[b0 + i] = lds_p[i];
+    __syncthreads();
+  }
   if (threadIdx.x == 0) a.cu_tokens[a.B] = stored(base.t), a.cu_pages[a.B] = stored(base.p);
 }
 
-// A wave takes kRun entries of one row, or kRun tokens, at a time.
+// A wave takes kRun entries of one row, or kTokens tokens, at a time.
 template <bool OWN>
 __global__ __launch_bounds__(kThreads) void tables_fill_kernel(TablesArgs a, Geometry g) {
   __shared__ int32_t lds_t[OWN ? kOwnScan : 1], lds_p[OWN ? kOwnScan : 1];
   const int32_t *cu_t = a.cu_tokens, *cu_p = a.cu_pages;
   int32_t total;
   if (OWN) {
-    const Sums end = scan_requests(a, g, 0, Sums{0, 0}, lds_t, lds_p);
+    const Sums end = scan_requests<kThreads>(a, g, 0, Sums{0, 0}, kOwnScan, lds_t, lds_p);
     cu_t = lds_t, cu_p = lds_p;
     total = stored(end.t);
     if (blockIdx.x == 0) {
@@ -156,28 +194,21 @@ __global__ __launch_bounds__(kThreads) void tables_fill_kernel(TablesArgs a, Geo
       }
       continue;
     }
-    // the run's first and last request once, each token's between them
-    const int64_t t0 = it * kRun, t1 = min(t0 + kRun, (int64_t)total);
-    int64_t b0 = 0, b1 = 1;
-    if (t0 < t1) {
-      b0 = request_of(cu_t, 0, a.B, t0);
-      b1 = request_of(cu_t, b0, a.B, t1 - 1) + 1;
-    }
-#pragma unroll
-    for (int k = 0; k < kRun / 64; ++k) {
-      const int64_t t = t0 + k * 64 + lane;
-      if (t >= a.tokens) continue;
-      int32_t slot = -1, pos = 0;
+    const int64_t t0 = it * kTokens, t = t0 + lane;
+    int32_t slot = -1, pos = 0;
+    if (t0 < total) {                         // the same for the wave
+      const int64_t b = lane_request_of(cu_t, a.B, request_of(cu_t, a.B, t0), min(t, (int64_t)total - 1));
+      const Need n = need_of(a, g, b);
       if (t < total) {
-        const int64_t lo = request_of(cu_t, b0, b1, t);
-        const Need n = need_of(a, g, lo);
-        pos = to_i32((int64_t)n.old + (t - cu_t[lo]));
+        pos = to_i32((int64_t)n.old + (t - cu_t[b]));
         const int32_t j = (int32_t)div_by(pos, g.page);
         if (j < n.need) {
-          const int32_t pg = entry_of(a, lo, n, cu_p[lo], j);
+          const int32_t pg = entry_of(a, b, n, cu_p[b], j);
           if (pg >= 0) slot = to_i32((int64_t)pg * a.page + (pos - j * (int32_t)a.page));
         }
       }
+    }
+    if (t < a.tokens) {
       a.slots[t] = slot;
       a.positions[t] = pos;
     }
@@ -191,7 +222,7 @@ hipError_t launch_page_tables(const TablesArgs& a, hipStream_t s) {
   g.page = fast_div((uint32_t)a.page);
   const int64_t cap = a.page * a.width;
   g.cap = (int32_t)(cap < 0x7FFFFFFF ? cap : 0x7FFFFFFF);
-  g.token_items = (int32_t)((a.tokens + kRun - 1) / kRun);
+  g.token_items = (int32_t)((a.tokens + kTokens - 1) / kTokens);
   g.row_items = (a.width + kRun - 1) / kRun;
   g.items = g.token_items + a.B * g.row_items;
   const int64_t need = (g.items + kWaves - 1) / kWaves, most = (int64_t)device_cus() * 4;
@@ -200,7 +231,7 @@ hipError_t launch_page_tables(const TablesArgs& a, hipStream_t s) {
     tables_fill_kernel<true><<<blocks, kThreads, 0, s>>>(a, g);
     return hipGetLastError();
   }
-  tables_scan_kernel<<<1, kThreads, 0, s>>>(a, g);
+  tables_scan_kernel<<<1, kScanThreads, 0, s>>>(a, g);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   tables_fill_kernel<false><<<blocks, kThreads, 0, s>>>(a, g);
