@@ -198,7 +198,7 @@ template <int DT, int DP> struct Shape {
   static constexpr int keys = 16 * tiles;                   // keys per wave and step
   static constexpr int unit = DT == FK_F32 ? 4 : 8;         // elements in 16 bytes
   static constexpr int nc = DP / (4 * unit);                // 16-byte key loads per row and lane
-  static constexpr int ve = DP / 16 < unit ? DP / 16 : unit;    // elements per value load
+  static constexpr int ve = DP == 192 ? 4 : (DP / 16 < unit ? DP / 16 : unit);   // elements per value load
   static constexpr int nu = DP / (16 * ve);                 // value loads per row and lane
   static constexpr int rows = 4 * tiles;                    // value rows per lane
   static constexpr int ldo = DP + 4;                        // LDS row of merged results
@@ -623,7 +623,7 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const float* x) {
 // holds blocks at once.
 constexpr int waves_per_simd(int64_t D, int64_t width) {
   const bool two = width > kHeadTile;
-  return D <= 32 ? 3 : (D <= 64 ? (two ? 2 : 3) : (D <= 128 ? 2 : 1));
+  return D <= 64 ? (D > 32 && two ? 2 : 3) : (D <= 128 ? 2 : 1);
 }
 constexpr int kMaxParts = kMaxCus * 3;
 
@@ -896,6 +896,7 @@ hipError_t run(const AttnArgs& a, void* ws, hipStream_t s) {
   return D <= 32    ? run_mfma<DT, 32, 1>(a, ws, s)
          : D <= 64  ? run_mfma<DT, 64, 1>(a, ws, s)
          : D <= 128 ? run_mfma<DT, 128, 1>(a, ws, s)
+         : D <= 192 ? run_mfma<DT, 192, 1>(a, ws, s)
                     : run_mfma<DT, 256, 1>(a, ws, s);
 }
 
