@@ -543,7 +543,7 @@ struct Start {
   int64_t lo, hi;            // this part's range of costs
   int64_t b, before;         // request that holds lo, cost of those before it
   __device__ __forceinline__ void cut(int64_t total, const Plan& p, int w) {
-    const int64_t most = total / (2 * p.team);     // less is not worth a part of its own
+    const int64_t most = total / p.team;           // a part is a step of each wave at least
     const int64_t parts = most < 1 ? 1 : (most < p.parts ? most : p.parts);
     lo = w < parts ? total * w / parts : total;
     hi = w < parts ? total * (w + 1) / parts : total;
