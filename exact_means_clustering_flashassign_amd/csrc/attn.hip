@@ -129,7 +129,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn_any_join_kernel(AttnArgs a, 
   const float* ml = pml + bh * parts * 2;
   float top = -INFINITY, total = 0.f;
   for (int i = 0; i < parts; ++i) top = fmaxf(top, ml[2 * i]);
-  for (int i = 0; i < parts; ++i) total = fmaf(join_factor(ml[2 * i], ml[2 * i + 1], top), ml[2 * i + 1], total);
+  for (int i = 0; i < parts; ++i)
+    total = fmaf(join_factor(ml[2 * i], ml[2 * i + 1], top), ml[2 * i + 1], total);
   const bool any = total != 0.f;
   for (int e = threadIdx.x; e < D; e += kWaves * 64) {
     float t = 0.f;
@@ -190,6 +191,14 @@ int64_t longest(const AttnArgs& a) {
 // lane that computed them, and the lane loads rows 4g + j of V itself, elements
 // VE m .. VE m + VE - 1 (16 lanes cover a row), picking tile t's element of
 // each row with byte permutes. Nothing goes through LDS but row addresses.
+//
+// A wave's step is 32 keys (fp32: 16). The next step's keys are asked for as soon as the
+// scores are out of the registers they sit in, the next values after the last product with
+// these, so that one of the two is always on its way without a second set of
+// registers; 8 to 12 waves a CU keep 128 KB and more in flight. A step of 16 KB costs about
+// 254 VALU and 24 matrix instructions, an eighth of the time its bytes take.
+// Measured: 32 requests of 2048 to 65536 keys, 8 heads of 128 bf16, 4.43 GB, 671 us or 6.6
+// TB/s (a large copy reads and writes 4.8 on the same card).
 constexpr int kHeadTile = 16;
 constexpr int kMaxCus = 256;
 
@@ -219,7 +228,9 @@ __device__ __forceinline__ uint4 load16(uint64_t addr) {
 }
 
 // A load of n = 16, 8 or 4 bytes into the first words. STREAM: bytes that no one else
-// reads are marked so and do not push out of L2 what others will read again.
+// reads are marked so and do not push out of L2 what others will read again (the 4.43 GB
+// above 815 -> 779 us); where waves share lines the mark makes them come twice (8 x 32768
+// keys, 8 heads of 80: 200 us marked, 137 plain).
 template <int n, bool STREAM> __device__ __forceinline__ uint4 load_row(uint64_t addr) {
   if constexpr (n == 16) {
     return __builtin_bit_cast(uint4, STREAM ? __builtin_nontemporal_load((gptr16)addr) : *(gptr16)addr);
@@ -234,14 +245,14 @@ template <int n, bool STREAM> __device__ __forceinline__ uint4 load_row(uint64_t
 // Keys that do not count are read from here: zeros, whatever the cache holds.
 __device__ const uint4 zero_row[64] = {};
 
-// How the work is shared. Request b costs its steps of `keys` keys plus
-// one step of each of its waves (queries, first loads, joining, storing). The
-// requests' costs are laid end to end and cut into equal parts, one per block of
-// a cache head, so that a batch of any lengths fills the chip evenly. A request
-// inside one part is finished there; one that is cut leaves a partial
-// result per part, at most two a block (one that started before, one that goes
-// on), joined by attn_join_kernel.
-
+// How the work is shared. Request b costs its steps plus one step of each wave of its
+// team (queries, first loads, joining, storing). The requests' costs are laid end to
+// end and cut into equal parts, as many as the chip holds teams for each head, so that a
+// batch of any lengths fills the chip evenly. A request inside one part is finished
+// there; one that is cut leaves a partial result per part, at most two a part (one that
+// started before, one that goes on), joined by attn_join_kernel. A larger share for a
+// request's start was slower (one step 54.6, two 55.7, four 57.7 us for 32 requests
+// of 0 to 16384 keys spread over the logarithm, 8 heads of 128).
 struct Plan {
   int parts;            // blocks per (cache head, head tile); 0: a team per request
   int team;             // waves that share a request's steps: 4, 2 or 1
@@ -558,10 +569,11 @@ __device__ __forceinline__ int64_t cost_of(const AttnArgs& a, const Plan& p, int
 template <int KEYS>
 __device__ __forceinline__ Start find_start(const AttnArgs& a, const Plan& p, int w) {
   Start st;
-  if (a.B <= 64) {
-    // a request a lane: every wave by itself, without barriers
+  if (a.B <= 64 && a.width * a.cache.page <= (1 << 29)) {
+    // a request a lane, every wave by itself, without barriers; 64 costs of at most
+    // 2^29 / 16 + 4 fit 32 bits
     const int lane = threadIdx.x & 63;
-    const uint32_t mine = lane < a.B ? (uint32_t)cost_of<KEYS>(a, p, lane) : 0;   // < 2^26 each
+    const uint32_t mine = lane < a.B ? (uint32_t)cost_of<KEYS>(a, p, lane) : 0;
     uint32_t incl = mine;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -722,7 +734,9 @@ __global__ __launch_bounds__(kWaves * 64, waves_per_simd(DP, HT * kHeadTile)) vo
 constexpr int kJoin = 256;        // threads of a joining block
 
 // Joins the partial results of a request that was cut: slot 1 of its first part,
-// slot 0 of the others. R (request, query head) rows a block: one, or one a wave.
+// slot 0 of the others. R (request, query head) rows a block: one, or one a wave. Bound by
+// latency: the two parts' numbers, their sums, then the rows, 4 to 9 us; more threads a row or
+// more blocks a row did not change it.
 template <int DT, int R>
 __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Plan p) {
   constexpr int threads = kJoin / R;
@@ -801,7 +815,8 @@ bool aligned16(const AttnArgs& a, int eb) {
 }
 
 // Query heads a wave serves at once: 32 where there are more than 16 and the registers
-// hold both tiles (16-bit rows of at most 128).
+// hold both tiles (16-bit rows of at most 128; 8 requests of 32768 keys, 8 heads of 64 with
+// 32 query heads each: 106 us, 5.1 TB/s).
 int64_t tile_width(int dt, int64_t D, int64_t G) {
   return G > kHeadTile && dt != FK_F32 && D <= 128 ? 2 * kHeadTile : kHeadTile;
 }
@@ -839,9 +854,9 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   if (cut) {
     // Where there are steps enough for every wave of the chip, a block's waves take
     // neighbouring heads, whose rows lie side by side in the cache, instead of one
-    // head's steps in turn: the block reads 4 rows' length in one piece (long_b32: 774 us
-    // with 1 head a block, 697 with 2, 670 with 4). With fewer steps the waves share them
-    // and join in LDS, not through memory.
+    // head's steps in turn: the block reads 4 rows' length in one piece (the 4.43 GB
+    // above: 774 us with 1 head a block, 697 with 2, 670 with 4). With fewer steps the
+    // waves share them and join in LDS, not through memory.
     const double steps = (double)units * a.B * ((most + Shape<DT, DP>::keys - 1) / Shape<DT, DP>::keys);
     p.team = steps >= 4.0 * kWaves * resident ? team_of(units) : kWaves;
     const int64_t groups = units * p.team / kWaves;       // blocks that make one part
@@ -865,7 +880,8 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   // Caches that the 256 MB last-level cache may still hold from the step before are read
   // without the mark (4 requests of 512 keys: 10.4 us, marked 13.3).
   const double bytes = 2.0 * a.B * most * a.cache.heads * DP * Val<DT>::bytes;
-  const bool exact = bytes >= (double)(128 << 20) && a.cache.dim == DP && p.tiles == 1 && DP * Val<DT>::bytes % 128 == 0 &&
+  const bool exact = bytes >= (double)(128 << 20) && a.cache.dim == DP && p.tiles == 1 &&
+                     DP * Val<DT>::bytes % 128 == 0 &&
                      aligned((uintptr_t)a.cache.k, a.cache.k_stride) &&
                      aligned((uintptr_t)a.cache.v, a.cache.v_stride);
   const bool extra = a.softcap > 0.f || a.cache.key_bias;

@@ -344,8 +344,11 @@ fk_status_t fk_qk_norm_rope(const void* q, const int64_t q_stride[2], const void
  *             is split; a longer request is still computed in full.
  *   out (B,Hq,D) dt out; lse (B,Hq) fp32 out, may be null.
  *   ws: fk_workspace_size_attn(dt, B, Hq, Hkv, D) bytes, 256-byte aligned.
- * D <= 1024 (FK_ERR_UNSUPPORTED above). Same results on every run with the
- * same arguments.
+ * D <= 1024 (FK_ERR_UNSUPPORTED above). Rows of at most 256 elements that
+ * start at multiples of 16 bytes and hold whole 16-byte units run on the
+ * matrix cores, others on a path several times slower. The same arguments give
+ * the same bits on every run; another batch around a request, or another
+ * max_len, may change its last bits (where its keys are split).
  */
 fk_status_t fk_paged_attn(const void* q, const int64_t q_stride[2], fk_dtype_t dt, int64_t B,
                           int64_t Hq, const fk_kv_cache_t* cache, const int32_t* table,
