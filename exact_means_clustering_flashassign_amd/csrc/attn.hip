@@ -14,6 +14,7 @@ constexpr int kWaves = 4;
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2eRest = 1.92596299112661746887e-8f;    // log2 e - kLog2e
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // cap * tanh(s / cap) to a few units in the last place of its own size (scores of a few
@@ -301,6 +302,16 @@ template <> struct Mfma16<FK_F32> {
 // still a subnormal fp16 and a long tail of small ones is not lost.
 template <int DT> constexpr float kProbShift = DT == FK_F16 ? 14.f : 0.f;
 
+// e^x (x <= 0), scaled. 16-bit caches: x log2 e is rounded once, |x| 2^-24 of the result, less
+// than a probability's own rounding. fp32: the whole part is taken off before that
+// rounding, and the constant's own rest added.
+template <int DT> __device__ __forceinline__ float prob(float x) {
+  if constexpr (DT != FK_F32) return fast_exp2(fmaf(x, kLog2e, kProbShift<DT>));
+  const float n = rintf(fmaxf(x, -200.f) * kLog2e);
+  const float f = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -n));
+  return x < -200.f ? 0.f : __builtin_amdgcn_ldexpf(fast_exp2(f), (int)n);
+}
+
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }
@@ -441,11 +452,16 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
     for (int h = 0; h < HT; ++h)
 #pragma unroll
       for (int u = 0; u < S::tiles; ++u) {
-        floatx4_t x = {0.f, 0.f, 0.f, 0.f};
+        // fp32: four sums, a quarter of the rounding steps each, as the products are not exact
+        constexpr int sums = DT == FK_F32 && S::nc >= 4 ? 4 : 1;
+        floatx4_t x[sums];
 #pragma unroll
-        for (int i = 0; i < S::nc; ++i) x = Mfma16<DT>::run(kf[u][i], q[h][i], x);
+        for (int i = 0; i < sums; ++i) x[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[h][u][i] = x[i];
+        for (int i = 0; i < S::nc; ++i) x[i % sums] = Mfma16<DT>::run(kf[u][i], q[h][i], x[i % sums]);
+        if constexpr (sums == 4) x[0] = (x[0] + x[1]) + (x[2] + x[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[h][u][i] = x[0][i];
       }
     load_k(next);
     __builtin_amdgcn_sched_barrier(0);   // the next keys are on their way before the softmax
@@ -478,7 +494,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
       for (int u = 0; u < S::tiles; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[h][u][i] = fast_exp2(fmaf(s[h][u][i] - ref, kLog2e, kProbShift<DT>));
+          s[h][u][i] = prob<DT>(s[h][u][i] - ref);
           part += s[h][u][i];
         }
       acc.l[h] = fmaf(acc.l[h], alpha, part);
