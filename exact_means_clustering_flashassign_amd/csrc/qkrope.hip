@@ -85,7 +85,7 @@ __global__ __launch_bounds__(kWaves * 64) void rope_any_kernel(RopeArgs a, int64
 }
 
 // ---------------------------------------------------------------------------
-// Rows in whole VE-element units (16, 8 or 4 bytes)
+// Rows in whole VE-element units (16 or 8 bytes)
 // ---------------------------------------------------------------------------
 // Memory-bound: each element is read and written once. A lane holds two units of
 // a row, for pairs (i, i + rot/2) the two halves of VE pairs, so a pair is never
@@ -102,18 +102,24 @@ struct RopePlan {
   FastDiv page, per;         // tokens a page, rows a token
 };
 
+enum { kApart, kSideBySide, kExchange };
+
 template <int DT, int VE> struct Unit {
   typedef typename Val<DT>::arith T;
   typedef T vec __attribute__((ext_vector_type(VE)));
 };
 
+// MODE: pairs are half the rotated part apart and that half is whole units, so that one
+// lane holds both of a pair; or pairs lie side by side; or neither, and the rotated
+// elements of a row are exchanged through LDS.
 // FLAT: rows of all tokens end to end, each lane with its own token. Takes the
 // tokens whose rows would leave lanes of their own wave idle.
-template <int DT, int VE, bool INTER, bool FLAT>
+template <int DT, int VE, int MODE, bool FLAT>
 __global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopePlan p,
                                                                int64_t waves) {
   typedef typename Unit<DT, VE>::T T;
   typedef typename Unit<DT, VE>::vec V;
+  __shared__ float xch[MODE == kExchange ? kWaves : 1][MODE == kExchange ? 64 * 2 * VE : 1];
   const int lane = threadIdx.x & 63;
   const int64_t wave =
       (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -163,20 +169,29 @@ __global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopeP
   };
   Row next = load(pass0);      // on its way before anything is waited for
 
+  // element i of a then b rotates with its own cosine and sine (kExchange), else pair i
   const int half = (int)(a.rot >> 1);
-  float cs[VE] = {}, sn[VE] = {};
-  bool on[VE];               // pair i of this lane rotates
+  constexpr int turns = MODE == kExchange ? 2 * VE : VE;
+  float cs[turns] = {}, sn[turns] = {};
+  bool on[turns];
 #pragma unroll
-  for (int i = 0; i < VE; ++i) on[i] = !INTER && turn;
+  for (int i = 0; i < turns; ++i) on[i] = MODE == kApart && turn;
   if (half) {
     const int64_t pos = clamp_pos(a.positions[t], a.max_pos);
     const float* row = a.rope + pos * a.rot;
-    if (INTER) {
+    if constexpr (MODE == kSideBySide) {
 #pragma unroll
       for (int i = 0; i < VE; ++i) {         // first the pairs of unit a, then those of b
         const int pr = (i < VE / 2 ? ea / 2 + i : eb / 2 + i - VE / 2);
         on[i] = (i < VE / 2 ? va : vb) && pr < half;
         if (on[i]) cs[i] = row[pr], sn[i] = row[half + pr];
+      }
+    } else if constexpr (MODE == kExchange) {
+#pragma unroll
+      for (int i = 0; i < 2 * VE; ++i) {
+        const int el = i < VE ? ea + i : eb + i - VE, pr = el < half ? el : el - half;
+        on[i] = (i < VE ? va : vb) && el < 2 * half;
+        if (on[i]) cs[i] = row[pr], sn[i] = el < half ? -row[half + pr] : row[half + pr];
       }
     } else if (turn) {
 #pragma unroll
@@ -219,14 +234,30 @@ __global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopeP
 #pragma unroll
       for (int i = 0; i < VE; ++i) fa[i] = fa[i] * r * (float)wa[i], fb[i] = fb[i] * r * (float)wb[i];
     }
+    if constexpr (MODE == kExchange) {
+      float* mine = xch[threadIdx.x >> 6] + sub * 2 * VE * p.L;
+      // (only this wave's lanes read it: the compiler's order is enough)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      // pair i: elements 2i, 2i+1 of a then b, or element i of both
-      float* e0 = !INTER ? &fa[i] : (i < VE / 2 ? &fa[2 * i] : &fb[2 * i - VE]);
-      float* e1 = !INTER ? &fb[i] : e0 + 1;
-      const float u = *e0, w = *e1;
-      *e0 = on[i] ? u * cs[i] - w * sn[i] : u;
-      *e1 = on[i] ? w * cs[i] + u * sn[i] : w;
+      for (int i = 0; i < 2 * VE; ++i)
+        if (on[i]) mine[i < VE ? ea + i : eb + i - VE] = i < VE ? fa[i] : fb[i - VE];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int i = 0; i < 2 * VE; ++i) {
+        const int el = i < VE ? ea + i : eb + i - VE;
+        float& f = i < VE ? fa[i] : fb[i - VE];
+        if (on[i]) f = f * cs[i] + mine[el < half ? el + half : el - half] * sn[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        // pair i: elements 2i, 2i+1 of a then b, or element i of both
+        float* e0 = MODE == kApart ? &fa[i] : (i < VE / 2 ? &fa[2 * i] : &fb[2 * i - VE]);
+        float* e1 = MODE == kApart ? &fb[i] : e0 + 1;
+        const float u = *e0, w = *e1;
+        *e0 = on[i] ? u * cs[i] - w * sn[i] : u;
+        *e1 = on[i] ? w * cs[i] + u * sn[i] : w;
+      }
     }
     if (x.kind == 3) continue;
     V ya, yb;
@@ -255,8 +286,7 @@ __global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopeP
   }
 }
 
-// Whether every row starts at a multiple of `bytes` and holds whole units of it,
-// with rotated pairs either side by side or whole units apart.
+// Whether every row starts at a multiple of `bytes` and holds whole units of it.
 bool in_units(const RopeArgs& a, int eb, int bytes) {
   const fk_kv_cache_t& c = a.cache;
   int64_t s = a.D | a.q_stride[0] | a.q_stride[1] | a.k_stride[0] | a.k_stride[1];
@@ -267,15 +297,14 @@ bool in_units(const RopeArgs& a, int eb, int bytes) {
     for (int i = 0; i < 3; ++i) s |= c.k_stride[i] | c.v_stride[i];
     p |= (uintptr_t)a.v | (uintptr_t)c.k | (uintptr_t)c.v;
   }
-  if (!a.interleaved) s |= a.rot / 2;
   return s * eb % bytes == 0 && p % bytes == 0;     // powers of two: a bit below shows in the or
 }
 
-template <int DT, int VE>
-hipError_t run_vec(const RopeArgs& a, hipStream_t s) {
+template <int DT, int VE, int MODE>
+hipError_t run_mode(const RopeArgs& a, hipStream_t s) {
   RopePlan p{};
   p.units = (int)(a.D / VE);
-  p.hp = a.interleaved ? 0 : (int)(a.rot / 2 / VE);
+  p.hp = MODE == kApart ? (int)(a.rot / 2 / VE) : 0;
   p.rem = (p.units - 2 * p.hp + 1) / 2;
   p.L = 1;
   while (p.L < p.hp + p.rem) p.L *= 2;
@@ -299,11 +328,15 @@ hipError_t run_vec(const RopeArgs& a, hipStream_t s) {
   const int64_t blocks = (waves + kWaves - 1) / kWaves;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   const auto kernel =
-      a.interleaved
-          ? (flat ? rope_vec_kernel<DT, VE, true, true> : rope_vec_kernel<DT, VE, true, false>)
-          : (flat ? rope_vec_kernel<DT, VE, false, true> : rope_vec_kernel<DT, VE, false, false>);
+      flat ? rope_vec_kernel<DT, VE, MODE, true> : rope_vec_kernel<DT, VE, MODE, false>;
   kernel<<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, p, waves);
   return hipGetLastError();
+}
+
+template <int DT, int VE>
+hipError_t run_vec(const RopeArgs& a, hipStream_t s) {
+  if (a.interleaved) return run_mode<DT, VE, kSideBySide>(a, s);
+  return a.rot / 2 % VE ? run_mode<DT, VE, kExchange>(a, s) : run_mode<DT, VE, kApart>(a, s);
 }
 
 }  // namespace
@@ -311,19 +344,18 @@ hipError_t run_vec(const RopeArgs& a, hipStream_t s) {
 hipError_t launch_qk_norm_rope(const RopeArgs& a, int dt, hipStream_t s) {
   const int64_t rows = a.T * (a.Hq + a.Hkv * (a.cache.k ? 2 : 1));
   if (rows == 0) return hipSuccess;
-  // The widest units that the rows, and half the rotated part, are whole numbers of;
-  // 64 lanes of two units are the longest row.
+  // 64 lanes of two units are the longest row
   if (dt == FK_F32) {
     if (a.D <= 512 && in_units(a, 4, 16)) return run_vec<FK_F32, 4>(a, s);
-    if (a.D <= 256 && in_units(a, 4, 8)) return run_vec<FK_F32, 2>(a, s);
   } else {
     const bool f16 = dt == FK_F16;
-    if (a.D <= 1024 && in_units(a, 2, 16))
+    // A half of whole 8-byte units takes those rather than an exchange (20000 tokens of 24
+    // heads of 128, 72 rotated: 61 us, exchanged 93; with a half of 6 the exchange is left, 74).
+    const bool narrow = !a.interleaved && a.rot / 2 % 8 == 4 && a.D <= 512;
+    if (a.D <= 1024 && !narrow && in_units(a, 2, 16))
       return f16 ? run_vec<FK_F16, 8>(a, s) : run_vec<FK_BF16, 8>(a, s);
     if (a.D <= 512 && in_units(a, 2, 8))
       return f16 ? run_vec<FK_F16, 4>(a, s) : run_vec<FK_BF16, 4>(a, s);
-    if (a.D <= 256 && in_units(a, 2, 4))
-      return f16 ? run_vec<FK_F16, 2>(a, s) : run_vec<FK_BF16, 2>(a, s);
   }
   const int64_t blocks = (rows + kWaves - 1) / kWaves;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
