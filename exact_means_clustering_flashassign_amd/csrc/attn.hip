@@ -214,6 +214,13 @@ template <int DT, int DP> struct Shape {
   static constexpr int ldo = DP + 4;                        // LDS row of merged results
 };
 
+// A value that is the same in every lane, moved to scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 // Loads by address: the address space is stated, so that they are global loads
 // and not generic ones, which the LDS counter would wait for too.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -256,7 +263,7 @@ __device__ const uint4 zero_row[64] = {};
 // of 0 to 16384 keys spread over the logarithm, 8 heads of 128).
 struct Plan {
   int parts;            // blocks per (cache head, head tile); 0: a team per request
-  int team;             // waves that share a request's steps: 4, 2 or 1
+  int team;             // waves that share a request's steps: 8, 4, 2 or 1
   int heads, tiles;     // cache heads, head tiles per cache head
   int G, width, hr;     // query heads per cache head, per head tile, and per tile at most
   FastDiv page;
@@ -649,39 +656,44 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const float* x) {
 
 // Waves a SIMD holds (by their registers). The parts of a call are as many as the chip
 // holds blocks at once.
-constexpr int waves_per_simd(int64_t D, int64_t width) {
-  const bool two = width > kHeadTile;
-  return D <= 64 ? (D > 32 && two ? 2 : 3) : (D <= 128 ? 2 : 1);
+constexpr int waves_per_simd(int64_t D) {
+  return D <= 32 ? 4 : (D <= 64 ? 3 : (D <= 128 ? 2 : 1));
 }
-constexpr int kMaxParts = kMaxCus * 3;
+constexpr int kMaxParts = kMaxCus * 4;
 
-template <int DT, int DP, int HT, bool EXTRA, bool EXACT>
-__global__ __launch_bounds__(kWaves * 64, waves_per_simd(DP, HT * kHeadTile)) void attn_mfma_kernel(AttnArgs a, Plan p) {
+template <int DT, int DP, int HT, bool EXTRA, bool EXACT, int W>
+__global__ __launch_bounds__(W * 64, W == kWaves ? waves_per_simd(DP) : W / 4) void attn_mfma_kernel(AttnArgs a, Plan p) {
   using S = Shape<DT, DP>;
-  __shared__ Rows<DT, DP> rows[kWaves][2];
-  __shared__ float so[kWaves][kHeadTile][S::ldo];
-  __shared__ float sm[kWaves][kHeadTile], sl[kWaves][kHeadTile];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
+  __shared__ Rows<DT, DP> rows[W][2];
+  __shared__ float so[W][kHeadTile][S::ldo];
+  __shared__ float sm[W][kHeadTile], sl[W][kHeadTile];
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Waves k0 .. k1 - 1 of this block are one team; its teams take neighbouring heads.
-  const int k0 = w / p.team * p.team, k1 = k0 + p.team, teams = kWaves / p.team;
+  const int k0 = w / p.team * p.team, k1 = k0 + p.team, teams = W / p.team;
   const int64_t unit = xcd_remap(blockIdx.x, gridDim.x) * teams + w / p.team;
   const int ht = (int)(unit % p.tiles), hk = (int)((unit / p.tiles) % p.heads);
   const int64_t part = unit / ((int64_t)p.tiles * p.heads);
   const int D = (int)a.cache.dim;
 
   Start st;
-  if (p.parts > 0) {
+  const bool cut = W == kWaves && p.parts > 0;
+  if (cut) {
+    // the same for the block: held in scalar registers through the steps, which
+    // have none to spare among the others
     st = find_start<S::keys>(a, p, (int)part);
+    st.lo = uniform(st.lo), st.hi = uniform(st.hi);
+    st.b = uniform(st.b), st.before = uniform(st.before);
     if (st.lo >= st.hi) return;
   } else {
     st.lo = 0, st.hi = 1, st.b = part, st.before = 0;
   }
-  const bool idle = p.parts == 0 && part >= a.B;     // a wave past the last request
+  const bool idle = !cut && part >= a.B;     // a wave past the last request
   for (int64_t b = st.b, at = st.before; at < st.hi;) {
-    const int len = idle ? 0 : len_of(a, b);
+    const int len = idle ? 0 : __builtin_amdgcn_readfirstlane(len_of(a, b));
     const int steps = (len + S::keys - 1) / S::keys;
     int t0 = 0, t1 = steps;
-    if (p.parts > 0) {
+    if (cut) {
       const int64_t first = at + p.team;
       t0 = (int)max((int64_t)0, min(st.lo - first, (int64_t)steps));
       t1 = (int)max((int64_t)0, min(st.hi - first, (int64_t)steps));
@@ -736,12 +748,12 @@ __global__ __launch_bounds__(kWaves * 64, waves_per_simd(DP, HT * kHeadTile)) vo
           }
         }
       }
-      if (p.parts > 0 && hk == 0 && ht == 0 && threadIdx.x == 0) {
+      if (cut && hk == 0 && ht == 0 && threadIdx.x == 0) {
         if (t0 == 0) p.cover[2 * b] = (int32_t)part;
         if (t1 == steps) p.cover[2 * b + 1] = (int32_t)part;
       }
     }
-    if (p.parts == 0) break;
+    if (!cut) break;
     at += p.team + steps;
     ++b;
   }
@@ -839,7 +851,7 @@ bool aligned16(const AttnArgs& a, int eb) {
 
 // Query heads a wave serves at once: 32 where there are more than 16 and the registers
 // hold both tiles (16-bit rows of at most 128; 8 requests of 32768 keys, 8 heads of 64 with
-// 32 query heads each: 106 us, 5.1 TB/s).
+// 32 query heads each: 109 us, 4.9 TB/s; 4 heads of 128: 107 us, 5.0).
 int64_t tile_width(int dt, int64_t D, int64_t G) {
   return G > kHeadTile && dt != FK_F32 && D <= 128 ? 2 * kHeadTile : kHeadTile;
 }
@@ -847,8 +859,8 @@ int64_t tile_width(int dt, int64_t D, int64_t G) {
 // Parts per (cache head, head tile): `blocks` shared out.
 int64_t parts_of(int64_t blocks, int64_t units) { return units >= blocks ? 1 : blocks / units; }
 
-int64_t chip_blocks(int64_t cus, int64_t D, int64_t width) {
-  return (cus < kMaxCus ? cus : kMaxCus) * waves_per_simd(D, width) * 4 / kWaves;
+int64_t chip_blocks(int64_t cus, int64_t D) {
+  return (cus < kMaxCus ? cus : kMaxCus) * waves_per_simd(D) * 4 / kWaves;
 }
 
 // Waves a head when requests are cut: the block's waves take as many neighbouring
@@ -871,9 +883,16 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   // many, whose lengths may differ: one wave each is best up to 8 steps, and beyond that
   // cutting evens them out (256 requests up to 512 keys, spread over the logarithm: 35 us
   // cut, 50 whole; all alike: 91 and 87).
-  const int64_t resident = chip_blocks(device_cus(), DP, p.width);
+  const int64_t resident = chip_blocks(device_cus(), DP);
   const bool many = units * a.B >= 2 * resident;
-  const bool cut = most > 512 || (many && most > 8 * Shape<DT, DP>::keys);
+  // Where every block has a CU to itself and half the CUs have one, 8 waves do up to 64 steps
+  // whole (6 requests of 607 keys, 32 heads of 64: 12.6 us, cut 20.9; 16 of 1500, 8 heads of
+  // 128: 23 and 27). With fewer blocks a CU's own rate is the bound, and more of them the
+  // remedy (4 of 2000, 8 heads: 26, cut 17).
+  const int64_t cus = device_cus(), rows = units * a.B;
+  const bool eight = DP <= 128 && most > 512 && most <= 64 * Shape<DT, DP>::keys &&
+                     rows <= cus && 2 * rows >= cus;
+  const bool cut = !eight && (most > 512 || (many && most > 8 * Shape<DT, DP>::keys));
   if (cut) {
     // Where there are steps enough for every wave of the chip, a block's waves take
     // neighbouring heads, whose rows lie side by side in the cache, instead of one
@@ -892,9 +911,10 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   } else {
     // One wave each where that alone fills the chip, or where a second wave would
     // find nothing to do (222 requests of 3 keys, 32 heads: 19 us, 40 with four waves).
-    p.team = many || most <= Shape<DT, DP>::keys ? 1 : kWaves;
+    p.team = eight ? 8 : (many || most <= Shape<DT, DP>::keys ? 1 : kWaves);
   }
-  const int64_t blocks = (units * (cut ? p.parts : a.B) * p.team + kWaves - 1) / kWaves;
+  const int W = eight ? 8 : kWaves;
+  const int64_t blocks = (units * (cut ? p.parts : a.B) * p.team + W - 1) / W;
   if (blocks > 0x7FFFFFFF || a.B * a.Hq > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   // EXACT: rows fill their lanes and whole 128-byte lines, and no other wave reads them.
   const auto aligned = [](uintptr_t base, const int64_t* s) {
@@ -908,25 +928,29 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
                      aligned((uintptr_t)a.cache.k, a.cache.k_stride) &&
                      aligned((uintptr_t)a.cache.v, a.cache.v_stride);
   const bool extra = a.softcap > 0.f || a.cache.key_bias;
-  const auto kernel = exact ? (extra ? attn_mfma_kernel<DT, DP, HT, true, true>
-                                     : attn_mfma_kernel<DT, DP, HT, false, true>)
-                            : (extra ? attn_mfma_kernel<DT, DP, HT, true, false>
-                                     : attn_mfma_kernel<DT, DP, HT, false, false>);
-  kernel<<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, p);
+  auto kernel = exact ? (extra ? attn_mfma_kernel<DT, DP, HT, true, true, kWaves>
+                               : attn_mfma_kernel<DT, DP, HT, false, true, kWaves>)
+                      : (extra ? attn_mfma_kernel<DT, DP, HT, true, false, kWaves>
+                               : attn_mfma_kernel<DT, DP, HT, false, false, kWaves>);
+  if constexpr (DP <= 128) {
+    if (eight)
+      kernel = extra ? attn_mfma_kernel<DT, DP, HT, true, false, 8>
+                     : attn_mfma_kernel<DT, DP, HT, false, false, 8>;
+  }
+  kernel<<<(unsigned)blocks, W * 64, 0, s>>>(a, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !cut) return e;
   // Many rows: most were not cut or have few parts, and a wave is enough for one.
-  const int64_t rows = a.B * a.Hq;
-  const int cus = device_cus();
-  if (rows >= 8 * cus) {
-    attn_join_kernel<DT, 4><<<(unsigned)((rows + 3) / 4), kJoin, 0, s>>>(a, p, 1);
+  const int64_t outs = a.B * a.Hq;
+  if (outs >= 8 * cus) {
+    attn_join_kernel<DT, 4><<<(unsigned)((outs + 3) / 4), kJoin, 0, s>>>(a, p, 1);
     return hipGetLastError();
   }
   // Few rows have many parts: as many blocks a row as there are CUs for, down to 64 bytes
   // of a partial result (one request of 131072 keys, 32 query heads: 95.9 -> 94.5 us).
   int slices = 1;
-  while (2 * slices * rows <= cus && a.cache.dim / (2 * slices) >= 16) slices *= 2;
-  attn_join_kernel<DT, 1><<<(unsigned)(rows * slices), kJoin, 0, s>>>(a, p, slices);
+  while (2 * slices * outs <= cus && a.cache.dim / (2 * slices) >= 16) slices *= 2;
+  attn_join_kernel<DT, 1><<<(unsigned)(outs * slices), kJoin, 0, s>>>(a, p, slices);
   return hipGetLastError();
 }
 
@@ -956,7 +980,7 @@ size_t attn_ws_bytes(int dt, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   // sized for the largest chip: a pure function of the shape
   const int64_t G = Hq / Hkv, width = tile_width(dt, D, G), units = Hkv * ((G + width - 1) / width);
   const int64_t groups = units * team_of(units) / kWaves;
-  const size_t slots = (size_t)units * parts_of(chip_blocks(kMaxCus, D, width), groups) * 2 * (G < width ? G : width);
+  const size_t slots = (size_t)units * parts_of(chip_blocks(kMaxCus, D), groups) * 2 * (G < width ? G : width);
   const size_t cut = slots * D * 4 + slots * 8 + (size_t)B * 8;
   return cut > any ? cut : any;
 }

@@ -387,6 +387,17 @@ def test_paged_attn_many_ragged_requests(fk):
         _check_attn(fk.fk_paged_attn(max_len=hint, **args), want, "f16", 128, 0.0)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("case", [(64, 32, 128, 16, [900, 1, 0, 640, 77], "log", 30.0, "plain"),
+                                  (80, 4, 64, 7, [5 * i for i in range(40)] + [700], None, 0.0, "heads"),
+                                  (8, 8, 32, 16, [13 * i % 600 for i in range(20)], None, 0.0, "plain")],
+                         ids=["heads32", "g20", "d32"])
+def test_paged_attn_a_block_for_every_cu(fk, case, dtype):
+    """Middle lengths and about as many (request, head) pairs as CUs."""
+    args, want = _attn_case(case, dtype, seed=17)
+    _check_attn(fk.fk_paged_attn(max_len=max(case[4]), **args), want, dtype, case[2], case[6])
+
+
 def test_paged_attn_same_bits_any_workspace_and_stream(fk):
     torch = _torch()
     args, want = _attn_case((8, 2, 128, 16, [6000, 0, 37, 900], "log", 0.0, "plain"), "bf16", 8)
