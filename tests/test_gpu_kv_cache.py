@@ -417,6 +417,26 @@ def test_paged_attn_same_bits_any_workspace_and_stream(fk):
         first = got
 
 
+@pytest.mark.parametrize("D", [64, 33])
+def test_paged_attn_nothing_to_do(fk, D):
+    """No requests, tables without columns, caches without pages, lengths below zero."""
+    torch = _torch()
+    z = lambda *s, t=torch.float16: torch.zeros(s, dtype=t, device="cuda")      # noqa: E731
+    i32 = torch.int32
+    kc = z(3, 16, 2, D)
+    out, lse = fk.fk_paged_attn(z(0, 4, D), kc, kc, z(0, 5, t=i32), z(0, t=i32), return_lse=True)
+    assert out.shape == (0, 4, D) and lse.shape == (0, 4)
+    q, lens = torch.ones(2, 4, D, dtype=torch.float16, device="cuda"), _dev(np.array([7, -3], np.int32))
+    for cache, table in ((kc, z(2, 0, t=i32)), (z(0, 16, 2, D), z(2, 100, t=i32)),
+                         (kc, torch.full((2, 100), -1, dtype=i32, device="cuda"))):
+        out, lse = fk.fk_paged_attn(q, cache, cache, table, lens, return_lse=True)
+        assert (out == 0).all() and (lse == -math.inf).all()
+    x = z(5, 6, D)
+    _, ko = fk.fk_qk_norm_rope(x[:, :4], x[:, 4:], x[:, 4:], slots=z(5, t=i32), k_cache=z(0, 16, 2, D),
+                               v_cache=z(0, 16, 2, D))
+    assert ko is None
+
+
 def test_paged_attn_offsets_past_32_bits(fk):
     """Pages 3 * 2^30 elements apart: offsets of 12 GB and more."""
     torch = _torch()
