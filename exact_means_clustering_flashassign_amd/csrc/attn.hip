@@ -263,10 +263,10 @@ __device__ const uint4 zero_row[64] = {};
 // of 0 to 16384 keys spread over the logarithm, 8 heads of 128).
 struct Plan {
   int parts;            // blocks per (cache head, head tile); 0: a team per request
-  int team;             // waves that share a request's steps: 8, 4, 2 or 1
+  int team, team_log;   // waves that share a request's steps: 8, 4, 2 or 1
   int heads, tiles;     // cache heads, head tiles per cache head
   int G, width, hr;     // query heads per cache head, per head tile, and per tile at most
-  FastDiv page;
+  FastDiv page, by_tiles, by_heads;
   float* o;             // (parts, heads, tiles, 2, hr, D) partial sums
   float* ml;            // (parts, heads, tiles, 2, hr, 2) their maximum and sum
   int32_t* cover;       // (B, 2) first and last part of a request
@@ -576,11 +576,19 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
 struct Start {
   int64_t lo, hi;            // this part's range of costs
   int64_t b, before;         // request that holds lo, cost of those before it
+  // Part w of the parts in use: floor(total w / parts) on, in 32-bit divisions where the
+  // total allows (a 64-bit one is some 150 instructions of a call's first microsecond).
   __device__ __forceinline__ void cut(int64_t total, const Plan& p, int w) {
-    const int64_t most = total / p.team;           // a part is a step of each wave at least
-    const int64_t parts = most < 1 ? 1 : (most < p.parts ? most : p.parts);
-    lo = w < parts ? total * w / parts : total;
-    hi = w < parts ? total * (w + 1) / parts : total;
+    const int64_t most = total >> p.team_log;      // a part is a step of each wave at least
+    const uint32_t parts = most < 1 ? 1 : (uint32_t)min(most, (int64_t)p.parts);
+    if (w >= (int)parts) {
+      lo = hi = total;
+      return;
+    }
+    const int64_t q = total >> 32 ? total / parts : (int64_t)((uint32_t)total / parts);
+    const uint32_t r = (uint32_t)(total - q * parts);
+    lo = q * w + r * w / parts;
+    hi = q * (w + 1) + r * (w + 1) / parts;
   }
 };
 
@@ -603,10 +611,10 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, const Plan& p, in
       const uint32_t o = __shfl_up(incl, off, 64);
       if (lane >= off) incl += o;
     }
-    st.cut(__shfl(incl, 63, 64), p, w);
+    st.cut((uint32_t)__builtin_amdgcn_readlane(incl, 63), p, w);
     const int b = __popcll(__ballot(incl <= st.lo));      // requests that end at or before lo
     st.b = b;
-    st.before = b ? __shfl(incl, b - 1, 64) : 0;
+    st.before = b ? (uint32_t)__builtin_amdgcn_readlane(incl, b - 1) : 0;
     return st;
   }
   __shared__ int64_t wave_tot[kWaves];
@@ -670,10 +678,12 @@ __global__ __launch_bounds__(W * 64, W == kWaves ? waves_per_simd(DP) : W / 4) v
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Waves k0 .. k1 - 1 of this block are one team; its teams take neighbouring heads.
-  const int k0 = w / p.team * p.team, k1 = k0 + p.team, teams = W / p.team;
-  const int64_t unit = xcd_remap(blockIdx.x, gridDim.x) * teams + w / p.team;
-  const int ht = (int)(unit % p.tiles), hk = (int)((unit / p.tiles) % p.heads);
-  const int64_t part = unit / ((int64_t)p.tiles * p.heads);
+  const int k0 = w >> p.team_log << p.team_log, k1 = k0 + p.team, teams = W >> p.team_log;
+  const uint32_t unit =
+      (uint32_t)xcd_remap(blockIdx.x, gridDim.x) * teams + (w >> p.team_log);
+  const uint32_t rest = div_by(unit, p.by_tiles), at_head = div_by(rest, p.by_heads);
+  const int ht = (int)(unit - rest * p.tiles), hk = (int)(rest - at_head * p.heads);
+  const int64_t part = at_head;
   const int D = (int)a.cache.dim;
 
   Start st;
@@ -772,9 +782,9 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Plan p, in
   __shared__ float red[kJoin][4], redl[kJoin];
   const int me = R == 1 ? 0 : threadIdx.x / threads, tid = threadIdx.x - me * threads;
   const int slice = R == 1 ? blockIdx.x % slices : 0;
-  const int64_t out_row = R == 1 ? blockIdx.x / slices : (int64_t)blockIdx.x * R + me;
+  const int64_t out_row = R == 1 ? blockIdx.x / slices : blockIdx.x * R + me;
   if (out_row >= a.B * a.Hq) return;
-  const int64_t b = out_row / a.Hq;
+  const int64_t b = (uint32_t)out_row / (uint32_t)a.Hq;
   const int h = (int)(out_row - b * a.Hq);
   const int first = p.cover[2 * b], last = p.cover[2 * b + 1];
   if (first == last) return;
@@ -914,8 +924,11 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
     p.team = eight ? 8 : (many || most <= Shape<DT, DP>::keys ? 1 : kWaves);
   }
   const int W = eight ? 8 : kWaves;
+  p.team_log = p.team == 8 ? 3 : (p.team == 4 ? 2 : p.team - 1);
+  p.by_tiles = fast_div((uint32_t)p.tiles);
+  p.by_heads = fast_div((uint32_t)p.heads);
   const int64_t blocks = (units * (cut ? p.parts : a.B) * p.team + W - 1) / W;
-  if (blocks > 0x7FFFFFFF || a.B * a.Hq > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (units * a.B + W > 0x7FFFFFFF || a.B * a.Hq > 0x7FFFFFFF - 4) return hipErrorInvalidConfiguration;
   // EXACT: rows fill their lanes and whole 128-byte lines, and no other wave reads them.
   const auto aligned = [](uintptr_t base, const int64_t* s) {
     return !((base | (uintptr_t)((s[0] | s[1] | s[2]) * Val<DT>::bytes)) & 127);

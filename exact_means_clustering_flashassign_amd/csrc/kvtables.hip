@@ -19,7 +19,7 @@ constexpr int kOwnScan = 2048;
 constexpr int kRun = 256, kTokens = 64;       // entries and tokens a wave takes at a time
 
 struct Geometry {
-  FastDiv page;
+  FastDiv page, by_row;
   int32_t cap;            // tokens that a row of pages holds, at most 2^31 - 1
   int64_t row_items, items;
   int32_t token_items;
@@ -185,7 +185,8 @@ __global__ __launch_bounds__(kThreads) void tables_fill_kernel(TablesArgs a, Geo
   const int64_t wave = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int64_t it = wave; it < g.items; it += (int64_t)gridDim.x * kWaves) {
     if (it >= g.token_items) {
-      const int64_t r = it - g.token_items, b = r / g.row_items, c = r - b * g.row_items;
+      const uint32_t r = (uint32_t)(it - g.token_items);
+      const int64_t b = div_by(r, g.by_row), c = r - b * g.row_items;
       const Need n = need_of(a, g, b);
       const int32_t taken = cu_p[b];
       if (c == 0 && lane == 0) a.lens[b] = to_i32((int64_t)n.old + n.fresh);
@@ -227,6 +228,8 @@ hipError_t launch_page_tables(const TablesArgs& a, hipStream_t s) {
   g.token_items = (int32_t)((a.tokens + kTokens - 1) / kTokens);
   g.row_items = (a.width + kRun - 1) / kRun;
   g.items = g.token_items + a.B * g.row_items;
+  if (g.items > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  g.by_row = fast_div((uint32_t)g.row_items);
   const int64_t need = (g.items + kWaves - 1) / kWaves, most = (int64_t)device_cus() * 4;
   const unsigned blocks = (unsigned)(need < 1 ? 1 : (need < most ? need : most));
   if (a.B <= kOwnScan) {

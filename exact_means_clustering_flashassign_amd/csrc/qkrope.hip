@@ -99,7 +99,7 @@ struct RopePlan {
   int L, rp;                 // lanes a row (a power of two), rows a pass
   int rows, passes;          // rows a token, passes a token
   int ppw, wpt;              // passes a wave, waves a token
-  FastDiv page, per;         // tokens a page, rows a token
+  FastDiv page, per, by_wpt; // tokens a page, rows a token, waves a token
 };
 
 enum { kApart, kSideBySide, kExchange };
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(kWaves * 64) void rope_vec_kernel(RopeArgs a, RopeP
     t = live ? div_by(row, p.per) : 0;
     row0 = live ? row - (uint32_t)t * p.rows : 0;
   } else {
-    t = wave / p.wpt;
+    t = div_by((uint32_t)wave, p.by_wpt);
     pass0 = (int)(wave - t * p.wpt) * p.ppw;
     pass1 = min(pass0 + p.ppw, p.passes);
   }
@@ -319,6 +319,7 @@ hipError_t run_mode(const RopeArgs& a, hipStream_t s) {
   p.wpt = (p.passes + p.ppw - 1) / p.ppw;
   p.page = fast_div(a.cache.k ? (uint32_t)a.cache.page : 1);
   p.per = fast_div((uint32_t)p.rows);
+  p.by_wpt = fast_div((uint32_t)p.wpt);
   // Tokens of one pass, or that leave a quarter of their passes' lanes idle, go end to
   // end (60000 tokens of 3 rows: 51 -> 26 us; of 10 rows in two passes: 47 -> 41); with more
   // rows the wave that stays with its token is faster (48 rows: 356 us, end to end 406).
@@ -326,7 +327,7 @@ hipError_t run_mode(const RopeArgs& a, hipStream_t s) {
                     a.T * p.rows < 0x7FFFFFFF - 64;
   const int64_t waves = flat ? (a.T * p.rows + p.rp - 1) / p.rp : a.T * p.wpt;
   const int64_t blocks = (waves + kWaves - 1) / kWaves;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (waves > 0x7FFFFFFF - kWaves) return hipErrorInvalidConfiguration;
   const auto kernel =
       flat ? rope_vec_kernel<DT, VE, MODE, true> : rope_vec_kernel<DT, VE, MODE, false>;
   kernel<<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, p, waves);
