@@ -323,19 +323,26 @@ _pack2 = struct.Struct("2q").pack
 _pack_cache = struct.Struct("3P4q9q").pack      # the layout of fk_kv_cache_t
 
 
-def _raw_stream(index: int) -> int:
-    return _torch_c()._cuda_getCurrentRawStream(index)
+_tc = None
 
 
-@functools.lru_cache(None)
-def _torch_c():
-    return _torch()._C
+class _TorchCalls:
+    """What the calls below need of torch, looked up once."""
+
+    def __init__(self):
+        torch = _torch()
+        self.empty, self.empty_like = torch.empty, torch.empty_like
+        self.i32, self.f32, self.u8 = torch.int32, torch.float32, torch.uint8
+        self.codes = {torch.float32: FK_F32, torch.float16: FK_F16, torch.bfloat16: FK_BF16}
+        self.stream = torch._C._cuda_getCurrentRawStream
 
 
-@functools.lru_cache(None)
-def _codes():
-    torch = _torch()
-    return {torch.float32: FK_F32, torch.float16: FK_F16, torch.bfloat16: FK_BF16}
+def _calls():
+    global _tc
+    if _tc is None:
+        load()
+        _tc = _TorchCalls()
+    return _tc
 
 
 def _gpu_index(t, name) -> int:
@@ -380,7 +387,7 @@ def _kv_cache(k_cache, v_cache, key_bias, dtype, heads, dim, index):
     bp, sb = None, (0, 0, 0)
     if key_bias is not None:
         sb = key_bias.stride()
-        if key_bias.shape != shape[:3] or key_bias.dtype is not _torch().float32 or \
+        if key_bias.shape != shape[:3] or key_bias.dtype is not _calls().f32 or \
                 key_bias.get_device() != index or key_bias.requires_grad:
             raise ValueError(f"key_bias must be float32 of shape {tuple(shape[:3])} on "
                              f"cuda:{index} without grad, got {key_bias.dtype} "
@@ -398,8 +405,8 @@ def fk_page_tables(len_old, len_new, free_pages, page: int, width: int, tokens: 
     (table (B,width), lens (B), cu_tokens (B+1), cu_pages (B+1), slots (tokens),
     positions (tokens)), views of one buffer; `out`: those six tensors, to
     write into."""
-    torch = _torch()
-    i32, index = torch.int32, _gpu_index(len_old, "len_old")
+    tc = _tc or _calls()
+    i32, index = tc.i32, _gpu_index(len_old, "len_old")
     B = len_old.numel()
     p_old = _on(len_old, "len_old", i32, (B,), index)
     p_new = _on(len_new, "len_new", i32, (B,), index)
@@ -413,9 +420,9 @@ def fk_page_tables(len_old, len_new, free_pages, page: int, width: int, tokens: 
         if width < 1 or tokens < 0:
             raise ValueError("width must be at least 1 and tokens non-negative")
         n = B * width
-        buf = torch.empty(n + 3 * B + 2 + 2 * tokens, dtype=i32, device=len_old.device)
-        o = buf.split_with_sizes((n, B, B + 1, B + 1, tokens, tokens))
-        out = (o[0].view(B, width), *o[1:])
+        buf = tc.empty(n + 3 * B + 2 + 2 * tokens, dtype=i32, device=len_old.device)
+        rows, *rest = buf.split_with_sizes((n, B, B + 1, B + 1, tokens, tokens))
+        out = (rows.view(B, width), *rest)
         p = buf.data_ptr()
         n, B4, T4 = 4 * n, 4 * B, 4 * tokens
         ps = (p, p + n, p + n + B4, p + n + 2 * B4 + 4, p + n + 3 * B4 + 8, p + n + 3 * B4 + 8 + T4)
@@ -424,10 +431,12 @@ def fk_page_tables(len_old, len_new, free_pages, page: int, width: int, tokens: 
             raise ValueError("out must hold table, lens, cu_tokens, cu_pages, slots, positions")
         shapes = ((B, width), (B,), (B + 1,), (B + 1,), (tokens,), (tokens,))
         ps = [_on(t, f"out[{i}]", i32, s, index) for i, (t, s) in enumerate(zip(out, shapes))]
-    st = load().fk_page_tables(p_old, p_new, p_in, width_in, p_free, n_free, B, page, width,
-                               tokens, *ps, _raw_stream(index))
-    _check(st, "fk_page_tables")
-    return tuple(out)
+        out = tuple(out)
+    st = _lib.fk_page_tables(p_old, p_new, p_in, width_in, p_free, n_free, B, page, width, tokens,
+                             *ps, tc.stream(index))
+    if st:
+        _check(st, "fk_page_tables")
+    return out
 
 
 def fk_qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-6, rope=None,
@@ -439,9 +448,9 @@ def fk_qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-
     With slots (T) int32, keys and values are stored in k_cache and v_cache
     (pages, page, Hkv, D), with a key_bias (pages, page, Hkv) of 0. Returns
     (q_out, k_out); k_out is None with a cache unless given."""
-    torch = _torch()
+    tc = _tc or _calls()
     dt, index = q.dtype, _gpu_index(q, "q")
-    code = _codes().get(dt)
+    code = tc.codes.get(dt)
     if code is None:
         code = dtype_code(dt)            # says what is supported
     sq, sk = _rows(q, "q", dt, 3, index), _rows(k, "k", dt, 3, index)
@@ -458,16 +467,19 @@ def fk_qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-
         if v.shape != ks:
             raise ValueError(f"v must have k's shape {tuple(ks)}, got {tuple(v.shape)}")
         vp, sv = v.data_ptr(), _pack2(sv[0], sv[1])
-        sp = _on(slots, "slots", torch.int32, (T,), index)
+        sp = _on(slots, "slots", tc.i32, (T,), index)
         cache = _kv_cache(k_cache, v_cache, key_bias, dt, Hkv, D, index)[0]
     elif v is not None or k_cache is not None or v_cache is not None or key_bias is not None:
         raise ValueError("v and the cache need slots")
     elif k_out is None:
-        k_out = torch.empty((T, Hkv, D), dtype=dt, device=q.device)
+        k_out = tc.empty((T, Hkv, D), dtype=dt, device=q.device)
     if k_out is not None:
         p_ko = _on(k_out, "k_out", dt, (T, Hkv, D), index)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+        q_out = tc.empty((T, Hq, D), dtype=dt, device=q.device)
+        p_qo = q_out.data_ptr()
+    else:
+        p_qo = _on(q_out, "q_out", dt, (T, Hq, D), index)
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
     p_qw = p_kw = rp = pp = None
@@ -479,13 +491,14 @@ def fk_qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-
         if rope.dim() != 2 or positions is None:
             raise ValueError("rope must be (max_pos, rot), with positions")
         max_pos, rot = rope.shape
-        rp = _on(rope, "rope", torch.float32, (max_pos, rot), index)
-        pp = _on(positions, "positions", torch.int32, (T,), index)
-    st = load().fk_qk_norm_rope(
+        rp = _on(rope, "rope", tc.f32, (max_pos, rot), index)
+        pp = _on(positions, "positions", tc.i32, (T,), index)
+    st = _lib.fk_qk_norm_rope(
         q.data_ptr(), _pack2(sq[0], sq[1]), k.data_ptr(), _pack2(sk[0], sk[1]), vp, sv, code, T,
         Hq, Hkv, D, p_qw, p_kw, eps, rp, max_pos, rot, interleaved, pp, sp, cache,
-        _on(q_out, "q_out", dt, (T, Hq, D), index), p_ko, _raw_stream(index))
-    _check(st, "fk_qk_norm_rope")
+        p_qo, p_ko, tc.stream(index))
+    if st:
+        _check(st, "fk_qk_norm_rope")
     return q_out, k_out
 
 
@@ -506,45 +519,49 @@ def fk_paged_attn(q, k_cache, v_cache, table, lens, scale: Optional[float] = Non
     int32: softmax(softcap(scale q.k) + key_bias) v, with scale 1/sqrt(D) by
     default. Returns out (B,Hq,D), and with return_lse (or lse given) the
     natural log of the softmax's sum, (B,Hq) fp32."""
-    torch = _torch()
+    tc = _tc or _calls()
     dt, index = q.dtype, _gpu_index(q, "q")
-    code = _codes().get(dt)
+    code = tc.codes.get(dt)
     if code is None:
         code = dtype_code(dt)            # says what is supported
     sq = _rows(q, "q", dt, 3, index)
     B, Hq, D = q.shape
     cache, heads = _kv_cache(k_cache, v_cache, key_bias, dt, 0, D, index)
-    st2 = _rows(table, "table", torch.int32, 2, index)
+    st2 = _rows(table, "table", tc.i32, 2, index)
     rows, width = table.shape
     if rows != B:
         raise ValueError(f"table must have {B} rows, got {tuple(table.shape)}")
-    p_lens = _on(lens, "lens", torch.int32, (B,), index)
+    p_lens = _on(lens, "lens", tc.i32, (B,), index)
     need = _attn_ws(code, B, Hq, heads, D)
     if need == 0:
         raise ValueError(f"{Hq} query heads of {D} do not go with {heads} cache heads")
     dev = q.device
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=dt, device=dev)
+        if q.is_contiguous():
+            out = tc.empty_like(q)
+        else:
+            out = tc.empty((B, Hq, D), dtype=dt, device=dev)
         p_out = out.data_ptr()
     else:
         p_out = _on(out, "out", dt, (B, Hq, D), index)
     p_lse = None
     if lse is not None:
-        p_lse = _on(lse, "lse", torch.float32, (B, Hq), index)
+        p_lse = _on(lse, "lse", tc.f32, (B, Hq), index)
     elif return_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = tc.empty((B, Hq), dtype=tc.f32, device=dev)
         p_lse = lse.data_ptr()
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = tc.empty(need, dtype=tc.u8, device=dev)
         p_ws = ws.data_ptr()
     else:
         need = ws.numel()
-        p_ws = _on(ws, "ws", torch.uint8, (need,), index)
-    st = load().fk_paged_attn(
+        p_ws = _on(ws, "ws", tc.u8, (need,), index)
+    st = _lib.fk_paged_attn(
         q.data_ptr(), _pack2(sq[0], sq[1]), code, B, Hq, cache, table.data_ptr(),
         st2[0] if B > 1 else width, width, p_lens, max_len, D ** -0.5 if scale is None else scale,
-        softcap, p_out, p_lse, p_ws, need, _raw_stream(index))
-    _check(st, "fk_paged_attn")
+        softcap, p_out, p_lse, p_ws, need, tc.stream(index))
+    if st:
+        _check(st, "fk_paged_attn")
     return out if lse is None else (out, lse)
 
 
