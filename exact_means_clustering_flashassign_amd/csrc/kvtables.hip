@@ -7,8 +7,8 @@
 // in LDS (8 bytes a request from L2) and one launch does it all: the call is a
 // few microseconds of latency, and a second launch would add as much again.
 // Beyond that one block writes the sums first and the others read them. Measured: 32
-// requests with one new token and 4726 entries each 4.4 us, 1024 requests with a million
-// new tokens 11.3 us in one launch (13.8 in two), 3723 requests in two 10.6 us.
+// requests with one new token and 4726 entries each 4.4 us, 1024 requests with 0.84 million
+// new tokens 11 us in one launch (13.8 in two), 3723 requests in two 10.6 us.
 #include "fk_kv.hpp"
 
 namespace fk {
