@@ -230,7 +230,7 @@ hipError_t launch_page_tables(const TablesArgs& a, hipStream_t s) {
   g.items = g.token_items + a.B * g.row_items;
   if (g.items > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   g.by_row = fast_div((uint32_t)g.row_items);
-  const int64_t need = (g.items + kWaves - 1) / kWaves, most = (int64_t)device_cus() * 4;
+  const int64_t need = (g.items + kWaves - 1) / kWaves, most = device_cus() > 0 ? (int64_t)device_cus() * 4 : 1;
   const unsigned blocks = (unsigned)(need < 1 ? 1 : (need < most ? need : most));
   if (a.B <= kOwnScan) {
     tables_fill_kernel<true><<<blocks, kThreads, 0, s>>>(a, g);

@@ -314,7 +314,8 @@ hipError_t run_mode(const RopeArgs& a, hipStream_t s) {
   p.rows = (int)rows;
   p.passes = (p.rows + p.rp - 1) / p.rp;
   // A wave takes several passes once there are waves enough for every CU's slots.
-  const int64_t all = a.T * p.passes, want = (int64_t)device_cus() * 32;
+  const int64_t all = a.T * p.passes;
+  const int64_t want = device_cus() > 0 ? (int64_t)device_cus() * 32 : 1;
   p.ppw = (int)(all / want < 1 ? 1 : (all / want < p.passes ? all / want : p.passes));
   p.wpt = (p.passes + p.ppw - 1) / p.ppw;
   p.page = fast_div(a.cache.k ? (uint32_t)a.cache.page : 1);

@@ -97,6 +97,22 @@ def test_paged_attn_refusals(fk, lib):
     assert lib.fk_workspace_size_attn(1, 0, 4, 2, 64) >= 256
 
 
+def test_without_a_gpu_valid_calls_report_an_error(fk, lib):
+    """Arguments in order but no device: a status, not a crash."""
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("the addresses here are made up: only for machines without a GPU")
+    c = _cache(fk)
+    HIP = 4
+    assert lib.fk_page_tables(P, P, None, 0, P, 4, 2, 16, 8, 2, P, P, P, P, P, P, None) == HIP
+    assert lib.fk_qk_norm_rope(P, I2(256, 64), P, I2(128, 64), P, I2(128, 64), 1, 3, 4, 2, 64, P, P, 1e-6, P, 9,
+                               64, 0, P, P, ctypes.byref(c), P, None, None) == HIP
+    for width in (8, 4000):
+        assert lib.fk_paged_attn(P, I2(256, 64), 1, 3, 4, ctypes.byref(c), P, width, width, P, 0, 0.1, 0.0, P,
+                                 None, P, lib.fk_workspace_size_attn(1, 3, 4, 2, 64), None) == HIP
+
+
 def test_python_refusals(fk):
     import torch
 
