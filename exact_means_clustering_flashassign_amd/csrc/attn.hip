@@ -622,6 +622,7 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, const Plan& p, in
   const int64_t n = (a.B + kWaves * 64 - 1) / (kWaves * 64);
   const int64_t b0 = threadIdx.x * n, b1 = b0 + n < a.B ? b0 + n : a.B;
   int64_t mine = 0;
+#pragma unroll 8
   for (int64_t b = b0; b < b1; ++b) mine += cost_of<KEYS>(a, p, b);
   int64_t incl = mine;
 #pragma unroll
