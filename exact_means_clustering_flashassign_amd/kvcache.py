@@ -64,13 +64,14 @@ class ClusteredKVCache:
         if taken > self.free.numel():
             raise RuntimeError(f"{taken} pages needed, {self.free.numel()} free")
         n = torch.tensor(new, dtype=torch.int32).to(self.k.device)
-        self.table, self.lens_dev, _, _, slots, pos = fk.fk_page_tables(
+        table, lens_dev, _, _, slots, pos = fk.fk_page_tables(
             self.lens_dev, n, self.free, self.page, self.width, T, table=self.table)
-        self.free = self.free[taken:]
         if rope is not None:
             pos = pos + torch.repeat_interleave(self.shift, n, output_size=T)
         out, _ = fk.fk_qk_norm_rope(q, k, v, q_weight, k_weight, eps, rope, pos, interleaved,
                                     slots, self.k, self.v, self.key_bias)
+        # only now: a refused call leaves the cache as it was
+        self.table, self.lens_dev, self.free = table, lens_dev, self.free[taken:]
         self.lens = lens
         self.seen = [a + b for a, b in zip(self.seen, new)]
         return out
