@@ -212,6 +212,7 @@ template <int DT, int DP> struct Shape {
   static constexpr int nu = DP / (16 * ve);                 // value loads per row and lane
   static constexpr int rows = 4 * tiles;                    // value rows per lane
   static constexpr int ldo = DP + 4;                        // LDS row of merged results
+  static constexpr int least = DP <= 32 ? 0 : (DP <= 64 ? 32 : (DP <= 192 ? DP - 64 : 192));  // D is above it
 };
 
 // A value that is the same in every lane, moved to scalar registers.
@@ -323,6 +324,10 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }
 
+// Rows narrower than the tile, rows that fill it, and rows that fill it and whole
+// 128-byte lines that no other wave reads, by streaming loads.
+enum { kNarrow, kWhole, kStream };
+
 // State of one wave over a run of steps.
 template <int DT, int DP, int HT> struct Acc {
   using S = Shape<DT, DP>;
@@ -337,7 +342,7 @@ template <int DT, int DP> struct Rows {
   float bias[n];
 };
 
-template <int DT, int DP, int HT, bool EXTRA, bool EXACT>
+template <int DT, int DP, int HT, bool EXTRA, int KIND>
 __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t b, int hk, int ht,
                                        int len, int step, int stride, int end,
                                        Rows<DT, DP>* rows,
@@ -345,7 +350,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
   using S = Shape<DT, DP>;
   const fk_kv_cache_t& c = a.cache;
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-  const int D = EXACT ? DP : (int)c.dim;
+  const int D = KIND == kNarrow ? (int)c.dim : DP;
   constexpr int eb = Val<DT>::bytes;
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
@@ -356,15 +361,16 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
   }
   if (step >= end) return;
 
-  // Query fragments; heads past G and elements past D are zero. An element
-  // past D reads the key row's start instead, times a zero query.
+  // Query fragments; heads past G and elements past D are zero. Elements past D of a
+  // key are read from the zeros too: an infinity of the row times a zero query is NaN.
+  // A value's read the row's start again and are not stored.
   uint4 q[HT][S::nc];
   uint32_t koff[S::nc], voff[S::nu];
+  const auto past = [&](int i) {            // unit i of this lane's part of a key is past D
+    return (i + 1) * 4 * S::unit > S::least && i * 4 * S::unit + g * S::unit >= D;
+  };
 #pragma unroll
-  for (int i = 0; i < S::nc; ++i) {
-    const int e = i * 4 * S::unit + g * S::unit;
-    koff[i] = e < D ? e * eb : 0;
-  }
+  for (int i = 0; i < S::nc; ++i) koff[i] = past(i) ? 0 : (i * 4 + g) * S::unit * eb;
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
     const int head = (ht * HT + h) * kHeadTile + m;
@@ -373,7 +379,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
 #pragma unroll
     for (int i = 0; i < S::nc; ++i) {
       q[h][i] = load16((uint64_t)(qp + koff[i]));
-      if (i * 4 * S::unit + g * S::unit >= D || head >= p.G) q[h][i] = make_uint4(0, 0, 0, 0);
+      if (past(i) || head >= p.G) q[h][i] = make_uint4(0, 0, 0, 0);
     }
   }
 #pragma unroll
@@ -429,7 +435,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
     for (int s = 0; s < S::tiles; ++s) {
       const uint64_t ad = r.k[16 * s + m];
 #pragma unroll
-      for (int i = 0; i < S::nc; ++i) kf[s][i] = load_row<16, EXACT>(ad + koff[i]);
+      for (int i = 0; i < S::nc; ++i) kf[s][i] = load_row<16, KIND == kStream>((past(i) ? zero : ad) + koff[i]);
     }
   };
   uint4 vf[S::rows][S::nu];            // a load of fewer bytes fills the first words
@@ -438,7 +444,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
     for (int j = 0; j < S::rows; ++j) {
       const uint64_t ad = r.v[16 * (j >> 2) + 4 * g + (j & 3)];
 #pragma unroll
-      for (int i = 0; i < S::nu; ++i) vf[j][i] = load_row<S::ve * eb, EXACT>(ad + voff[i]);
+      for (int i = 0; i < S::nu; ++i) vf[j][i] = load_row<S::ve * eb, KIND == kStream>(ad + voff[i]);
     }
   };
 
@@ -670,7 +676,7 @@ constexpr int waves_per_simd(int64_t D) {
 }
 constexpr int kMaxParts = kMaxCus * 4;
 
-template <int DT, int DP, int HT, bool EXTRA, bool EXACT, int W>
+template <int DT, int DP, int HT, bool EXTRA, int KIND, int W>
 __global__ __launch_bounds__(W * 64, W == kWaves ? waves_per_simd(DP) : W / 4) void attn_mfma_kernel(AttnArgs a, Plan p) {
   using S = Shape<DT, DP>;
   __shared__ Rows<DT, DP> rows[W][2];
@@ -685,7 +691,7 @@ __global__ __launch_bounds__(W * 64, W == kWaves ? waves_per_simd(DP) : W / 4) v
   const uint32_t rest = div_by(unit, p.by_tiles), at_head = div_by(rest, p.by_heads);
   const int ht = (int)(unit - rest * p.tiles), hk = (int)(rest - at_head * p.heads);
   const int64_t part = at_head;
-  const int D = (int)a.cache.dim;
+  const int D = KIND == kNarrow ? (int)a.cache.dim : DP;
 
   Start st;
   const bool cut = W == kWaves && p.parts > 0;
@@ -712,7 +718,7 @@ __global__ __launch_bounds__(W * 64, W == kWaves ? waves_per_simd(DP) : W / 4) v
     const bool starts = at >= st.lo;           // the request begins in this part
     if (t0 < t1 || (steps == 0 && starts)) {
       Acc<DT, DP, HT> acc;
-      attend<DT, DP, HT, EXTRA, EXACT>(a, p, b, hk, ht, len, t0 + w - k0, p.team, t1, rows[w], acc);
+      attend<DT, DP, HT, EXTRA, KIND>(a, p, b, hk, ht, len, t0 + w - k0, p.team, t1, rows[w], acc);
       const bool whole = t0 == 0 && t1 == steps;
       const int slot = t0 == 0 ? 1 : 0;
       const int64_t ps = (((part * p.heads + hk) * p.tiles + ht) * 2 + slot) * p.hr;
@@ -930,26 +936,29 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   p.by_heads = fast_div((uint32_t)p.heads);
   const int64_t blocks = (units * (cut ? p.parts : a.B) * p.team + W - 1) / W;
   if (units * a.B + W > 0x7FFFFFFF || a.B * a.Hq > 0x7FFFFFFF - 4) return hipErrorInvalidConfiguration;
-  // EXACT: rows fill their lanes and whole 128-byte lines, and no other wave reads them.
   const auto aligned = [](uintptr_t base, const int64_t* s) {
     return !((base | (uintptr_t)((s[0] | s[1] | s[2]) * Val<DT>::bytes)) & 127);
   };
   // Caches that the 256 MB last-level cache may still hold from the step before are read
   // without the mark (4 requests of 512 keys: 10.4 us, marked 13.3).
   const double bytes = 2.0 * a.B * most * a.cache.heads * DP * Val<DT>::bytes;
-  const bool exact = bytes >= (double)(128 << 20) && a.cache.dim == DP && p.tiles == 1 &&
-                     DP * Val<DT>::bytes % 128 == 0 &&
-                     aligned((uintptr_t)a.cache.k, a.cache.k_stride) &&
-                     aligned((uintptr_t)a.cache.v, a.cache.v_stride);
-  const bool extra = a.softcap > 0.f || a.cache.key_bias;
-  auto kernel = exact ? (extra ? attn_mfma_kernel<DT, DP, HT, true, true, kWaves>
-                               : attn_mfma_kernel<DT, DP, HT, false, true, kWaves>)
-                      : (extra ? attn_mfma_kernel<DT, DP, HT, true, false, kWaves>
-                               : attn_mfma_kernel<DT, DP, HT, false, false, kWaves>);
+  const bool full = a.cache.dim == DP, extra = a.softcap > 0.f || a.cache.key_bias;
+  auto kernel = full ? (extra ? attn_mfma_kernel<DT, DP, HT, true, kWhole, kWaves>
+                              : attn_mfma_kernel<DT, DP, HT, false, kWhole, kWaves>)
+                     : (extra ? attn_mfma_kernel<DT, DP, HT, true, kNarrow, kWaves>
+                              : attn_mfma_kernel<DT, DP, HT, false, kNarrow, kWaves>);
+  if constexpr (DP * Val<DT>::bytes % 128 == 0) {
+    if (full && bytes >= (double)(128 << 20) && p.tiles == 1 &&
+        aligned((uintptr_t)a.cache.k, a.cache.k_stride) && aligned((uintptr_t)a.cache.v, a.cache.v_stride))
+      kernel = extra ? attn_mfma_kernel<DT, DP, HT, true, kStream, kWaves>
+                     : attn_mfma_kernel<DT, DP, HT, false, kStream, kWaves>;
+  }
   if constexpr (DP <= 128) {
     if (eight)
-      kernel = extra ? attn_mfma_kernel<DT, DP, HT, true, false, 8>
-                     : attn_mfma_kernel<DT, DP, HT, false, false, 8>;
+      kernel = full ? (extra ? attn_mfma_kernel<DT, DP, HT, true, kWhole, 8>
+                             : attn_mfma_kernel<DT, DP, HT, false, kWhole, 8>)
+                    : (extra ? attn_mfma_kernel<DT, DP, HT, true, kNarrow, 8>
+                             : attn_mfma_kernel<DT, DP, HT, false, kNarrow, 8>);
   }
   kernel<<<(unsigned)blocks, W * 64, 0, s>>>(a, p);
   hipError_t e = hipGetLastError();

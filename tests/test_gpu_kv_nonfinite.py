@@ -1,0 +1,67 @@
+"""Paged attention where keys, values and queries that count are infinite or NaN,
+against what the formula gives for them in IEEE arithmetic:
+
+  * a key whose score is -inf has weight 0 and drops out: the result is the one
+    without it (the oracle's, with that key masked).
+
+Error bounds of the finite results are those of test_gpu_kv_cache.py.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+import synthdata
+from gpu_helpers import host_f64, to_dev
+from test_gpu_kv_cache import _check_attn, _dev, _rand
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = ["f16", "bf16", "f32"]
+# rows narrower than the tile that holds them, rows that fill it, and rows of odd size
+DIMS = [(2, 1, 24), (6, 2, 72), (4, 2, 80), (17, 1, 96), (2, 1, 160), (3, 1, 200), (4, 2, 64), (8, 2, 128),
+        (2, 1, 256), (3, 3, 33), (2, 1, 320)]
+LENS = [70, 5, 700]
+
+
+def _case(Hq, Hkv, D, dtype, lens, seed):
+    """Inputs with one page per 16 tokens, in order of requests, and their fp64 values."""
+    rng = np.random.default_rng(seed)
+    page, B = 16, len(lens)
+    held = [-(-n // page) for n in lens]
+    table = np.full((B, max(held)), -1, np.int32)
+    at = 0
+    for b, h in enumerate(held):
+        table[b, :h] = np.arange(at, at + h)
+        at += h
+    q, k, v = _rand(rng, (B, Hq, D), dtype), *(_rand(rng, (at, page, Hkv, D), dtype) for _ in range(2))
+    f64 = [synthdata.to_f64(t, dtype) for t in (q, k, v)]
+    dev = [to_dev(t, dtype) for t in (q, k, v)]
+    return dev, f64, table
+
+
+def _wide(table):
+    """Room for 2^20 keys a request: the plan of large caches."""
+    return np.concatenate([table, np.full((table.shape[0], 1 << 16), -1, np.int32)], 1)
+
+
+def _all_plans(fk, q, k, v, table, lens, D, check, **kw):
+    ls = _dev(np.array(lens, np.int32))
+    for tab, hint in ((table, 1), (table, max(lens)), (table, 0), (_wide(table), 0)):
+        check(fk.fk_paged_attn(q, k, v, _dev(tab), ls, max_len=hint, return_lse=True, **kw))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dims", DIMS, ids=[f"{a}x{b}d{d}" for a, b, d in DIMS])
+def test_keys_of_score_minus_infinity_drop_out(fk, dims, dtype):
+    Hq, Hkv, D = dims
+    (q, k, v), (q64, k64, v64), table = _case(Hq, Hkv, D, dtype, LENS, D)
+    q[..., :2] = q[..., :2].abs() + 0.5             # -inf times these is -inf for every head
+    q64 = host_f64(q, dtype)
+    bias = np.zeros(k64.shape[:3])
+    for page, tok, e in ((0, 0, 0), (1, 3, 1), (4, 2, 0), (table[1, 0], 4, 1), (table[2, 20], 15, 0)):
+        k[page, tok, :, e] = -math.inf
+        bias[page, tok] = -math.inf
+    want = oracle.paged_attn(q64, k64, v64, table, LENS, D ** -0.5, 0.0, bias)
+    _all_plans(fk, q, k, v, table, LENS, D, lambda got: _check_attn(got, want, dtype, D, 0.0))
