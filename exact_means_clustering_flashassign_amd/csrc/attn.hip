@@ -489,10 +489,12 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
       for (int u = 0; u < S::tiles; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // -inf where a key does not count: its score is 0 (a zero row)
+          // -inf where a key does not count: its score is 0 (a zero row), or NaN where
+          // the query is not finite
+          const float bias = now.bias[16 * u + 4 * g + i];
           float x = s[h][u][i] * a.scale;
           if (cap) x = capped(x, a.softcap, inv_cap);
-          s[h][u][i] = x + now.bias[16 * u + 4 * g + i];
+          s[h][u][i] = bias == -INFINITY ? bias : (EXTRA ? x + bias : x);
           top = fmaxf(top, s[h][u][i]);
         }
       top = fmaxf(top, __shfl_xor(top, 16, 64));

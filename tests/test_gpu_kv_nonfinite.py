@@ -2,7 +2,8 @@
 against what the formula gives for them in IEEE arithmetic:
 
   * a key whose score is -inf has weight 0 and drops out: the result is the one
-    without it (the oracle's, with that key masked).
+    without it (the oracle's, with that key masked);
+  * a request whose keys are all masked gives 0 and -inf, whatever its query holds.
 
 Error bounds of the finite results are those of test_gpu_kv_cache.py.
 """
@@ -65,3 +66,39 @@ def test_keys_of_score_minus_infinity_drop_out(fk, dims, dtype):
         bias[page, tok] = -math.inf
     want = oracle.paged_attn(q64, k64, v64, table, LENS, D ** -0.5, 0.0, bias)
     _all_plans(fk, q, k, v, table, LENS, D, lambda got: _check_attn(got, want, dtype, D, 0.0))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("masked", ["pages", "bias"])
+@pytest.mark.parametrize("dims", [(4, 2, 64), (8, 2, 128), (40, 2, 96), (2, 1, 256), (3, 3, 33)],
+                         ids=["d64", "d128", "g20d96", "d256", "d33"])
+def test_nothing_left_whatever_the_query_holds(fk, dims, masked, dtype):
+    import torch
+
+    Hq, Hkv, D = dims
+    lens = [70, 5, 700, 40]
+    (q, k, v), (q64, k64, v64), table = _case(Hq, Hkv, D, dtype, lens, D + 1)
+    q[0], q[2, :, 1] = math.nan, math.inf
+    bias = np.zeros(k64.shape[:3], np.float32)
+    if masked == "pages":
+        table = np.where(np.isin(np.arange(4), (0, 2))[:, None], -1, table).astype(np.int32)
+    else:
+        for b in (0, 2):
+            bias[table[b, :-(-lens[b] // 16)]] = -np.inf
+    want = oracle.paged_attn(np.nan_to_num(q64), k64, v64, table, lens, D ** -0.5, 0.0, bias.astype(np.float64))
+    assert (want[1][[0, 2]] == -np.inf).all()
+    for kw in ({}, dict(softcap=9.0)):
+        if masked == "bias" or kw:
+            kw["key_bias"] = _dev(bias)
+        if kw.get("softcap"):
+            want = oracle.paged_attn(np.nan_to_num(q64), k64, v64, table, lens, D ** -0.5, 9.0,
+                                     bias.astype(np.float64))
+        _all_plans(fk, q, k, v, table, lens, D,
+                   lambda got: _check_attn(got, want, dtype, D, kw.get("softcap", 0.0)), **kw)
+    # a query that is NaN and has keys is NaN, and no other request is
+    q2 = torch.zeros_like(q)
+    q2[1, 0, 0] = math.nan
+    out, lse = fk.fk_paged_attn(q2, k, v, _dev(table), _dev(np.array(lens, np.int32)), key_bias=_dev(bias),
+                                return_lse=True)
+    assert out[1, 0].isnan().all() and lse[1, 0].isnan()
+    assert not out[1, 1:].isnan().any() and not out[[0, 2, 3]].isnan().any() and not lse[[0, 2, 3]].isnan().any()
