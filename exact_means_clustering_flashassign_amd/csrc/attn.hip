@@ -320,6 +320,36 @@ template <int DT> __device__ __forceinline__ float prob(float x) {
   return x < -200.f ? 0.f : __builtin_amdgcn_ldexpf(fast_exp2(f), (int)n);
 }
 
+// Eight numbers x >= 0 as hi + lo in 16 bits each: hi is x rounded down, lo the rest to
+// nearest but at least the smallest number that a product does not flush, 2^-126 (bf16) or
+// 2^-24 (fp16, 2^-38 of the largest probability); x = 0 gives 0 and 0.
+template <int DT> struct Halves {
+  typedef typename Val<DT>::arith T;
+  typedef T T2 __attribute__((ext_vector_type(2)));
+  static constexpr float tiny = DT == FK_F16 ? 0x1p-24f : 0x1p-126f;
+  __device__ static __forceinline__ void split(const float (&x)[8], uint4& hi, uint4& lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = x[2 * i], b = x[2 * i + 1];
+      float ra, rb;
+      if constexpr (DT == FK_F16) {
+        const auto d = __builtin_amdgcn_cvt_pkrtz(a, b);
+        h[i] = __builtin_bit_cast(uint32_t, d);
+        ra = a - (float)d[0], rb = b - (float)d[1];
+      } else {
+        const uint32_t ua = __builtin_bit_cast(uint32_t, a), ub = __builtin_bit_cast(uint32_t, b);
+        h[i] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+        ra = a - __builtin_bit_cast(float, ua & 0xFFFF0000u);
+        rb = b - __builtin_bit_cast(float, ub & 0xFFFF0000u);
+      }
+      const T2 d = {(T)fmaxf(ra, a == 0.f ? 0.f : tiny), (T)fmaxf(rb, b == 0.f ? 0.f : tiny)};
+      l[i] = __builtin_bit_cast(uint32_t, d);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]), lo = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+};
+
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }
@@ -534,21 +564,17 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
       // Probabilities as the sum of two 16-bit numbers: one alone would round
       // each to 8 (bf16) or 11 bits, an error as large as the result's own
       // rounding. The second product rides on matrix units that are idle anyway.
-      typedef typename Val<DT>::arith T;
-      typedef T T8 __attribute__((ext_vector_type(8)));
+      // The first is rounded down and the second is above 0 where the probability is: an
+      // infinite value times 0 or a negative rest would be NaN or take the infinity off.
 #pragma unroll
       for (int y = 0; y < S::tiles / 2; ++y) {
         uint4 ph[HT], pl[HT];
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
-          T8 hi, lo;
+          float x[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float x = s[h][2 * y + (j >> 2)][j & 3];
-            hi[j] = (T)x;
-            lo[j] = (T)(x - (float)hi[j]);
-          }
-          ph[h] = __builtin_bit_cast(uint4, hi), pl[h] = __builtin_bit_cast(uint4, lo);
+          for (int j = 0; j < 8; ++j) x[j] = s[h][2 * y + (j >> 2)][j & 3];
+          Halves<DT>::split(x, ph[h], pl[h]);
         }
         auto pick = [&](int j, int u, int t) {       // element t of rows j (low half) and j + 1
           return __builtin_amdgcn_perm(word(vf[8 * y + j + 1][u], t >> 1),

@@ -3,7 +3,8 @@ against what the formula gives for them in IEEE arithmetic:
 
   * a key whose score is -inf has weight 0 and drops out: the result is the one
     without it (the oracle's, with that key masked);
-  * a request whose keys are all masked gives 0 and -inf, whatever its query holds.
+  * a request whose keys are all masked gives 0 and -inf, whatever its query holds;
+  * an infinite value gives an infinite element, a NaN one NaN, and the others stay as they are.
 
 Error bounds of the finite results are those of test_gpu_kv_cache.py.
 """
@@ -102,3 +103,30 @@ def test_nothing_left_whatever_the_query_holds(fk, dims, masked, dtype):
                                 return_lse=True)
     assert out[1, 0].isnan().all() and lse[1, 0].isnan()
     assert not out[1, 1:].isnan().any() and not out[[0, 2, 3]].isnan().any() and not lse[[0, 2, 3]].isnan().any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dims", DIMS, ids=[f"{a}x{b}d{d}" for a, b, d in DIMS])
+def test_infinite_and_nan_values_stay_in_their_element(fk, dims, dtype):
+    Hq, Hkv, D = dims
+    (q, k, v), (q64, k64, v64), table = _case(Hq, Hkv, D, dtype, LENS, D + 2)
+    q *= 0.125                                       # scores of a few tenths: no weight underflows
+    q64 = host_f64(q, dtype)
+    want = oracle.paged_attn(q64, k64, v64, table, LENS, D ** -0.5)
+    put = {0: (0, 1, 3, math.inf), 1: (table[1, 0], 4, D - 1, -math.inf), 2: (table[2, 40], 0, D // 2, math.nan)}
+    for page, tok, e, x in put.values():
+        v[page, tok, :, e] = x
+    for b in range(len(LENS)):
+        for at in range(0, LENS[b], 9):              # and, in one element, an infinity at many keys
+            v[table[b, at // 16], at % 16, :, 5] = math.inf
+
+    def check(got):
+        out = got[0].double().cpu().numpy()
+        for b, (_, _, e, x) in put.items():
+            assert np.isnan(out[b, :, e]).all() if x != x else (out[b, :, e] == x).all(), (b, e)
+            assert (out[b, :, 5] == np.inf).all(), b
+            out[b, :, [e, 5]] = want[0][b, :, [e, 5]]
+        fixed = to_dev(synthdata.to_storage(out.astype(np.float32), dtype), dtype)
+        _check_attn((fixed, got[1]), want, dtype, D, 0.0)
+
+    _all_plans(fk, q, k, v, table, LENS, D, check)
