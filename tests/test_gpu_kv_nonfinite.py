@@ -4,7 +4,8 @@ against what the formula gives for them in IEEE arithmetic:
   * a key whose score is -inf has weight 0 and drops out: the result is the one
     without it (the oracle's, with that key masked);
   * a request whose keys are all masked gives 0 and -inf, whatever its query holds;
-  * an infinite value gives an infinite element, a NaN one NaN, and the others stay as they are.
+  * an infinite value gives an infinite element, a NaN one NaN, and the others stay as they are;
+  * NaN in a key reaches its request and the query heads of its cache head, and no others.
 
 Error bounds of the finite results are those of test_gpu_kv_cache.py.
 """
@@ -130,3 +131,26 @@ def test_infinite_and_nan_values_stay_in_their_element(fk, dims, dtype):
         _check_attn((fixed, got[1]), want, dtype, D, 0.0)
 
     _all_plans(fk, q, k, v, table, LENS, D, check)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dims", DIMS, ids=[f"{a}x{b}d{d}" for a, b, d in DIMS])
+def test_nan_keys_reach_their_request_and_head_only(fk, dims, dtype):
+    Hq, Hkv, D = dims
+    (q, k, v), (q64, k64, v64), table = _case(Hq, Hkv, D, dtype, LENS, D + 3)
+    want = oracle.paged_attn(q64, k64, v64, table, LENS, D ** -0.5)
+    k[table[2, 3], 7, Hkv - 1, D - 1] = math.nan
+
+    def check(got):
+        G = Hq // Hkv
+        assert got[0][2, -G:].isnan().all() and got[1][2, -G:].isnan().all()
+        out, lse = got[0].clone(), got[1].clone()
+        out[2, -G:], lse[2, -G:] = (_like(w[2, -G:], t) for w, t in zip(want, (out, lse)))
+        _check_attn((out, lse), want, dtype, D, 0.0)
+
+    _all_plans(fk, q, k, v, table, LENS, D, check)
+
+
+def _like(a, t):
+    import torch
+    return torch.from_numpy(a).to(t.dtype).to(t.device)
