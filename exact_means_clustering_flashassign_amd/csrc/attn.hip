@@ -279,6 +279,11 @@ __device__ __forceinline__ int len_of(const AttnArgs& a, int64_t b) {
   return n <= 0 ? 0 : (n < cap ? n : (int)cap);
 }
 
+// Steps of a request; a length may be 2^31 - 1, so the sum is unsigned.
+template <int KEYS> __device__ __forceinline__ int steps_of(int len) {
+  return (int)(((uint32_t)len + KEYS - 1) / KEYS);
+}
+
 template <int DT> struct Mfma16;
 template <> struct Mfma16<FK_F16> {
   __device__ static __forceinline__ floatx4_t run(uint4 a, uint4 b, floatx4_t c) {
@@ -628,7 +633,7 @@ struct Start {
 
 template <int KEYS>
 __device__ __forceinline__ int64_t cost_of(const AttnArgs& a, const Plan& p, int64_t b) {
-  return p.team + (len_of(a, b) + KEYS - 1) / KEYS;
+  return p.team + steps_of<KEYS>(len_of(a, b));
 }
 
 template <int KEYS>
@@ -736,7 +741,7 @@ __global__ __launch_bounds__(W * 64, W == kWaves ? waves_per_simd(DP) : W / 4) v
   const bool idle = !cut && part >= a.B;     // a wave past the last request
   for (int64_t b = st.b, at = st.before; at < st.hi;) {
     const int len = idle ? 0 : __builtin_amdgcn_readfirstlane(len_of(a, b));
-    const int steps = (len + S::keys - 1) / S::keys;
+    const int steps = steps_of<S::keys>(len);
     int t0 = 0, t1 = steps;
     if (cut) {
       const int64_t first = at + p.team;
