@@ -445,7 +445,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Plan& p, int64_t
     const bool live = (uint32_t)pg < (uint32_t)c.pages;
     float bias = 0.f;
     if (has_bias) {
-      const uint32_t key = (uint32_t)st * S::keys + kl;
+      // (the last one's place for a key past the end: one past 2^31 would not divide)
+      const uint32_t key = min((uint32_t)st * S::keys + kl, (uint32_t)len - 1);
       const uint32_t tok = key - div_by(key, p.page) * p.page.d;
       bias = *(gptr_f32)(bbase + (uint64_t)((live ? pg : 0) * c.bias_stride[0] + tok * c.bias_stride[1]) * 4);
     }

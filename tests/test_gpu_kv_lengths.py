@@ -41,3 +41,13 @@ def _longest(fk, dtype, live=None):
 def test_longest_request(fk, dtype):
     import torch
     _longest(fk, getattr(torch, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["float16", "float32"])
+def test_longest_request_with_bias(fk, dtype):
+    """The bias of the steps asked for beyond the end is read inside the page."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(4)
+    live = torch.rand(PAGE, device="cuda", generator=g) < 0.5
+    live[0] = True
+    _longest(fk, getattr(torch, dtype), live)
