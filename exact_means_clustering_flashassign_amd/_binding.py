@@ -335,6 +335,7 @@ class _TorchCalls:
         self.i32, self.f32, self.u8 = torch.int32, torch.float32, torch.uint8
         self.codes = {torch.float32: FK_F32, torch.float16: FK_F16, torch.bfloat16: FK_BF16}
         self.stream = torch._C._cuda_getCurrentRawStream
+        self.grad = torch.is_grad_enabled
 
 
 def _calls():
@@ -373,6 +374,13 @@ def _rows(t, name, dtype, dims, index):
                          f"on cuda:{index}, got {t.dtype} {tuple(t.shape)} strides {s} on "
                          f"{t.device}")
     return s
+
+
+def _no_grad(t, name):
+    """Parameters may be given where no gradient is asked for; else it would be lost."""
+    if t.requires_grad and _tc.grad():
+        raise ValueError(f"{name} requires grad: the call has no backward pass, detach it or use "
+                         f"torch.no_grad()")
 
 
 def _kv_cache(k_cache, v_cache, key_bias, dtype, heads, dim, index):
@@ -445,6 +453,7 @@ def fk_qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-
     """q (T,Hq,D), k and v (T,Hkv,D): per-head RMS norm with the weights (D)
     (none: no norm) and rotation of the first rot elements by rope (max_pos,
     rot) fp32, cosines then sines, at positions (T) int32 (none: no rotation).
+    Weights and rope that require grad are taken under torch.no_grad() only.
     With slots (T) int32, keys and values are stored in k_cache and v_cache
     (pages, page, Hkv, D), with a key_bias (pages, page, Hkv) of 0. Returns
     (q_out, k_out); k_out is None with a cache unless given."""
@@ -486,12 +495,15 @@ def fk_qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-
     if q_weight is not None:
         p_qw = _on(q_weight, "q_weight", dt, (D,), index)
         p_kw = _on(k_weight, "k_weight", dt, (D,), index)
+        _no_grad(q_weight, "q_weight")
+        _no_grad(k_weight, "k_weight")
     rot = max_pos = 0
     if rope is not None:
         if rope.dim() != 2 or positions is None:
             raise ValueError("rope must be (max_pos, rot), with positions")
         max_pos, rot = rope.shape
         rp = _on(rope, "rope", tc.f32, (max_pos, rot), index)
+        _no_grad(rope, "rope")
         pp = _on(positions, "positions", tc.i32, (T,), index)
     st = _lib.fk_qk_norm_rope(
         q.data_ptr(), _pack2(sq[0], sq[1]), k.data_ptr(), _pack2(sk[0], sk[1]), vp, sv, code, T,
