@@ -52,7 +52,8 @@ class ClusteredKVCache:
     def append(self, q, k, v, new, q_weight=None, k_weight=None, eps: float = 1e-6, rope=None,
                interleaved: bool = False):
         """Store a step's tokens: new[b] tokens of request b, in order of requests, as
-        q (T,Hq,D), k and v (T,Hkv,D). Returns the normed and rotated queries."""
+        q (T,Hq,D), k and v (T,Hkv,D). Returns the normed and rotated queries. Positions
+        count all tokens a request has seen, and have to be inside rope's rows."""
         torch = fk._torch()
         T = int(q.shape[0])
         if len(new) != len(self.lens) or min(new) < 0 or sum(new) != T:
@@ -60,6 +61,9 @@ class ClusteredKVCache:
         lens = [a + n for a, n in zip(self.lens, new)]
         if max(lens) > self.max_len:
             raise ValueError(f"a request would hold {max(lens)} tokens, more than {self.max_len}")
+        most = max((s + n for s, n in zip(self.seen, new) if n), default=0)
+        if rope is not None and most > rope.shape[0]:
+            raise ValueError(f"a request would have {most} positions, more than rope's {rope.shape[0]}")
         taken = sum(self._pages(b) - self._pages(a) for a, b in zip(self.lens, lens))
         if taken > self.free.numel():
             raise RuntimeError(f"{taken} pages needed, {self.free.numel()} free")

@@ -108,3 +108,24 @@ def test_refused_append_then_steps_match_the_oracle(fk):
         _consistent(c, 12)
         _check(c, q, got, "f16", D)
     assert c.lens == [22, 9]
+
+
+def test_positions_past_the_rotation_table_are_refused(cpu_cache):
+    """Positions go on counting what compression took out: they can pass max_len."""
+    import torch
+
+    c = cpu_cache(2, 12, 4, 2, 8, 20)
+    x, rope = torch.zeros(9, 2, 8), torch.zeros(24, 8)
+    c.append(x[:9], x[:9], x[:9], [9, 0], rope=rope)
+    c.lens[0], c.lens_dev[0], c.shift[0] = 3, 3, 6       # as a compression leaves it: 3 held of 9 seen
+    c.free = torch.cat([c.free, c.table[0, 1:3]])
+    c.append(x[:9], x[:9], x[:9], [9, 0], rope=rope)
+    assert _store.positions == list(range(9, 18)) and c.seen == [18, 0]
+    before = _books(c)
+    with pytest.raises(ValueError, match="25 positions, .* 24"):
+        c.append(x[:7], x[:7], x[:7], [7, 0], rope=rope)
+    assert _same(before, _books(c))
+    c.append(x[:6], x[:6], x[:6], [6, 0], rope=rope)     # the last row of the table
+    assert _store.positions == list(range(18, 24))
+    c.append(x[:8], x[:8], x[:8], [0, 8], rope=rope)     # the full request gets nothing: fine
+    c.append(x[:1], x[:1], x[:1], [1, 0])                # and no rotation needs no table
