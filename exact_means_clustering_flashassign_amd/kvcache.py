@@ -122,3 +122,11 @@ class ClusteredKVCache:
         self.shift[request] = self.seen[request] - held
         self.lens[request], self.centres[request] = held, c0 + n_clusters
         return held
+
+    def release(self, request: int) -> None:
+        """End a request: its pages go back to the list, and its row is empty for another."""
+        torch = fk._torch()
+        self.free = torch.cat([self.free, self.table[request, :self._pages(self.lens[request])]])
+        self.table[request] = -1
+        self.lens_dev[request] = self.shift[request] = 0
+        self.lens[request] = self.seen[request] = self.centres[request] = 0

@@ -129,3 +129,47 @@ def test_positions_past_the_rotation_table_are_refused(cpu_cache):
     assert _store.positions == list(range(18, 24))
     c.append(x[:8], x[:8], x[:8], [0, 8], rope=rope)     # the full request gets nothing: fine
     c.append(x[:1], x[:1], x[:1], [1, 0])                # and no rotation needs no table
+
+
+def test_release_gives_the_pages_back(cpu_cache):
+    import torch
+
+    c = cpu_cache(2, 6, 4, 2, 8, 20)
+    x = torch.arange(20 * 2 * 8, dtype=torch.float32).view(20, 2, 8)
+    for turn in range(4):                                # more tokens in all than there are pages for
+        c.append(x[:14], x[:14], x[:14], [13, 1])
+        _consistent(c, 6)
+        c.release(0)
+        assert c.lens == [0, turn + 1] and c.seen == [0, turn + 1]
+        assert (c.table[0] == -1).all()
+        _consistent(c, 6)
+    c.lens[1], c.centres[1], c.shift[1] = 4, 2, 3        # as a compression leaves it
+    c.lens_dev[1] = 4
+    c.release(1)
+    assert c.lens == c.seen == c.centres == [0, 0] and c.shift.tolist() == [0, 0]
+    _consistent(c, 6)
+    c.append(x[:2], x[:2], x[:2], [0, 2], rope=torch.zeros(5, 8))
+    assert _store.positions == [0, 1]
+    c.release(0)                                         # nothing held: nothing happens
+    _consistent(c, 6)
+
+
+@pytest.mark.gpu
+def test_release_then_another_request_matches_the_oracle(fk):
+    import torch
+    from test_gpu_kv_path import _check
+
+    H, D, page = 2, 64, 8
+    c = fk.ClusteredKVCache(2, 14, page, H, D, 60, torch.float16)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for turn in range(3):
+        x = torch.randn(70 - turn, 3 * H, D, device="cuda", generator=g).half()
+        c.append(x[:, :H], x[:, H:2 * H], x[:, 2 * H:], [60 - turn, 10])
+        if turn == 0:
+            c.compress(1, 4, keep=3, niter=2)
+        _consistent(c, 14)
+        q = torch.randn(2, 2 * H, D, device="cuda", generator=g).half()
+        _check(c, q, c.attend(q, return_lse=True), "f16", D)
+        c.release(0)
+        out, lse = c.attend(q, return_lse=True)
+        assert (out[0] == 0).all() and (lse[0] == -float("inf")).all()
