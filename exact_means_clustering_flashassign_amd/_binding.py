@@ -376,6 +376,37 @@ def _rows(t, name, dtype, dims, index):
     return s
 
 
+def _apart(outs, ins):
+    """Refuses outputs (name, address, end) that overlap one another or an input (name, address,
+    end of its extent, and the tensor where that may have gaps)."""
+    for i, (name, lo, hi) in enumerate(outs):
+        for other, a, b in outs[:i]:
+            if lo < b and a < hi:
+                raise ValueError(f"{name} overlaps {other}")
+        for other, a, b, *t in ins:
+            if lo < b and a < hi and (not t or _meets(lo - a, hi - a, t[0])):
+                raise ValueError(f"{name} overlaps {other}, which the call reads")
+
+
+def _meets(lo, hi, t):
+    """Whether bytes lo to hi from a tensor's address hold any of its elements."""
+    size = t.element_size()
+
+    def within(lo, hi, axes, extent):
+        if not axes:
+            return lo < size and hi > 0
+        (s, n), *rest = axes
+        extent -= (n - 1) * s                    # of one index
+        first = max(0, (lo - extent) // s + 1) if s else 0
+        last = min(n - 1, (hi - 1) // s) if s else 0
+        # three indices in a row: the middle one lies between lo and hi whole
+        return last - first >= 2 or any(within(lo - i * s, hi - i * s, rest, extent)
+                                        for i in range(first, last + 1))
+
+    axes = sorted(((s * size, n) for s, n in zip(t.stride(), t.shape) if n > 1), reverse=True)
+    return lo < hi and within(lo, hi, axes, sum((n - 1) * s for s, n in axes) + size)
+
+
 def _no_grad(t, name):
     """Parameters may be given where no gradient is asked for; else it would be lost."""
     if t.requires_grad and _tc.grad():
@@ -412,7 +443,8 @@ def fk_page_tables(len_old, len_new, free_pages, page: int, width: int, tokens: 
     holds the pages they have (None: none). All int32 on the GPU. Returns
     (table (B,width), lens (B), cu_tokens (B+1), cu_pages (B+1), slots (tokens),
     positions (tokens)), views of one buffer; `out`: those six tensors, to
-    write into."""
+    write into: the first may be `table` itself, else none may overlap
+    another or an input."""
     tc = _tc or _calls()
     i32, index = tc.i32, _gpu_index(len_old, "len_old")
     B = len_old.numel()
@@ -440,6 +472,12 @@ def fk_page_tables(len_old, len_new, free_pages, page: int, width: int, tokens: 
         shapes = ((B, width), (B,), (B + 1,), (B + 1,), (tokens,), (tokens,))
         ps = [_on(t, f"out[{i}]", i32, s, index) for i, (t, s) in enumerate(zip(out, shapes))]
         out = tuple(out)
+        ins = [("len_old", p_old, p_old + 4 * B), ("len_new", p_new, p_new + 4 * B),
+               ("free_pages", p_free, p_free + 4 * n_free)]
+        if p_in is not None and (p_in != ps[0] or width_in != width):
+            ins.append(("table", p_in, p_in + 4 * B * width_in))
+        _apart([(f"out[{i}]", p, p + 4 * t.numel()) for i, (p, t) in enumerate(zip(ps, out))
+                if t.numel()], ins)
     st = _lib.fk_page_tables(p_old, p_new, p_in, width_in, p_free, n_free, B, page, width, tokens,
                              *ps, tc.stream(index))
     if st:

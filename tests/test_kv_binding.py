@@ -1,0 +1,78 @@
+"""What the paged-cache calls' Python side refuses beyond types and shapes."""
+import pytest
+
+
+@pytest.mark.gpu
+def test_trained_weights_are_refused_unless_no_gradient_is_asked_for(fk):
+    import torch
+
+    q, k = torch.randn(3, 4, 64, device="cuda"), torch.randn(3, 2, 64, device="cuda")
+    w = torch.rand(64, device="cuda")
+    par = torch.nn.Parameter(w.clone())
+    rope, pos = torch.rand(9, 64, device="cuda"), torch.arange(3, dtype=torch.int32, device="cuda")
+    turn = torch.nn.Parameter(rope.clone())
+    want = fk.fk_qk_norm_rope(q, k, None, w, w, rope=rope, positions=pos)
+    for ws, r, name in (((par, w), rope, "q_weight"), ((w, par), rope, "k_weight"), ((w, w), turn, "rope")):
+        with pytest.raises(ValueError, match=f"{name} requires grad"):
+            fk.fk_qk_norm_rope(q, k, None, *ws, rope=r, positions=pos)
+        with torch.no_grad():
+            got = fk.fk_qk_norm_rope(q, k, None, *ws, rope=r, positions=pos)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_meets_is_exact():
+    """Overlap of a byte range with a strided tensor, against marks on every byte."""
+    import random
+
+    import torch
+    from exact_means_clustering_flashassign_amd._binding import _meets
+
+    rng, buf = random.Random(1), torch.zeros(4000, dtype=torch.int16)
+    for _ in range(400):
+        shape = [rng.randint(1, 4) for _ in range(3)]
+        inner = [1, shape[2] + rng.randint(0, 3)]
+        inner.append((shape[1] - 1) * inner[1] + shape[2] + rng.randint(0, 40))
+        strides = [inner[2], inner[1], 1]
+        if rng.random() < 0.3:                           # heads outside tokens
+            shape[0], shape[1], strides[0], strides[1] = shape[1], shape[0], strides[1], strides[0]
+        t = buf.as_strided(shape, strides)
+        used = torch.zeros(4000, dtype=torch.bool)
+        used.as_strided(shape, strides).fill_(True)
+        used = used.repeat_interleave(2)
+        lo = rng.randint(-30, 300)
+        hi = lo + rng.randint(0, 60)
+        assert _meets(lo, hi, t) == bool(used[max(lo, 0):max(hi, 0)].any()), (shape, strides, lo, hi)
+
+
+def _tables(fk, B=40, page=4, width=9):
+    import torch
+
+    i32 = dict(dtype=torch.int32, device="cuda")
+    old, new = torch.arange(B, **i32) % 20, torch.arange(B, **i32) % 7
+    T = int(new.sum())
+    free, table = torch.arange(500, **i32), torch.full((B, width), 3, **i32)
+    out = [torch.empty(s, **i32) for s in ((B, width), (B,), (B + 1,), (B + 1,), (T,), (T,))]
+    return (old, new, free, page, width, T), table, out
+
+
+@pytest.mark.gpu
+def test_page_tables_outputs_apart(fk):
+    import torch
+
+    args, table, out = _tables(fk)
+    want = fk.fk_page_tables(*args, table=table)
+    assert all(torch.equal(a, b) for a, b in zip(want, fk.fk_page_tables(*args, table=table, out=out)))
+    big = torch.zeros(2000, dtype=torch.int32, device="cuda")
+    B, T, width = 40, args[5], 9
+    shifted = big[:B * width + 7]
+    for bad, kw, name in [
+            ({1: args[0]}, {}, r"out\[1\] overlaps len_old"), ({1: args[1]}, {}, r"out\[1\] overlaps len_new"),
+            ({4: args[2][:T]}, {}, r"out\[4\] overlaps free_pages"), ({5: out[4]}, {}, r"out\[5\] overlaps out\[4\]"),
+            ({2: big[:B + 1], 3: big[B:2 * B + 1]}, {}, r"out\[3\] overlaps out\[2\]"),
+            ({0: shifted[7:].view(B, width)}, dict(table=shifted[:B * width].view(B, width)), r"out\[0\] overlaps table"),
+            ({1: table.view(-1)[:B]}, {}, r"out\[1\] overlaps table")]:
+        outs = [bad.get(i, t) for i, t in enumerate(out)]
+        with pytest.raises(ValueError, match=name):
+            fk.fk_page_tables(*args, **dict(dict(table=table), **kw), out=outs)
+    got = fk.fk_page_tables(*args, table=table, out=[table] + out[1:])
+    assert got[0] is table and all(torch.equal(a, b) for a, b in zip(want, got))
