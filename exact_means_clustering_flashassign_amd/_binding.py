@@ -388,6 +388,14 @@ def _apart(outs, ins):
                 raise ValueError(f"{name} overlaps {other}, which the call reads")
 
 
+def _span(name, t, stride, size):
+    """An input for _apart with its extent; its gaps are looked into where that is met."""
+    p = t.data_ptr()
+    if not t.numel():
+        return name, p, p
+    return name, p, p + (sum((n - 1) * s for n, s in zip(t.shape, stride)) + 1) * size, t
+
+
 def _meets(lo, hi, t):
     """Whether bytes lo to hi from a tensor's address hold any of its elements."""
     size = t.element_size()
@@ -494,7 +502,8 @@ def fk_qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-
     Weights and rope that require grad are taken under torch.no_grad() only.
     With slots (T) int32, keys and values are stored in k_cache and v_cache
     (pages, page, Hkv, D), with a key_bias (pages, page, Hkv) of 0. Returns
-    (q_out, k_out); k_out is None with a cache unless given."""
+    (q_out, k_out); k_out is None with a cache unless given. q_out and k_out
+    given may not overlap each other, the cache or an input (not even q itself)."""
     tc = _tc or _calls()
     dt, index = q.dtype, _gpu_index(q, "q")
     code = tc.codes.get(dt)
@@ -520,13 +529,17 @@ def fk_qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-
         raise ValueError("v and the cache need slots")
     elif k_out is None:
         k_out = tc.empty((T, Hkv, D), dtype=dt, device=q.device)
-    if k_out is not None:
+        p_ko = k_out.data_ptr()
+    given = []                           # outputs of the caller's
+    if k_out is not None and p_ko is None:
         p_ko = _on(k_out, "k_out", dt, (T, Hkv, D), index)
+        given.append(("k_out", p_ko, k_out))
     if q_out is None:
         q_out = tc.empty((T, Hq, D), dtype=dt, device=q.device)
         p_qo = q_out.data_ptr()
     else:
         p_qo = _on(q_out, "q_out", dt, (T, Hq, D), index)
+        given.append(("q_out", p_qo, q_out))
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
     p_qw = p_kw = rp = pp = None
@@ -543,6 +556,19 @@ def fk_qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-
         rp = _on(rope, "rope", tc.f32, (max_pos, rot), index)
         _no_grad(rope, "rope")
         pp = _on(positions, "positions", tc.i32, (T,), index)
+    if given:
+        e = q.element_size()
+        outs = [(n, p, p + t.numel() * e) for n, p, t in given if t.numel()]
+        ins = [_span("q", q, sq, e), _span("k", k, sk, e)]
+        if cache:
+            ins += [_span("v", v, v.stride(), e), ("slots", sp, sp + 4 * T),
+                    _span("k_cache", k_cache, k_cache.stride(), e),
+                    _span("v_cache", v_cache, v_cache.stride(), e)]
+        if p_qw:
+            ins += [("q_weight", p_qw, p_qw + D * e), ("k_weight", p_kw, p_kw + D * e)]
+        if rp:
+            ins += [("rope", rp, rp + 4 * rope.numel()), ("positions", pp, pp + 4 * T)]
+        _apart(outs, ins)
     st = _lib.fk_qk_norm_rope(
         q.data_ptr(), _pack2(sq[0], sq[1]), k.data_ptr(), _pack2(sk[0], sk[1]), vp, sv, code, T,
         Hq, Hkv, D, p_qw, p_kw, eps, rp, max_pos, rot, interleaved, pp, sp, cache,

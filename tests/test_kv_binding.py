@@ -76,3 +76,38 @@ def test_page_tables_outputs_apart(fk):
             fk.fk_page_tables(*args, **dict(dict(table=table), **kw), out=outs)
     got = fk.fk_page_tables(*args, table=table, out=[table] + out[1:])
     assert got[0] is table and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 33])
+def test_norm_rope_outputs_apart(fk, D):
+    import torch
+
+    T, Hq, H, page = 3, 4, 2, 4
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=gen)      # noqa: E731
+    qkv, w, rot = rnd(T, Hq + 2 * H, D), rnd(D), D // 2 * 2
+    rope, pos = rnd(T * Hq * D // rot + 2, rot), torch.arange(T, dtype=torch.int32, device="cuda")
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + H], qkv[:, Hq + H:]
+    kc, vc = torch.zeros(8, page, H, D, device="cuda"), torch.zeros(8, page, H, D, device="cuda")
+    kw = dict(rope=rope, positions=pos, slots=torch.arange(T, dtype=torch.int32, device="cuda"), k_cache=kc, v_cache=vc)
+    want = fk.fk_qk_norm_rope(q, k, v, w, w, **kw, k_out=torch.empty(T, H, D, device="cuda"))
+    qc, n, m = q.contiguous(), T * Hq * D, T * H * D
+    flat = qkv.view(-1)
+    one = torch.empty(n + m - 1, device="cuda")
+    for q_, bad, name in [(qc, dict(q_out=qc), "q_out overlaps q,"), (q, dict(q_out=flat[:n].view(T, Hq, D)), "q_out overlaps"),
+                          (q, dict(k_out=flat[-m:].view(T, H, D)), "k_out overlaps"),
+                          (q, dict(q_out=rope.view(-1)[:n].view(T, Hq, D)), "q_out overlaps rope"),
+                          (q, dict(q_out=kc.view(-1)[:n].view(T, Hq, D)), "q_out overlaps k_cache"),
+                          (q, dict(k_out=vc.view(-1)[-m:].view(T, H, D)), "k_out overlaps v_cache"),
+                          (q, dict(q_out=one[:n].view(T, Hq, D), k_out=one[-m:].view(T, H, D)), "overlaps k_out")]:
+        with pytest.raises(ValueError, match=name):
+            fk.fk_qk_norm_rope(q_, k, v, w, w, **kw, **bad)
+    # outputs in the gaps of an input are apart from it
+    row = Hq * D + T * Hq * D
+    buf = torch.zeros(T * row, device="cuda")
+    wide = buf.as_strided((T, Hq, D), (row, D, 1))
+    wide.copy_(q)
+    got = fk.fk_qk_norm_rope(wide, k, v, w, w, **kw, q_out=buf[Hq * D:row].view(T, Hq, D),
+                             k_out=buf[row + Hq * D:row + Hq * D + m].view(T, H, D))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(wide, q)
