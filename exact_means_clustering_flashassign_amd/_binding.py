@@ -594,7 +594,8 @@ def fk_paged_attn(q, k_cache, v_cache, table, lens, scale: Optional[float] = Non
     of k_cache and v_cache (pages, page, Hkv, D) found through table (B,W)
     int32: softmax(softcap(scale q.k) + key_bias) v, with scale 1/sqrt(D) by
     default. Returns out (B,Hq,D), and with return_lse (or lse given) the
-    natural log of the softmax's sum, (B,Hq) fp32."""
+    natural log of the softmax's sum, (B,Hq) fp32. out, lse and ws given may not
+    overlap each other or an input, but out may be a contiguous q itself."""
     tc = _tc or _calls()
     dt, index = q.dtype, _gpu_index(q, "q")
     code = tc.codes.get(dt)
@@ -620,6 +621,9 @@ def fk_paged_attn(q, k_cache, v_cache, table, lens, scale: Optional[float] = Non
         p_out = out.data_ptr()
     else:
         p_out = _on(out, "out", dt, (B, Hq, D), index)
+        if p_out != q.data_ptr() or not q.is_contiguous():
+            _apart([("out", p_out, p_out + out.numel() * q.element_size())],
+                   [_span("q", q, sq, q.element_size())])
     p_lse = None
     if lse is not None:
         p_lse = _on(lse, "lse", tc.f32, (B, Hq), index)

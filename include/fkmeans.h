@@ -344,6 +344,8 @@ fk_status_t fk_qk_norm_rope(const void* q, const int64_t q_stride[2], const void
  *             is split; a longer request is still computed in full.
  *   out (B,Hq,D) dt out; lse (B,Hq) fp32 out, may be null.
  *   ws: fk_workspace_size_attn(dt, B, Hq, Hkv, D) bytes, 256-byte aligned.
+ * out, lse and ws may not overlap each other or an input, but out may be q itself
+ * where q is contiguous.
  * D <= 1024 (FK_ERR_UNSUPPORTED above). Rows of at most 256 elements that
  * start at multiples of 16 bytes and hold whole 16-byte units run on the
  * matrix cores, others on a path several times slower. The same arguments give

@@ -111,3 +111,31 @@ def test_norm_rope_outputs_apart(fk, D):
     got = fk.fk_qk_norm_rope(wide, k, v, w, w, **kw, q_out=buf[Hq * D:row].view(T, Hq, D),
                              k_out=buf[row + Hq * D:row + Hq * D + m].view(T, H, D))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(wide, q)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 33])
+def test_paged_attn_in_place_or_apart(fk, D):
+    """out over q: the same bits where it is q, refused where it is a part of it."""
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    B, Hq, H, page, width = 3, 8, 2, 16, 400
+    kc, vc = (torch.randn(60, page, H, D, device="cuda", generator=gen).half() for _ in range(2))
+    table = torch.randint(0, 60, (B, width), device="cuda", generator=gen, dtype=torch.int32)
+    lens = torch.tensor([width * page, 0, 77], dtype=torch.int32, device="cuda")
+    buf = torch.randn((2 * B + 1) * Hq * D, device="cuda", generator=gen).half()
+    n = B * Hq * D
+    q = buf[:n].view(B, Hq, D)
+    for hint in (0, 40, 700):
+        want = fk.fk_paged_attn(q, kc, vc, table, lens, max_len=hint, return_lse=True)
+        mine = q.clone()
+        got = fk.fk_paged_attn(mine, kc, vc, table, lens, max_len=hint, out=mine, return_lse=True)
+        assert got[0] is mine and torch.equal(mine, want[0]) and torch.equal(got[1], want[1])
+    for q_, out in ((q, buf[D:n + D].view(B, Hq, D)), (buf.as_strided((B, Hq, D), (Hq * D, D, 1), 8), buf[:n].view(B, Hq, D)),
+                    (buf.as_strided((B, Hq, D), (2 * Hq * D, D, 1)), q)):
+        with pytest.raises(ValueError, match="out overlaps q"):
+            fk.fk_paged_attn(q_, kc, vc, table, lens, out=out)
+    gaps = buf.as_strided((2, Hq, D), (4 * Hq * D, D, 1))
+    got = fk.fk_paged_attn(gaps, kc, vc, table[:2], lens[:2], out=buf[Hq * D:3 * Hq * D].view(2, Hq, D))
+    assert torch.equal(got, fk.fk_paged_attn(gaps, kc, vc, table[:2], lens[:2]))
