@@ -500,8 +500,9 @@ def fk_qk_norm_rope(q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-
     (none: no norm) and rotation of the first rot elements by rope (max_pos,
     rot) fp32, cosines then sines, at positions (T) int32 (none: no rotation).
     Weights and rope that require grad are taken under torch.no_grad() only.
-    With slots (T) int32, keys and values are stored in k_cache and v_cache
-    (pages, page, Hkv, D), with a key_bias (pages, page, Hkv) of 0. Returns
+    With slots (T) int32, distinct where they are inside the cache, keys and
+    values are stored in k_cache and v_cache (pages, page, Hkv, D), with a
+    key_bias (pages, page, Hkv) of 0; others are skipped. Returns
     (q_out, k_out); k_out is None with a cache unless given. q_out and k_out
     given may not overlap each other, the cache or an input (not even q itself)."""
     tc = _tc or _calls()

@@ -314,8 +314,9 @@ fk_status_t fk_page_tables(const int32_t* len_old, const int32_t* len_new,
  *   q_out (T,Hq,D) dt out; k_out (T,Hkv,D) dt out, may be null.
  *   slots (T) int32, cache (host struct): keys and values (and, where the cache
  *             has one, a key_bias of 0) of token t go to slots[t]; a slot
- *             outside the cache is skipped. Equal slots give either token's
- *             rows. Both null, and v, to keep nothing.
+ *             outside the cache is skipped. Slots inside it have to differ:
+ *             rows of equal ones end up with elements of either token, key
+ *             and value each for itself. Both null, and v, to keep nothing.
  * Outputs may not overlap inputs. rot even, 0 <= rot <= D; eps >= 0 and finite.
  */
 fk_status_t fk_qk_norm_rope(const void* q, const int64_t q_stride[2], const void* k,
