@@ -1,11 +1,12 @@
-"""Paged attention where keys, values and queries that count are infinite or NaN,
-against what the formula gives for them in IEEE arithmetic:
+"""Paged attention, and norm + rotation, where what counts is infinite or NaN, against
+what the formulas give for it in IEEE arithmetic:
 
   * a key whose score is -inf has weight 0 and drops out: the result is the one
     without it (the oracle's, with that key masked);
   * a request whose keys are all masked gives 0 and -inf, whatever its query holds;
   * an infinite value gives an infinite element, a NaN one NaN, and the others stay as they are;
-  * NaN in a key reaches its request and the query heads of its cache head, and no others.
+  * NaN in a key reaches its request and the query heads of its cache head, and no others;
+  * a row that is not finite spoils itself, unnormed only its pairs, and values keep their bits.
 
 Error bounds of the finite results are those of test_gpu_kv_cache.py.
 """
@@ -154,3 +155,40 @@ def test_nan_keys_reach_their_request_and_head_only(fk, dims, dtype):
 def _like(a, t):
     import torch
     return torch.from_numpy(a).to(t.dtype).to(t.device)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(128, 128, False), (128, 12, False), (96, 40, True), (33, 20, False), (64, 0, False)],
+                         ids=["whole", "exchange", "sides", "odd", "none"])
+def test_rotation_of_rows_that_are_not_finite(fk, shape, dtype):
+    """Infinities and NaN stay in their row, and unnormed in their pair; values keep their bits."""
+    import torch
+
+    D, rot, inter = shape
+    rng = np.random.default_rng(D + rot)
+    T, Hq, Hkv = 9, 5, 2
+    x = to_dev(_rand(rng, (T, Hq + 2 * Hkv, D), dtype), dtype)
+    bad = x.clone()
+    bad[2, 1, 1], bad[4, 3, D - 1], bad[7, Hq, 0], bad[3, -1, 2] = math.nan, math.inf, -math.inf, math.nan
+    w = to_dev(_rand(rng, D, dtype), dtype)
+    kw = dict(interleaved=inter, slots=_dev(np.arange(T, dtype=np.int32)))
+    if rot:
+        kw.update(rope=_dev(rng.uniform(0.2, 0.9, (T, rot)).astype(np.float32)),
+                  positions=_dev(np.arange(T, dtype=np.int32)))
+    for ws in ((w, w), (None, None)):
+        res = []
+        for src in (x, bad):
+            kc, vc = (torch.zeros(T, 1, Hkv, D, dtype=x.dtype, device="cuda") for _ in range(2))
+            q, _ = fk.fk_qk_norm_rope(src[:, :Hq], src[:, Hq:Hq + Hkv], src[:, Hq + Hkv:], None, None, 1e-6,
+                                      k_cache=kc, v_cache=vc, **kw) if ws[0] is None else \
+                fk.fk_qk_norm_rope(src[:, :Hq], src[:, Hq:Hq + Hkv], src[:, Hq + Hkv:], *ws, k_cache=kc, v_cache=vc, **kw)
+            res.append(torch.cat([q, kc[:, 0], vc[:, 0]], 1))
+        same = (res[0] == res[1])
+        rows = {(2, 1): 1, (4, 3): D - 1, (7, Hq): 0, (3, Hq + 2 * Hkv - 1): 2}
+        for (t, h), e in rows.items():
+            assert not res[1][t, h, e].isfinite()
+            if ws[0] is None:                            # the element and its partner at most
+                assert (~same[t, h]).sum() <= 2
+            same[t, h] = True
+        assert same.all()
+        assert torch.equal(res[1][:, Hq + Hkv:].isnan(), bad[:, Hq + Hkv:].isnan())
