@@ -196,8 +196,9 @@ int64_t longest(const AttnArgs& a) {
 // A wave's step is 32 keys (fp32: 16). The next step's keys are asked for as soon as the
 // scores are out of the registers they sit in, the next values after the last product with
 // these, so that one of the two is always on its way without a second set of
-// registers; 8 to 12 waves a CU keep 128 KB and more in flight. A step of 16 KB costs about
-// 254 VALU and 24 matrix instructions, an eighth of the time its bytes take.
+// registers: 64 to 128 KB in flight a CU for 8 waves of 128-element rows, 48 to 96 for 12
+// of 64. A step of 16 KB costs about 280 VALU and 24 matrix instructions, a fifth of the
+// time its bytes take.
 // Measured: 32 requests of 2048 to 65536 keys, 8 heads of 128 bf16, 4.43 GB, 671 us or 6.6
 // TB/s (a large copy reads and writes 4.8 on the same card).
 constexpr int kHeadTile = 16;
@@ -239,7 +240,7 @@ __device__ __forceinline__ uint4 load16(uint64_t addr) {
 // A load of n = 16, 8 or 4 bytes into the first words. STREAM: bytes that no one else
 // reads are marked so and do not push out of L2 what others will read again (the 4.43 GB
 // above 815 -> 779 us); where waves share lines the mark makes them come twice (8 x 32768
-// keys, 8 heads of 80: 200 us marked, 137 plain).
+// keys, 8 heads of 80: 200 us marked, 137 plain, 132 now).
 template <int n, bool STREAM> __device__ __forceinline__ uint4 load_row(uint64_t addr) {
   if constexpr (n == 16) {
     return __builtin_bit_cast(uint4, STREAM ? __builtin_nontemporal_load((gptr16)addr) : *(gptr16)addr);

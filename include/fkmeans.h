@@ -337,8 +337,10 @@ fk_status_t fk_qk_norm_rope(const void* q, const int64_t q_stride[2], const void
  *   s_j = s_j + key_bias_j;  out = sum_j e^(s_j - lse) v_j;  lse = log sum_j e^s_j
  * Keys with bias -inf, or whose page is outside [0,pages), are left out, and
  * nothing stored there reaches the result, NaN included. A request with
- * nothing left gets out = 0 and lse = -inf. Scores, softmax statistics and sums
- * are fp32; the result is rounded once.
+ * nothing left gets out = 0 and lse = -inf, whatever its query holds. What counts and
+ * is not finite does what it does in the formula: a score of -inf drops its key,
+ * an infinite value makes its element infinite, NaN spreads to the results that use
+ * it. Scores, softmax statistics and sums are fp32; the result is rounded once.
  *   q (B,Hq,D) dt in, q_stride: elements between requests and between heads.
  *   table (B,width) int32 in, rows ld_table >= width apart; lens (B) int32 in.
  *   max_len: no length is above it (0: not known). It only chooses how the work
@@ -349,7 +351,7 @@ fk_status_t fk_qk_norm_rope(const void* q, const int64_t q_stride[2], const void
  * where q is contiguous.
  * D <= 1024 (FK_ERR_UNSUPPORTED above). Rows of at most 256 elements that
  * start at multiples of 16 bytes and hold whole 16-byte units run on the
- * matrix cores, others on a path several times slower. The same arguments give
+ * matrix cores, others on a path 10 to 40 times slower. The same arguments give
  * the same bits on every run; another batch around a request, or another
  * max_len, may change its last bits (where its keys are split).
  */
