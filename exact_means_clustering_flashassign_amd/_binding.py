@@ -381,10 +381,10 @@ def _apart(outs, ins):
     end of its extent, and the tensor where that may have gaps)."""
     for i, (name, lo, hi) in enumerate(outs):
         for other, a, b in outs[:i]:
-            if lo < b and a < hi:
+            if max(lo, a) < min(hi, b):
                 raise ValueError(f"{name} overlaps {other}")
         for other, a, b, *t in ins:
-            if lo < b and a < hi and (not t or _meets(lo - a, hi - a, t[0])):
+            if max(lo, a) < min(hi, b) and (not t or _meets(lo - a, hi - a, t[0])):
                 raise ValueError(f"{name} overlaps {other}, which the call reads")
 
 

@@ -139,3 +139,15 @@ def test_paged_attn_in_place_or_apart(fk, D):
     gaps = buf.as_strided((2, Hq, D), (4 * Hq * D, D, 1))
     got = fk.fk_paged_attn(gaps, kc, vc, table[:2], lens[:2], out=buf[Hq * D:3 * Hq * D].view(2, Hq, D))
     assert torch.equal(got, fk.fk_paged_attn(gaps, kc, vc, table[:2], lens[:2]))
+
+
+def test_empty_ranges_overlap_nothing():
+    from exact_means_clustering_flashassign_amd._binding import _apart
+
+    _apart([("out", 100, 200)], [("free_pages", 150, 150), ("q", 200, 300), ("k", 0, 100)])
+    _apart([("out", 100, 200), ("lens", 150, 150)], [])
+    for other in ((150, 151), (0, 101), (199, 300), (0, 300)):
+        with pytest.raises(ValueError, match="out overlaps x, which the call reads"):
+            _apart([("out", 100, 200)], [("x", *other)])
+        with pytest.raises(ValueError, match="out overlaps x"):
+            _apart([("x", *other), ("out", 100, 200)], [])
