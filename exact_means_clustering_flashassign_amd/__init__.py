@@ -12,11 +12,15 @@ from ._binding import (  # noqa: F401
     LIB_PATH,
     dtype_code,
     fk_assign,
+    fk_kv_load8,
+    fk_kv_store8,
     fk_lloyd,
     fk_lloyd_host,
     fk_norms,
     fk_page_tables,
     fk_paged_attn,
+    fk_paged_attn8,
+    fk_prompt_attn,
     fk_qk_norm_rope,
     fk_status_string,
     fk_trace_begin,
@@ -28,7 +32,9 @@ from ._binding import (  # noqa: F401
     fk_version,
     fk_workspace_size,
     fk_workspace_size_attn,
+    fk_workspace_size_attn8,
     fk_workspace_size_host,
+    fk_workspace_size_prompt,
     fkb_assign_materialized,
     fkb_mfma_peak,
     fkb_update_atomic,

@@ -34,6 +34,15 @@ class fk_trace_t(ctypes.Structure):
                 ("assign_ms", ctypes.c_double), ("update_ms", ctypes.c_double)]
 
 
+class fk_kv_cache8_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("key_bias", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("k_scale_stride", ctypes.c_int64 * 3),
+                ("v_scale_stride", ctypes.c_int64 * 3), ("bias_stride", ctypes.c_int64 * 3)]
+
+
 class fk_kv_cache_t(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("key_bias", ctypes.c_void_p),
                 ("pages", ctypes.c_int64), ("page", ctypes.c_int64), ("heads", ctypes.c_int64),
@@ -76,6 +85,14 @@ def load(path: Optional[str] = None):
         "fk_paged_attn": (ctypes.c_int, [P, P, ctypes.c_int, I64, I64, P, P, I64, I64, P, I64,
                                          ctypes.c_float, ctypes.c_float, P, P, P, SZ, P]),
         "fk_workspace_size_attn": (SZ, [ctypes.c_int, I64, I64, I64, I64]),
+        "fk_prompt_attn": (ctypes.c_int, [P, P, ctypes.c_int, I64, I64, I64, P, P, I64, I64, P, P,
+                                          I64, ctypes.c_float, ctypes.c_float, P, P, P, SZ, P]),
+        "fk_workspace_size_prompt": (SZ, [ctypes.c_int, I64, I64, I64, I64, I64]),
+        "fk_kv_store8": (ctypes.c_int, [P, P, P, P, ctypes.c_int, I64, P, P, P]),
+        "fk_kv_load8": (ctypes.c_int, [P, P, ctypes.c_int, I64, P, P, P]),
+        "fk_paged_attn8": (ctypes.c_int, [P, P, ctypes.c_int, I64, I64, P, P, I64, I64, P, I64,
+                                          ctypes.c_float, ctypes.c_float, P, P, P, SZ, P]),
+        "fk_workspace_size_attn8": (SZ, [ctypes.c_int, I64, I64, I64, I64]),
         "fk_trace_begin": (ctypes.c_int, [I32]),
         "fk_trace_end": (ctypes.c_int, [ctypes.POINTER(fk_trace_t)]),
     }
@@ -321,6 +338,7 @@ def fk_lloyd_host(x_host, init, max_iter: int, tol: float, chunk: int, ids=None,
 # ---------------------------------------------------------------------------
 _pack2 = struct.Struct("2q").pack
 _pack_cache = struct.Struct("3P4q9q").pack      # the layout of fk_kv_cache_t
+_pack_cache8 = struct.Struct("5P4q15q").pack    # the layout of fk_kv_cache8_t
 
 
 _tc = None
@@ -336,6 +354,8 @@ class _TorchCalls:
         self.codes = {torch.float32: FK_F32, torch.float16: FK_F16, torch.bfloat16: FK_BF16}
         self.stream = torch._C._cuda_getCurrentRawStream
         self.grad = torch.is_grad_enabled
+        self.e4m3 = torch.float8_e4m3fn
+        self.device, self.on_device = torch._C._cuda_getDevice, torch.cuda.device
 
 
 def _calls():
@@ -643,6 +663,230 @@ def fk_paged_attn(q, k_cache, v_cache, table, lens, scale: Optional[float] = Non
         softcap, p_out, p_lse, p_ws, need, tc.stream(index))
     if st:
         _check(st, "fk_paged_attn")
+    return out if lse is None else (out, lse)
+
+
+def _launch(where, index, fn, *args):
+    """Calls fn on device `index`, made the current one for the call if it is not."""
+    if _tc.device() == index:
+        st = fn(*args)
+    else:
+        with _tc.on_device(index):
+            st = fn(*args)
+    if st:
+        _check(st, where)
+
+
+def _attn_outputs(tc, q, sq, heads, need, out, lse, return_lse, ws, inputs, index):
+    """Outputs and workspace of an attention call, those given checked against each other and
+    the inputs (spans for _apart): out, lse, and the addresses of out, lse and ws with ws's size."""
+    dt, dev, given = q.dtype, q.device, []
+    if need == 0:
+        raise ValueError(f"{q.shape[1]} query heads of {q.shape[2]} do not go with {heads} cache heads")
+    if out is None:
+        out = tc.empty(q.shape, dtype=dt, device=dev)
+        p_out = out.data_ptr()
+    else:
+        p_out = _on(out, "out", dt, q.shape, index)
+        given.append(("out", p_out, p_out + out.numel() * out.element_size()))
+    p_lse = None
+    if lse is not None:
+        p_lse = _on(lse, "lse", tc.f32, q.shape[:2], index)
+        given.append(("lse", p_lse, p_lse + 4 * lse.numel()))
+    elif return_lse:
+        lse = tc.empty(q.shape[:2], dtype=tc.f32, device=dev)
+        p_lse = lse.data_ptr()
+    if ws is None:
+        ws = tc.empty(need, dtype=tc.u8, device=dev)
+        p_ws = ws.data_ptr()
+    else:
+        need = ws.numel()
+        p_ws = _on(ws, "ws", tc.u8, (need,), index)
+        given.append(("ws", p_ws, p_ws + need))
+    if given:
+        _apart([g for g in given if g[1] < g[2]],
+               [_span(n, t, t.stride(), t.element_size()) for n, t in inputs if t is not None])
+    return out, lse, p_out, p_lse, ws, p_ws, need
+
+
+@functools.lru_cache(256)
+def _prompt_ws(code, T, B, Hq, Hkv, D):
+    return int(load().fk_workspace_size_prompt(code, T, B, Hq, Hkv, D))
+
+
+def fk_workspace_size_prompt(dtype, T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    return _prompt_ws(dtype if isinstance(dtype, int) else dtype_code(dtype), T, B, Hq, Hkv, D)
+
+
+def fk_prompt_attn(q, k_cache, v_cache, table, lens, cu_tokens, scale: Optional[float] = None,
+                   softcap: float = 0.0, key_bias=None, max_len: int = 0, out=None, lse=None,
+                   return_lse: bool = False, ws=None):
+    """Causal attention of a step's tokens, q (T,Hq,D), requests one after another as
+    cu_tokens (B+1) int32 says: the last tokens of lens (B) int32 keys of k_cache and
+    v_cache (pages, page, Hkv, D), found through table (B,W) int32, each over the keys
+    up to its own. Otherwise as fk_paged_attn. Returns out (T,Hq,D), and with
+    return_lse (or lse given) the natural log of the softmax's sum, (T,Hq) fp32;
+    rows that no request has are not written. out, lse and ws given may not
+    overlap each other or an input."""
+    tc = _tc or _calls()
+    dt, index = q.dtype, _gpu_index(q, "q")
+    code = tc.codes.get(dt)
+    if code is None:
+        code = dtype_code(dt)            # says what is supported
+    sq = _rows(q, "q", dt, 3, index)
+    T, Hq, D = q.shape
+    cache, heads = _kv_cache(k_cache, v_cache, key_bias, dt, 0, D, index)
+    st2 = _rows(table, "table", tc.i32, 2, index)
+    B, width = table.shape
+    p_lens = _on(lens, "lens", tc.i32, (B,), index)
+    p_cu = _on(cu_tokens, "cu_tokens", tc.i32, (B + 1,), index)
+    out, lse, p_out, p_lse, ws, p_ws, need = _attn_outputs(
+        tc, q, sq, heads, _prompt_ws(code, T, B, Hq, heads, D), out, lse, return_lse, ws,
+        (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("key_bias", key_bias),
+         ("table", table), ("lens", lens), ("cu_tokens", cu_tokens)), index)
+    _launch("fk_prompt_attn", index, _lib.fk_prompt_attn, q.data_ptr(), _pack2(sq[0], sq[1]), code,
+            T, B, Hq, cache, table.data_ptr(), st2[0] if B > 1 else width, width, p_lens, p_cu,
+            max_len, D ** -0.5 if scale is None else scale, softcap, p_out, p_lse, p_ws, need,
+            tc.stream(index))
+    return out if lse is None else (out, lse)
+
+
+def _numbers(t, name, shape, index):
+    """Checks of fp32 numbers per slot and head, in any order of memory; address and strides."""
+    if t.shape != shape or t.dtype is not _tc.f32 or t.get_device() != index or t.requires_grad:
+        raise ValueError(f"{name} must be float32 of shape {tuple(shape)} on cuda:{index} without "
+                         f"grad, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr(), t.stride()
+
+
+def _kv_cache8(k_cache, v_cache, k_scale, v_scale, key_bias, heads, dim, index):
+    """fk_kv_cache8_t (as bytes) of e4m3 tensors (pages, page, heads, dim) and fp32 scales
+    (pages, page, heads), and the shape."""
+    sk = _rows(k_cache, "k_cache", _tc.e4m3, 4, index)
+    sv = _rows(v_cache, "v_cache", _tc.e4m3, 4, index)
+    shape = k_cache.shape
+    if v_cache.shape != shape or (dim and shape[3] != dim) or (heads and shape[2] != heads):
+        raise ValueError(f"k_cache and v_cache must have shape (pages, page, {heads or 'heads'}, "
+                         f"{dim or 'dim'}), got {tuple(shape)} and {tuple(v_cache.shape)}")
+    pk, ssk = _numbers(k_scale, "k_scale", shape[:3], index)
+    pv, ssv = _numbers(v_scale, "v_scale", shape[:3], index)
+    pb, sb = (0, (0, 0, 0)) if key_bias is None else \
+        _numbers(key_bias, "key_bias", shape[:3], index)
+    return _pack_cache8(k_cache.data_ptr(), v_cache.data_ptr(), pk, pv, pb, *shape, *sk[:3],
+                        *sv[:3], *ssk, *ssv, *sb), shape
+
+
+def _extent(t, stride):
+    """Address of a tensor's first element and of the byte past its last."""
+    p = t.data_ptr()
+    if not t.numel():
+        return p, p
+    return p, p + (sum((n - 1) * s for n, s in zip(t.shape, stride)) + 1) * t.element_size()
+
+
+def fk_kv_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, key_bias=None) -> None:
+    """Keys and values k, v (T,Hkv,D) quantised to e4m3 as they are stored in slots (T)
+    int32 of k_cache and v_cache (pages, page, Hkv, D) float8_e4m3fn: a row's scale, in
+    k_scale and v_scale (pages, page, Hkv) fp32, is the smallest power of two that takes its
+    largest element to 448 at most. key_bias (pages, page, Hkv) becomes 0. Slots outside
+    the cache are skipped, the others have to be distinct. k, v and slots may not
+    lie between the first and the last byte of any of the cache's tensors."""
+    tc = _tc or _calls()
+    dt, index = k.dtype, _gpu_index(k, "k")
+    code = tc.codes.get(dt)
+    if code is None:
+        code = dtype_code(dt)            # says what is supported
+    sk, sv = _rows(k, "k", dt, 3, index), _rows(v, "v", dt, 3, index)
+    if v.shape != k.shape:
+        raise ValueError(f"v must have k's shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    T, H, D = k.shape
+    p_slots = _on(slots, "slots", tc.i32, (T,), index)
+    cache, _ = _kv_cache8(k_cache, v_cache, k_scale, v_scale, key_bias, H, D, index)
+    held = [("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale)]
+    if key_bias is not None:
+        held.append(("key_bias", key_bias))
+    held = [(n, *_extent(t, t.stride())) for n, t in held]
+    for name, lo, hi in (("k", *_extent(k, sk)), ("v", *_extent(v, sv)),
+                         ("slots", p_slots, p_slots + 4 * T)):
+        for other, a, b in held:
+            if lo < b and a < hi:
+                raise ValueError(f"{other} overlaps {name}, which the call reads")
+    if held[0][1:] == held[1][1:] and T and k_cache.numel() or \
+            held[2][1:] == held[3][1:] and T and k_scale.numel():
+        raise ValueError("keys and values, and their scales, need tensors of their own")
+    _launch("fk_kv_store8", index, _lib.fk_kv_store8, k.data_ptr(), _pack2(sk[0], sk[1]),
+            v.data_ptr(), _pack2(sv[0], sv[1]), code, T, p_slots, cache, tc.stream(index))
+
+
+def fk_kv_load8(slots, k_cache, v_cache, k_scale, v_scale, dtype, k_out=None, v_out=None):
+    """Reads slots (T) int32 of an 8-bit cache (as in fk_kv_store8) back: keys and values
+    (T,Hkv,D) of `dtype`, zeros for slots outside the cache. k_out and v_out
+    given may not overlap each other or the cache."""
+    tc = _tc or _calls()
+    index = _gpu_index(slots, "slots")
+    code = tc.codes.get(dtype)
+    if code is None:
+        code = dtype_code(dtype)         # says what is supported
+    T = slots.numel()
+    p_slots = _on(slots, "slots", tc.i32, (T,), index)
+    cache, (_, _, H, D) = _kv_cache8(k_cache, v_cache, k_scale, v_scale, None, 0, 0, index)
+    shape, given = (T, H, D), []
+    if k_out is None:
+        k_out = tc.empty(shape, dtype=dtype, device=slots.device)
+    else:
+        given.append(("k_out", _on(k_out, "k_out", dtype, shape, index), k_out))
+    if v_out is None:
+        v_out = tc.empty(shape, dtype=dtype, device=slots.device)
+    else:
+        given.append(("v_out", _on(v_out, "v_out", dtype, shape, index), v_out))
+    if given:
+        _apart([(n, p, p + t.numel() * t.element_size()) for n, p, t in given if t.numel()],
+               [_span(n, t, t.stride(), t.element_size()) for n, t in
+                (("slots", slots), ("k_cache", k_cache), ("v_cache", v_cache),
+                 ("k_scale", k_scale), ("v_scale", v_scale))])
+    _launch("fk_kv_load8", index, _lib.fk_kv_load8, cache, p_slots, code, T, k_out.data_ptr(),
+            v_out.data_ptr(), tc.stream(index))
+    return k_out, v_out
+
+
+@functools.lru_cache(256)
+def _attn8_ws(code, B, Hq, Hkv, D):
+    return int(load().fk_workspace_size_attn8(code, B, Hq, Hkv, D))
+
+
+def fk_workspace_size_attn8(dtype, B: int, Hq: int, Hkv: int, D: int) -> int:
+    return _attn8_ws(dtype if isinstance(dtype, int) else dtype_code(dtype), B, Hq, Hkv, D)
+
+
+def fk_paged_attn8(q, k_cache, v_cache, k_scale, v_scale, table, lens,
+                   scale: Optional[float] = None, softcap: float = 0.0, key_bias=None,
+                   max_len: int = 0, out=None, lse=None, return_lse: bool = False, ws=None):
+    """fk_paged_attn over an 8-bit cache (as in fk_kv_store8), q (B,Hq,D) of any of the
+    library's types. out, lse and ws given may not overlap each other or an input, but
+    out may be a contiguous q itself."""
+    tc = _tc or _calls()
+    dt, index = q.dtype, _gpu_index(q, "q")
+    code = tc.codes.get(dt)
+    if code is None:
+        code = dtype_code(dt)            # says what is supported
+    sq = _rows(q, "q", dt, 3, index)
+    B, Hq, D = q.shape
+    cache, shape = _kv_cache8(k_cache, v_cache, k_scale, v_scale, key_bias, 0, D, index)
+    st2 = _rows(table, "table", tc.i32, 2, index)
+    rows, width = table.shape
+    if rows != B:
+        raise ValueError(f"table must have {B} rows, got {tuple(table.shape)}")
+    p_lens = _on(lens, "lens", tc.i32, (B,), index)
+    in_place = out is not None and out.data_ptr() == q.data_ptr() and q.is_contiguous()
+    out, lse, p_out, p_lse, ws, p_ws, need = _attn_outputs(
+        tc, q, sq, shape[2], _attn8_ws(code, B, Hq, shape[2], D), out, lse, return_lse, ws,
+        (("q", None if in_place else q), ("k_cache", k_cache), ("v_cache", v_cache),
+         ("k_scale", k_scale), ("v_scale", v_scale), ("key_bias", key_bias), ("table", table),
+         ("lens", lens)), index)
+    _launch("fk_paged_attn8", index, _lib.fk_paged_attn8, q.data_ptr(), _pack2(sq[0], sq[1]), code,
+            B, Hq, cache, table.data_ptr(), st2[0] if B > 1 else width, width, p_lens, max_len,
+            D ** -0.5 if scale is None else scale, softcap, p_out, p_lse, p_ws, need,
+            tc.stream(index))
     return out if lse is None else (out, lse)
 
 

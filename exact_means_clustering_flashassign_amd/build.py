@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfkmeans.so")
 SOURCES = ["norms.hip", "assign.hip", "assign_splitd.hip", "update.hip", "api.hip",
-           "kvtables.hip", "qkrope.hip", "attn.hip", "api_kv.hip"]
+           "kvtables.hip", "qkrope.hip", "attn.hip", "prompt.hip", "cache8.hip",
+           "attn8.hip", "api_kv.hip"]
 # The contrast baselines (materialised-distance assign, scatter-atomic
 # update) are a library of their own, linked against rocBLAS for the GEMM,
 # so the Lloyd library itself depends on nothing but the HIP runtime.

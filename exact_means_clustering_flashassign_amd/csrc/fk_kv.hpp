@@ -85,4 +85,40 @@ constexpr int64_t kAttnMaxDim = 1024;
 size_t attn_ws_bytes(int dt, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
 hipError_t launch_paged_attn(const AttnArgs& a, int dt, void* ws, hipStream_t s);
 
+
+// The 8-bit cache: k and v of `cache` are e4m3 codes.
+struct AttnArgs8 : AttnArgs {
+  const float *k_scale, *v_scale;
+  int64_t ks_stride[3], vs_stride[3];
+};
+size_t attn8_ws_bytes(int dt, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+hipError_t launch_paged_attn8(const AttnArgs8& a, int dt, void* ws, hipStream_t s);
+
+struct Cache8Args {
+  const void *k, *v;          // store: rows in
+  int64_t k_stride[2], v_stride[2];
+  int64_t T;
+  const int32_t* slots;
+  fk_kv_cache8_t cache;
+  void *k_out, *v_out;        // load: rows out
+};
+hipError_t launch_kv_store8(const Cache8Args& a, int dt, hipStream_t s);
+hipError_t launch_kv_load8(const Cache8Args& a, int dt, hipStream_t s);
+
+struct PromptArgs {
+  const void* q;
+  int64_t q_stride[2];
+  int64_t T, B, Hq;
+  fk_kv_cache_t cache;
+  const int32_t* table;
+  int64_t ld_table, width;
+  const int32_t *lens, *cu;
+  int64_t max_len;
+  float scale, softcap;
+  void* out;
+  float* lse;
+};
+size_t prompt_ws_bytes(int dt, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+hipError_t launch_prompt_attn(const PromptArgs& a, int dt, void* ws, hipStream_t s);
+
 }  // namespace fk

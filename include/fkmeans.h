@@ -365,6 +365,96 @@ fk_status_t fk_paged_attn(const void* q, const int64_t q_stride[2], fk_dtype_t d
 size_t fk_workspace_size_attn(fk_dtype_t dt, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
 
 /*
+ * Attention of a step's prompts over the cache: every token attends to what its
+ * request holds up to and with itself. Tokens lie one request after another
+ * (cu_tokens as fk_page_tables gives it); request b has n = cu_tokens[b+1] -
+ * cu_tokens[b] of them, the last n of the lens[b] keys it holds, so that token
+ * t = cu_tokens[b] + i sees the keys j <= lens[b] - n + i of its request: a whole
+ * prompt with lens[b] = n, a chunk of one with more. Scores, bias, cap, result and lse
+ * of token t are those of fk_paged_attn over these keys, and what is left out
+ * there is left out here; a row with nothing left gets out = 0 and lse = -inf.
+ * Nothing a key holds reaches the rows that do not see it, NaN included.
+ *   q (T,Hq,D) dt in, q_stride: elements between tokens and between heads.
+ *   table (B,width), lens (B) as in fk_paged_attn; cu_tokens (B+1) int32 in,
+ *             not decreasing, from 0 on. Rows of q that no request has are not
+ *             read, and their rows of out and lse stay as they were.
+ *   max_len: no length is above it (0: not known); it only chooses how the work is split.
+ *   out (T,Hq,D) dt out; lse (T,Hq) fp32 out, may be null.
+ *   ws: fk_workspace_size_prompt(dt, T, B, Hq, Hkv, D) bytes, 256-byte aligned.
+ * Scores, softmax statistics and sums are fp32; with 16-bit caches each
+ * probability is rounded to dt before its product with the value, and the result
+ * is rounded once. out, lse and ws may not overlap each other or an input.
+ * D <= 1024 (FK_ERR_UNSUPPORTED above). The same arguments give the same bits on
+ * every run; other requests around one, or another max_len, may change its last bits.
+ */
+fk_status_t fk_prompt_attn(const void* q, const int64_t q_stride[2], fk_dtype_t dt, int64_t T,
+                           int64_t B, int64_t Hq, const fk_kv_cache_t* cache,
+                           const int32_t* table, int64_t ld_table, int64_t width,
+                           const int32_t* lens, const int32_t* cu_tokens, int64_t max_len,
+                           float scale, float softcap, void* out, float* lse, void* ws,
+                           size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes fk_prompt_attn needs (at least 256); 0 for invalid arguments. */
+size_t fk_workspace_size_prompt(fk_dtype_t dt, int64_t T, int64_t B, int64_t Hq, int64_t Hkv,
+                                int64_t D);
+
+/*
+ * The cache in 8 bits: keys and values as e4m3 codes (OCP FP8: 4 exponent and 3
+ * fraction bits, largest 448, no infinity), with one fp32 scale per slot and head
+ * for keys and one for values; a code c of a row with scale s stands for s c.
+ * Axes and strides as in fk_kv_cache_t, strides of codes in bytes.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  float* key_bias;
+  int64_t pages, page, heads, dim;
+  int64_t k_stride[3], v_stride[3], k_scale_stride[3], v_scale_stride[3], bias_stride[3];
+} fk_kv_cache8_t;
+
+/*
+ * Quantises keys and values of T tokens as they are written to their slots.
+ * The scale of a row is the smallest power of two s >= 2^-126 with 448 s >= |x|
+ * for its finite elements x (1 for a row without any but zeros); a code is x / s
+ * rounded to the nearest e4m3 number, ties to even. s being a power of two, x / s is exact and that is the only
+ * rounding. Infinities and NaN are stored as NaN.
+ *   k, v (T,heads,dim) dt in; *_stride: elements between tokens and between heads.
+ *   slots (T) int32 in: as in fk_qk_norm_rope (a key_bias, where the cache has
+ *             one, becomes 0; slots outside the cache are skipped, the others have to differ).
+ * The cache may not overlap an input. The pages name low-bit quantisation of
+ * keys and values among the uses of clusters.
+ */
+fk_status_t fk_kv_store8(const void* k, const int64_t k_stride[2], const void* v,
+                         const int64_t v_stride[2], fk_dtype_t dt, int64_t T,
+                         const int32_t* slots, const fk_kv_cache8_t* cache, hipStream_t stream);
+
+/*
+ * Reads rows of an 8-bit cache back: k_out, v_out (T,heads,dim) dt out are what the
+ * codes of slots (T) int32 stand for, rounded once to dt; numbers past dt's largest
+ * become the largest. Slots may repeat; rows of slots outside the cache are 0.
+ */
+fk_status_t fk_kv_load8(const fk_kv_cache8_t* cache, const int32_t* slots, fk_dtype_t dt,
+                        int64_t T, void* k_out, void* v_out, hipStream_t stream);
+
+/*
+ * fk_paged_attn over an 8-bit cache: the same definition, with key and value of a
+ * slot the numbers that its codes and scales stand for. q and out are dt.
+ *   ws: fk_workspace_size_attn8(dt, B, Hq, Hkv, D) bytes, 256-byte aligned.
+ * Rows of at most 256 elements that start at multiples of 16 bytes and hold whole
+ * 16-byte units (of codes; q and out as in fk_paged_attn) run on the matrix cores.
+ */
+fk_status_t fk_paged_attn8(const void* q, const int64_t q_stride[2], fk_dtype_t dt, int64_t B,
+                           int64_t Hq, const fk_kv_cache8_t* cache, const int32_t* table,
+                           int64_t ld_table, int64_t width, const int32_t* lens, int64_t max_len,
+                           float scale, float softcap, void* out, float* lse, void* ws,
+                           size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes fk_paged_attn8 needs (at least 256); 0 for invalid arguments. */
+size_t fk_workspace_size_attn8(fk_dtype_t dt, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+
+/*
  * Optional timing trace of fk_lloyd (process-wide, not thread-safe).
  * fk_trace_begin(capacity) turns it on for up to `capacity` iterations in
  * total. Each traced iteration's norms and assign kernels are launched with

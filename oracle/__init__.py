@@ -20,4 +20,11 @@ from .kmeans import (  # noqa: F401
     UpdateResult,
     LloydResult,
 )
-from .kvcache import norm_rope, page_tables, paged_attn  # noqa: F401
+from .kvcache import (  # noqa: F401
+    e4m3_round,
+    norm_rope,
+    page_tables,
+    paged_attn,
+    prompt_attn,
+    quantise,
+)

@@ -101,3 +101,46 @@ def paged_attn(q, k_cache, v_cache, table, lens, scale, softcap=0.0, bias=None):
             info[b, h] = (np.abs(raw).max(), abs(scale) * (np.abs(k) @ np.abs(q[b, h])).max(),
                           np.abs(v).max(), len(p))
     return out, lse, info
+
+
+def prompt_attn(q, k_cache, v_cache, table, lens, cu, scale, softcap=0.0, bias=None):
+    """q (T,Hq,D): token cu[b] + i of request b over its keys up to place
+    lens[b] - n + i, n = cu[b+1] - cu[b]. -> (out, lse, info) as paged_attn, NaN in
+    rows of tokens that no request has."""
+    T, Hq, D = q.shape
+    out, lse = np.full((T, Hq, D), np.nan), np.full((T, Hq), np.nan)
+    info = np.zeros((T, Hq, 4))
+    for b in range(len(lens)):
+        n = int(cu[b + 1]) - int(cu[b])
+        for i in range(n):
+            t = int(cu[b]) + i
+            seen = max(int(lens[b]) - n + i + 1, 0)
+            o, s, f = paged_attn(q[t:t + 1], k_cache, v_cache, table[b:b + 1], [seen], scale, softcap, bias)
+            out[t], lse[t], info[t] = o[0], s[0], f[0]
+    return out, lse, info
+
+
+def e4m3_round(y):
+    """Nearest e4m3 number (multiples of 2^-9 up to 2^-6, then eight to a binade, up to 448), ties
+    to the even multiple; |y| <= 448."""
+    a = np.abs(y)
+    _, e = np.frexp(np.maximum(a, 2.0 ** -6))            # a = f 2^e, 0.5 <= f < 1
+    step = np.ldexp(1.0, e - 4)
+    return np.sign(y) * np.rint(a / step) * step
+
+
+def quantise(x):
+    """Rows x (..., D) float64 -> (numbers that the codes stand for, scale (...)): the scale
+    is the smallest power of two >= 2^-126 that takes the largest finite element to 448
+    at most (1 for zeros); what is not finite is NaN."""
+    ok = np.isfinite(x)
+    most = np.where(ok, np.abs(x), 0.0).max(-1)
+    scale = np.ones(most.shape)
+    for at in np.ndindex(most.shape):
+        if most[at] > 0:
+            s = 2.0 ** -126
+            while 448 * s < most[at]:
+                s *= 2
+            scale[at] = s
+    y = np.where(ok, x, 0.0) / scale[..., None]
+    return np.where(ok, e4m3_round(y) * scale[..., None], np.nan), scale
