@@ -86,6 +86,7 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 // and not generic ones, which the LDS counter would wait for too.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float floatx2_t __attribute__((ext_vector_type(2)));
 typedef const __attribute__((address_space(1))) u32x4* gptr16;
 typedef const __attribute__((address_space(1))) u32x2* gptr8;
 typedef const __attribute__((address_space(1))) uint32_t* gptr4;

@@ -1,11 +1,9 @@
 // Numbers of the 8-bit cache: e4m3 codes and the scale of a row.
 #pragma once
 
-#include "fk_kv.hpp"
+#include "attn_parts.hpp"
 
 namespace fk {
-
-typedef float floatx2_t __attribute__((ext_vector_type(2)));
 
 // Two neighbouring codes of a word (its upper two if HI) as fp32, exact.
 template <bool HI> __device__ __forceinline__ floatx2_t e4m3_pair(uint32_t w) {

@@ -89,6 +89,375 @@ __global__ __launch_bounds__(kWaves * 64) void prompt_any_kernel(PromptArgs a) {
   if (t < a.T) attend_row<DT, EPL>(a, t, r - t * a.Hq);
 }
 
+// ---------------------------------------------------------------------------
+// Matrix-core kernel of 16-bit caches: rows of at most 256 elements in whole 16-byte units
+// ---------------------------------------------------------------------------
+// The G query heads of a cache head see the same keys, so row r of a request is head r % G
+// of token r / G, and a tile is kRows rows in a run. A block takes one tile of one cache head
+// over a range of keys, a wave 32 of its rows, 64 keys a step.
+//
+// Lane (n = lane & 31, h = lane >> 5) of a wave. Scores are S^T = K Q^T with v_mfma 32x32x16:
+// register i of the lane holds the score of query row n with key (i & 3) + 8 (i >> 2) + 4 h of
+// 32. The values enter as O^T = V^T P^T: the contraction runs over keys, whose order is
+// free, so the eight probabilities a lane gives to a product are those it holds, of keys 4 h +
+// 0..3 and 8 + 4 h + 0..3 of 16, and V^T comes from LDS in that order by transposing reads
+// (four keys of one element a lane each). Nothing but keys and values goes through LDS.
+//
+// Keys and values go from the cache's pages straight to LDS, 16 bytes a lane, two buffers in
+// turn. Each wave brings 64 / waves rows a step; their addresses are found for as many
+// steps at once as make up 64, and table entries and biases are asked for two such groups ahead.
+typedef const __attribute__((address_space(1))) uint32_t* gptr32;
+typedef __attribute__((address_space(3))) uint32_t* lptr32;
+
+constexpr int kStep = 64;                  // keys a step
+
+template <int DP> struct Tile {
+  // 8 waves share the keys of a step; 256-element rows need the registers of 4
+  static constexpr int waves = DP > 128 ? 4 : 8;
+  static constexpr int rows = waves * 32;
+  static constexpr int units = DP / 8;                    // 16-byte units of a row
+  static constexpr int per_load = 64 / units;             // rows a wave brings with one load
+  static constexpr int per_wave = kStep / waves;          // rows a wave brings a step
+  static constexpr int loads = per_wave / per_load;
+  static constexpr int dt = DP / 32, kt = DP / 16;        // tiles of the output, steps of a score
+};
+
+// Where unit u of row r lies in its LDS row. Scores read one unit of 32 rows at once: 16
+// neighbouring rows are 16 different units. Transposing reads take two units of four
+// rows, or four of them: the rows are put 2 and 4 units apart, mod 8 and mod 16.
+template <int DP> __device__ __forceinline__ int key_swizzle(int r) { return r & (DP / 8 - 1) & 15; }
+template <int DP> __device__ __forceinline__ int value_swizzle(int r) {
+  if constexpr (DP == 64) return (r & 1) << 1 | (r & 2) << 1;
+  return (r & 1) << 2 | (r & 2) << 2 | (r & 2);
+}
+
+// Both halves' numbers of a wave, in every lane: (of lanes 0..31, of lanes 32..63).
+__device__ __forceinline__ floatx2_t both_halves(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t lo = r.x, hi = r.y;       // (a bit cast of an element itself takes the first one's)
+  return floatx2_t{__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
+}
+__device__ __forceinline__ float max_halves(float x) {
+  const floatx2_t r = both_halves(x);
+  return fmaxf(r.x, r.y);
+}
+__device__ __forceinline__ float sum_halves(float x) {
+  const floatx2_t r = both_halves(x);
+  return r.x + r.y;
+}
+
+// Four keys of one element each, 16 lanes a 4 x 16 block that lies in LDS key by key.
+__device__ __forceinline__ uint2 read_transposed(const char* at) {
+  typedef short s4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s4* lp;
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)at));
+}
+
+// The tile of a block: requests are taken from the last one on, their tiles likewise, so that
+// the longest rows of a prompt come first and the chip does not wait for one at the end.
+struct Where {
+  int64_t b;          // request, -1: none
+  int tile;           // tile of its rows
+};
+__device__ __forceinline__ Where find_tile(const PromptArgs& a, int G, int rows, uint32_t order) {
+  const int lane = threadIdx.x & 63;
+  uint32_t before = 0;
+  for (int64_t last = a.B - 1; last >= 0; last -= 64) {
+    const int64_t b = last - lane;
+    uint32_t mine = 0;
+    if (b >= 0) {
+      const int64_t n = (int64_t)a.cu[b + 1] - a.cu[b];
+      mine = n > 0 ? (uint32_t)((n * G + rows - 1) / rows) : 0;
+    }
+    uint32_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const uint32_t o = __shfl_up(incl, off, 64);
+      if (lane >= off) incl += o;
+    }
+    const uint32_t total = __builtin_amdgcn_readlane(incl, 63);
+    if (order < before + total) {
+      const int at = __popcll(__ballot(before + incl <= order));
+      const uint32_t end = before + __builtin_amdgcn_readlane(incl, at);
+      return {last - at, (int)(end - 1 - order)};
+    }
+    before += total;
+  }
+  return {-1, 0};
+}
+
+struct PromptPlan {
+  int heads, G, parts, chunk;     // cache heads, query heads of each, parts of a row's keys, steps of a part
+  FastDiv page, by_heads, by_parts, by_G;
+  float* o;                       // (parts, T, Hq, D) partial sums
+  float* ml;                      // (parts, T, Hq, 2) their maximum and sum
+};
+
+template <int DT, int DP, bool EXTRA>
+__global__ __launch_bounds__(Tile<DP>::waves * 64, Tile<DP>::waves / 4)
+void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
+  using L = Tile<DP>;
+  constexpr int W = L::waves, rb = DP * 2;             // bytes of a row
+  __shared__ __attribute__((aligned(1024))) char lk[2][kStep * rb], lv[2][kStep * rb];
+  __shared__ uint64_t row_k[W][64], row_v[W][64];
+  __shared__ uint64_t valid[2][W];                     // keys of a step that count, a bit each
+  __shared__ float biases[EXTRA ? 2 : 1][EXTRA ? W : 1][kStep];
+  const fk_kv_cache_t& c = a.cache;
+  const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int D = (int)c.dim;
+
+  const uint32_t rest = div_by(blockIdx.x, p.by_heads), hk = blockIdx.x - rest * p.heads;
+  const uint32_t order = div_by(rest, p.by_parts), part = rest - order * p.parts;
+  const Where at = find_tile(a, p.G, L::rows, order);
+  if (at.b < 0) return;
+  const int64_t b = uniform(at.b);
+  const int64_t cu0 = a.cu[b], cu1 = a.cu[b + 1], len = a.lens[b];
+  const int rows = (int)min((cu1 - cu0) * p.G - (int64_t)at.tile * L::rows, (int64_t)L::rows);
+  const int64_t held = min(a.width * c.page, (int64_t)0x7FFFFFC0);
+  // keys that row r of the tile sees
+  const auto seen = [&](int r) {
+    const int64_t t = div_by((uint32_t)(at.tile * L::rows + r), p.by_G);
+    return (int)max((int64_t)0, min(len - (cu1 - cu0) + t + 1, held));
+  };
+  const int most = __builtin_amdgcn_readfirstlane(seen(rows - 1));      // of the tile's last row
+  const int steps = (int)(((uint32_t)most + kStep - 1) / kStep);
+  const int t0 = (int)part * p.chunk, t1 = min(steps, t0 + p.chunk);
+  if (t0 >= t1 && part > 0) return;                    // (part 0 leaves the results of empty rows)
+
+  // queries; rows past the tile's end are zero, see everything and are not stored
+  const int r = w * 32 + n;
+  const bool mine = r < rows;
+  const uint32_t rr = at.tile * L::rows + min(r, rows - 1);
+  const int64_t tok = div_by(rr, p.by_G);
+  const int64_t t = cu0 + tok, qh = (int64_t)hk * p.G + (rr - tok * p.G);
+  const int limit = mine ? seen(r) : 0x7FFFFFFF;
+  const int wave_rows = min(rows - w * 32, 32);        // none or fewer: nothing to do
+  const int low = wave_rows > 0 ? __builtin_amdgcn_readfirstlane(seen(w * 32)) : 0;
+  const int high = wave_rows > 0 ? __builtin_amdgcn_readfirstlane(seen(w * 32 + wave_rows - 1)) : 0;
+  uint4 q[L::kt];
+  {
+    const uint64_t qp = (uint64_t)a.q + (uint64_t)(t * a.q_stride[0] + qh * a.q_stride[1]) * 2;
+#pragma unroll
+    for (int i = 0; i < L::kt; ++i) {
+      const int e = i * 16 + h * 8;
+      q[i] = load16(e < D && mine && t >= 0 && t < a.T ? qp + e * 2 : (uint64_t)zero_row);
+    }
+  }
+
+  // rows of keys: lane (s, j) looks after row j of this wave's share in step s of a group
+  constexpr int share = L::per_wave;
+  const int gs = lane / share, gj = w * share + lane % share;
+  const uint64_t table = (uint64_t)(a.table + b * a.ld_table);
+  const uint64_t kbase = (uint64_t)c.k + (uint64_t)hk * c.k_stride[2] * 2;
+  const uint64_t vbase = (uint64_t)c.v + (uint64_t)hk * c.v_stride[2] * 2;
+  const uint64_t bbase = (uint64_t)c.key_bias + (uint64_t)hk * c.bias_stride[2] * 4;
+  const uint64_t zero = (uint64_t)zero_row;
+  const bool has_bias = EXTRA && c.key_bias && c.pages > 0;
+  const auto key_of = [&](int group) { return (uint32_t)(t0 + group * W + gs) * kStep + gj; };
+  const auto entry = [&](int group) -> int32_t {       // page of the lane's key, -1: none
+    const uint32_t key = key_of(group), last = most > 0 ? most - 1 : 0;
+    const uint32_t pos = min(key, last);
+    const int32_t pg = most > 0 ? *(gptr_i32)(table + 4 * (uint64_t)div_by(pos, p.page)) : -1;
+    return key == pos && (uint32_t)pg < (uint32_t)c.pages ? pg : -1;
+  };
+  const auto bias_of = [&](int group, int32_t pg) -> float {
+    float x = 0.f;
+    if (has_bias) {
+      const uint32_t key = min(key_of(group), (uint32_t)most);
+      const uint32_t tk = key - div_by(key, p.page) * p.page.d;
+      x = *(gptr_f32)(bbase + (uint64_t)((pg < 0 ? 0 : pg) * c.bias_stride[0] + tk * c.bias_stride[1]) * 4);
+    }
+    return pg < 0 ? -INFINITY : x;
+  };
+  const auto put_rows = [&](int group, int32_t pg, float bias) {
+    const uint32_t key = key_of(group);
+    const uint32_t tk = key - div_by(key, p.page) * p.page.d;
+    const bool live = bias != -INFINITY;
+    const uint64_t ka = kbase + (uint64_t)(pg * c.k_stride[0] + tk * c.k_stride[1]) * 2;
+    const uint64_t va = vbase + (uint64_t)(pg * c.v_stride[0] + tk * c.v_stride[1]) * 2;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    row_k[w][lane] = live ? ka : zero;
+    row_v[w][lane] = live ? va : zero;
+    const uint64_t ok = __ballot(live);
+    if (lane < W) {
+      char* to = (char*)&valid[group & 1][lane];
+      if constexpr (share == 8) ((uint8_t*)to)[w] = (uint8_t)(ok >> (lane * 8));
+      else ((uint16_t*)to)[w] = (uint16_t)(ok >> (lane * 16));
+    }
+    if constexpr (EXTRA) biases[group & 1][gs][gj] = bias;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  };
+  const int unit = lane % L::units, sub = lane / L::units;
+  const auto load_step = [&](int s, int buf) {         // keys and values of step s of its group
+#pragma unroll
+    for (int i = 0; i < L::loads; ++i) {
+      const int j = i * L::per_load + sub;             // row of this wave's share
+      const int row = w * share + j;
+      const uint64_t ka = row_k[w][s * share + j], va = row_v[w][s * share + j];
+      const int ku = unit ^ key_swizzle<DP>(row), vu = unit ^ value_swizzle<DP>(row);
+      const int dst = (w * share + i * L::per_load) * rb;
+      __builtin_amdgcn_global_load_lds((gptr32)((ku * 8 < D ? ka : zero) + ku * 16), (lptr32)(lk[buf] + dst), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((gptr32)((vu * 8 < D ? va : zero) + vu * 16), (lptr32)(lv[buf] + dst), 16, 0, 0);
+    }
+  };
+
+  floatx16_t o[L::dt];
+#pragma unroll
+  for (int i = 0; i < L::dt; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  const float unit_log2 = EXTRA ? kLog2e : a.scale * kLog2e;      // of a score as it is held
+  const float cap = a.softcap, inv_cap = cap > 0.f ? 1.f / cap : 0.f;
+  constexpr float shift = DT == FK_F16 ? 13.f : 0.f;
+  constexpr float slack = DT == FK_F16 ? 2.f : 8.f;
+
+  int32_t pg1 = -1, pg2 = -1;
+  float bias1 = -INFINITY;
+  if (t0 < t1) {
+    const int32_t pg0 = entry(0);
+    pg1 = entry(1), pg2 = entry(2);
+    put_rows(0, pg0, bias_of(0, pg0));
+    bias1 = bias_of(1, pg1);
+    load_step(0, 0);
+  }
+  for (int st = t0; st < t1; ++st) {
+    const int i = st - t0, buf = i & 1;
+    const uint64_t* ok_at = &valid[(i / W) & 1][i % W];
+    __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0): this wave's rows are in
+    __syncthreads();                                   // and everyone's; the last step's are done with
+    if (st + 1 < t1) {
+      const int next = i + 1;
+      if (next % W == 0) {
+        put_rows(next / W, pg1, bias1);
+        pg1 = pg2;
+        bias1 = bias_of(next / W + 1, pg1);
+        pg2 = entry(next / W + 2);
+      }
+      load_step(next % W, buf ^ 1);
+    }
+    const int key0 = st * kStep;
+    if (key0 >= high) continue;
+    // scores
+    floatx16_t s[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[u][j] = 0.f;
+      const char* base = lk[buf] + (u * 32 + n) * rb;
+#pragma unroll
+      for (int k = 0; k < L::kt; ++k) {
+        const uint4 x = *(const uint4*)(base + ((2 * k + h) ^ key_swizzle<DP>(n)) * 16);
+        s[u] = Mfma<DT>::run(x, q[k], s[u]);
+      }
+    }
+    if constexpr (EXTRA) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j4 = 0; j4 < 4; ++j4) {
+          const float4 bs = *(const float4*)&biases[(i / W) & 1][i % W][u * 32 + j4 * 8 + h * 4];
+          const float bb[4] = {bs.x, bs.y, bs.z, bs.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float x = s[u][j4 * 4 + j] * a.scale;
+            if (cap > 0.f) x = capped(x, cap, inv_cap);
+            s[u][j4 * 4 + j] = bb[j] == -INFINITY ? -INFINITY : x + bb[j];
+          }
+        }
+    }
+    const uint64_t ok = *ok_at;
+    const bool whole = (EXTRA || __builtin_amdgcn_readfirstlane((uint32_t)(ok & (ok >> 32))) == 0xFFFFFFFFu);
+    const bool masked = key0 + kStep > low || !whole;
+    if (masked) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int key = u * 32 + (j & 3) + 8 * (j >> 2) + 4 * h;
+          const bool live = key0 + key < limit && (EXTRA || ((ok >> key) & 1));
+          s[u][j] = live ? s[u][j] : -INFINITY;
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = fmaxf(top, s[u][j]);
+    top = max_halves(top);
+    if (__any((top - m) * unit_log2 > slack)) {
+      const float mn = fmaxf(m, top);
+      const float f = m == -INFINITY ? 0.f : fast_exp2((m - mn) * unit_log2);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < L::dt; ++d)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[d][j] *= f;
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    const float off = fmaf(-ref, unit_log2, shift);
+    float sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float x = EXTRA ? fast_exp2(fmaf(s[u][j] - ref, kLog2e, shift)) : fast_exp2(fmaf(s[u][j], unit_log2, off));
+        s[u][j] = x;
+        sum += x;
+      }
+    l += sum;
+    // values
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int sb = 0; sb < 2; ++sb) {
+        typedef typename Val<DT>::arith T;
+        typedef T T8 __attribute__((ext_vector_type(8)));
+        T8 pt;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) pt[j] = (T)s[u][sb * 8 + j];
+        const uint4 pr = __builtin_bit_cast(uint4, pt);
+        const int l16 = lane & 15, vr = u * 32 + sb * 16 + 4 * h + (l16 >> 2);
+#pragma unroll
+        for (int d = 0; d < L::dt; ++d) {
+          const int un = (d * 4 + ((lane >> 4) & 1) * 2 + ((l16 & 3) >> 1)) ^ value_swizzle<DP>(l16 >> 2);
+          const char* at_v = lv[buf] + vr * rb + un * 16 + (l16 & 1) * 8;
+          const uint2 lo = read_transposed(at_v), hi = read_transposed(at_v + 8 * rb);
+          o[d] = Mfma<DT>::run(make_uint4(lo.x, lo.y, hi.x, hi.y), pr, o[d]);
+        }
+      }
+  }
+  l = sum_halves(l);
+  if (!mine || t < 0 || t >= a.T) return;
+  const int64_t row = t * a.Hq + qh;
+  const float m_nat = EXTRA ? m : m * a.scale;
+  if (p.parts > 1 && steps > p.chunk) {
+    const int64_t at_o = ((int64_t)part * a.T * a.Hq + row);
+#pragma unroll
+    for (int d = 0; d < L::dt; ++d)
+#pragma unroll
+      for (int j4 = 0; j4 < 4; ++j4) {
+        const int e = d * 32 + j4 * 8 + h * 4;
+        if (e < D) *(float4*)(p.o + at_o * D + e) = make_float4(o[d][j4 * 4], o[d][j4 * 4 + 1], o[d][j4 * 4 + 2], o[d][j4 * 4 + 3]);
+      }
+    if (h == 0) p.ml[at_o * 2] = l == 0.f ? -INFINITY : m_nat, p.ml[at_o * 2 + 1] = l;
+    return;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int d = 0; d < L::dt; ++d)
+#pragma unroll
+    for (int j4 = 0; j4 < 4; ++j4) {
+      const int e = d * 32 + j4 * 8 + h * 4;
+      const float x[4] = {o[d][j4 * 4] * inv, o[d][j4 * 4 + 1] * inv, o[d][j4 * 4 + 2] * inv, o[d][j4 * 4 + 3] * inv};
+      if (e < D) store4<DT>(a.out, row * D + e, x);
+    }
+  if (a.lse && h == 0) a.lse[row] = l == 0.f ? -INFINITY : m_nat + (logf(l) - shift * kLn2);
+}
+
 template <int DT> hipError_t run_any(const PromptArgs& a, hipStream_t s) {
   const int64_t D = a.cache.dim, blocks = (a.T * a.Hq + kWaves - 1) / kWaves;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
@@ -100,6 +469,44 @@ template <int DT> hipError_t run_any(const PromptArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Rows the matrix-core kernel can load: whole, aligned 16-byte units.
+bool aligned16(const PromptArgs& a) {
+  const fk_kv_cache_t& c = a.cache;
+  const int64_t s[] = {a.q_stride[0], a.q_stride[1], c.k_stride[0], c.k_stride[1], c.k_stride[2],
+                       c.v_stride[0], c.v_stride[1], c.v_stride[2], c.dim};
+  for (int64_t v : s)
+    if (v % 8) return false;
+  return !(((uintptr_t)a.q | (uintptr_t)c.k | (uintptr_t)c.v | (uintptr_t)a.out) & 15);
+}
+
+template <int DT, int DP> hipError_t run_mfma(const PromptArgs& a, void* ws, hipStream_t s) {
+  PromptPlan p{};
+  p.heads = (int)a.cache.heads;
+  p.G = (int)(a.Hq / a.cache.heads);
+  const int64_t tiles = (a.T * p.G + Tile<DP>::rows - 1) / Tile<DP>::rows + a.B;
+  p.parts = 1, p.chunk = 0x7FFFFFFF / kStep;
+  p.page = fast_div((uint32_t)a.cache.page);
+  p.by_heads = fast_div((uint32_t)p.heads);
+  p.by_parts = fast_div((uint32_t)p.parts);
+  p.by_G = fast_div((uint32_t)p.G);
+  const int64_t blocks = tiles * p.heads * p.parts;
+  if (blocks > 0x7FFFFF || a.T * p.G > 0x7FFFFFFF - 512) return hipErrorInvalidConfiguration;
+  const bool extra = a.softcap > 0.f || a.cache.key_bias || !(a.scale > 0.f);
+  const auto kernel = extra ? prompt_mfma_kernel<DT, DP, true> : prompt_mfma_kernel<DT, DP, false>;
+  kernel<<<(unsigned)blocks, Tile<DP>::waves * 64, 0, s>>>(a, p);
+  return hipGetLastError();
+}
+
+template <int DT> hipError_t run(const PromptArgs& a, void* ws, hipStream_t s) {
+  if constexpr (DT != FK_F32) {
+    if (a.cache.dim <= 256 && aligned16(a))
+      return a.cache.dim <= 64    ? run_mfma<DT, 64>(a, ws, s)
+             : a.cache.dim <= 128 ? run_mfma<DT, 128>(a, ws, s)
+                                  : run_mfma<DT, 256>(a, ws, s);
+  }
+  return run_any<DT>(a, s);
+}
+
 }  // namespace
 
 size_t prompt_ws_bytes(int dt, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
@@ -107,9 +514,9 @@ size_t prompt_ws_bytes(int dt, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, in
 }
 
 hipError_t launch_prompt_attn(const PromptArgs& a, int dt, void* ws, hipStream_t s) {
-  return dt == FK_F32   ? run_any<FK_F32>(a, s)
-         : dt == FK_F16 ? run_any<FK_F16>(a, s)
-                        : run_any<FK_BF16>(a, s);
+  return dt == FK_F32   ? run<FK_F32>(a, ws, s)
+         : dt == FK_F16 ? run<FK_F16>(a, ws, s)
+                        : run<FK_BF16>(a, ws, s);
 }
 
 }  // namespace fk
