@@ -66,7 +66,7 @@ int64_t any_parts(int64_t B, int64_t Hq) {
 }
 
 // Keys of the longest request, at most: what the tables hold, or the caller's bound.
-int64_t longest(const AttnArgs& a) {
+template <class Args> int64_t longest(const Args& a) {
   int64_t most = a.width * a.cache.page;
   if (most > 0x7FFFFFFF) most = 0x7FFFFFFF;
   return a.max_len > 0 && a.max_len < most ? a.max_len : most;

@@ -187,6 +187,11 @@ __device__ __forceinline__ Where find_tile(const PromptArgs& a, int G, int rows,
   return {-1, 0};
 }
 
+// fp16 probabilities are scaled by 2^13, and may pass the running maximum's by 2^2, bf16 by 2^8:
+// the sums are scaled anew only when a maximum grows by more.
+template <int DT> constexpr float prob_shift = DT == FK_F16 ? 13.f : 0.f;
+template <int DT> constexpr float prob_slack = DT == FK_F16 ? 2.f : 8.f;
+
 struct PromptPlan {
   int heads, G, parts, chunk;     // cache heads, query heads of each, parts of a row's keys, steps of a part
   FastDiv page, by_heads, by_parts, by_G;
@@ -223,7 +228,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   };
   const int most = __builtin_amdgcn_readfirstlane(seen(rows - 1));      // of the tile's last row
   const int steps = (int)(((uint32_t)most + kStep - 1) / kStep);
-  const int t0 = (int)part * p.chunk, t1 = min(steps, t0 + p.chunk);
+  const int t0 = (int)part * p.chunk, t1 = (int)part == p.parts - 1 ? steps : min(steps, t0 + p.chunk);
   if (t0 >= t1 && part > 0) return;                    // (part 0 leaves the results of empty rows)
 
   // queries; rows past the tile's end are zero, see everything and are not stored
@@ -311,8 +316,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   float m = -INFINITY, l = 0.f;
   const float unit_log2 = EXTRA ? kLog2e : a.scale * kLog2e;      // of a score as it is held
   const float cap = a.softcap, inv_cap = cap > 0.f ? 1.f / cap : 0.f;
-  constexpr float shift = DT == FK_F16 ? 13.f : 0.f;
-  constexpr float slack = DT == FK_F16 ? 2.f : 8.f;
+  constexpr float shift = prob_shift<DT>, slack = prob_slack<DT>;
 
   int32_t pg1 = -1, pg2 = -1;
   float bias1 = -INFINITY;
@@ -469,6 +473,65 @@ template <int DT> hipError_t run_any(const PromptArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Joins the partial results of rows whose keys were cut, a row a wave.
+template <int DT, int EPL>
+__global__ __launch_bounds__(kWaves * 64) void prompt_join_kernel(PromptArgs a, PromptPlan p, int rows) {
+  const int64_t r = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int64_t t = r / a.Hq, b = t < a.T ? request_of(a, t) : -1;
+  if (b < 0) return;
+  const int lane = threadIdx.x & 63, D = (int)a.cache.dim;
+  // steps of the row's tile, by its last row
+  const int64_t n = (a.cu[b + 1] - a.cu[b]) * (int64_t)p.G;
+  const int64_t own = (t - a.cu[b]) * p.G + (r - t * a.Hq) % p.G;
+  const int64_t last = min((own / rows + 1) * rows, n) - 1;
+  const int64_t steps = (seen_by(a, b, a.cu[b] + last / p.G) + kStep - 1) / kStep;
+  if (steps <= p.chunk) return;
+  const int parts = (int)min((int64_t)p.parts, (steps + p.chunk - 1) / p.chunk);
+  const int64_t every = a.T * a.Hq;
+  float m = -INFINITY, l = 0.f, o[EPL];
+  for (int i = 0; i < parts; ++i) m = fmaxf(m, p.ml[(i * every + r) * 2]);
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    const float2 ml = *(const float2*)(p.ml + (i * every + r) * 2);
+    const float f = join_factor(ml.x, ml.y, m);
+    l = fmaf(f, ml.y, l);
+#pragma unroll
+    for (int e = 0; e < EPL; ++e)
+      if (lane + 64 * e < D) o[e] = fmaf(f, p.o[(i * every + r) * D + lane + 64 * e], o[e]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < EPL; ++e)
+    if (lane + 64 * e < D)
+      Val<DT>::put((typename Val<DT>::type*)a.out + r * D + lane + 64 * e, o[e] * inv);
+  if (a.lse && lane == 0) a.lse[r] = l == 0.f ? -INFINITY : m + (logf(l) - prob_shift<DT> * kLn2);
+}
+
+// Parts that a row's keys may be cut into: two rounds of blocks over the chip at most.
+int64_t most_parts(int64_t T, int64_t G, int64_t heads, int64_t rows) {
+  const int64_t units = (T * G + rows - 1) / rows * heads;
+  const int64_t n = 2 * kMaxCus / (units < 1 ? 1 : units);
+  return n < 1 ? 1 : (n > 64 ? 64 : n);
+}
+
+// Parts of a call: the number with the shortest estimate, in steps of one block. A block spends
+// about 4 steps' time before and after its steps, and 4 more on a partial result.
+int parts_of_call(int64_t units, int64_t cus, int64_t longest, double mean, int64_t most) {
+  int best = 1;
+  double least = 1e300;
+  for (int64_t n = 1; n <= most && (n == 1 || longest / n >= 8); ++n) {
+    const double fixed = n > 1 ? 8 : 4, one = (double)((longest + n - 1) / n) + fixed;
+    double time = one;
+    if (units * n > cus) {
+      const double all = (double)units * (mean + n * fixed) / cus;
+      time = (all > one ? all : one) + 0.5 * one;
+    }
+    if (time < least) least = time, best = (int)n;
+  }
+  return best;
+}
+
 // Rows the matrix-core kernel can load: whole, aligned 16-byte units.
 bool aligned16(const PromptArgs& a) {
   const fk_kv_cache_t& c = a.cache;
@@ -483,8 +546,17 @@ template <int DT, int DP> hipError_t run_mfma(const PromptArgs& a, void* ws, hip
   PromptPlan p{};
   p.heads = (int)a.cache.heads;
   p.G = (int)(a.Hq / a.cache.heads);
-  const int64_t tiles = (a.T * p.G + Tile<DP>::rows - 1) / Tile<DP>::rows + a.B;
-  p.parts = 1, p.chunk = 0x7FFFFFFF / kStep;
+  constexpr int rows = Tile<DP>::rows;
+  const int64_t full = (a.T * p.G + rows - 1) / rows;      // at least so many tiles
+  const int64_t tiles = full + a.B - 1;                    // and at most so many
+  const int64_t most = longest(a), longest_steps = (most + kStep - 1) / kStep;
+  // mean keys of a row: all but half the tokens, as far as is known here
+  const double mean = most <= 0 ? 0. : (most - 0.5 * (double)(a.T / a.B < most ? a.T / a.B : most)) / kStep;
+  p.parts = parts_of_call((full > a.B ? full : a.B) * p.heads, device_cus(), longest_steps, mean,
+                          most_parts(a.T, p.G, p.heads, rows));
+  p.chunk = p.parts == 1 ? 0x7FFFFFFF / kStep : (int)((longest_steps + p.parts - 1) / p.parts);
+  p.o = (float*)ws;
+  p.ml = p.o + (int64_t)p.parts * a.T * a.Hq * a.cache.dim;
   p.page = fast_div((uint32_t)a.cache.page);
   p.by_heads = fast_div((uint32_t)p.heads);
   p.by_parts = fast_div((uint32_t)p.parts);
@@ -494,6 +566,9 @@ template <int DT, int DP> hipError_t run_mfma(const PromptArgs& a, void* ws, hip
   const bool extra = a.softcap > 0.f || a.cache.key_bias || !(a.scale > 0.f);
   const auto kernel = extra ? prompt_mfma_kernel<DT, DP, true> : prompt_mfma_kernel<DT, DP, false>;
   kernel<<<(unsigned)blocks, Tile<DP>::waves * 64, 0, s>>>(a, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.parts == 1) return e;
+  prompt_join_kernel<DT, DP / 64><<<(unsigned)((a.T * a.Hq + kWaves - 1) / kWaves), kWaves * 64, 0, s>>>(a, p, rows);
   return hipGetLastError();
 }
 
@@ -510,7 +585,10 @@ template <int DT> hipError_t run(const PromptArgs& a, void* ws, hipStream_t s) {
 }  // namespace
 
 size_t prompt_ws_bytes(int dt, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
-  return 0;
+  if (D > 256 || dt == FK_F32) return 0;
+  const int64_t rows = D <= 128 ? Tile<128>::rows : Tile<256>::rows;
+  const int64_t parts = most_parts(T, Hq / Hkv, Hkv, rows);
+  return parts == 1 ? 0 : (size_t)(parts * T * Hq) * (D + 2) * 4;
 }
 
 hipError_t launch_prompt_attn(const PromptArgs& a, int dt, void* ws, hipStream_t s) {
