@@ -120,5 +120,6 @@ struct PromptArgs {
 };
 size_t prompt_ws_bytes(int dt, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
 hipError_t launch_prompt_attn(const PromptArgs& a, int dt, void* ws, hipStream_t s);
+hipError_t launch_prompt_wide(const PromptArgs& a, int dt, void* ws, hipStream_t s);   // rows of 129 to 256
 
 }  // namespace fk

@@ -1,0 +1,678 @@
+// Attention of a step's prompts over a paged key-value cache: every new token over
+// its request's keys up to itself. The kernels; prompt.hip and prompt_wide.hip build them.
+#pragma once
+
+#include <type_traits>
+
+#include "attn_parts.hpp"
+
+namespace fk {
+namespace {
+
+// Request of token t: the last one that starts at or before it and is not empty; -1: none.
+__device__ __forceinline__ int64_t request_of(const PromptArgs& a, int64_t t) {
+  int64_t lo = 0, hi = a.B;                // first b with cu[b + 1] > t
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (a.cu[mid + 1] > t) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo < a.B && a.cu[lo] <= t ? lo : -1;
+}
+
+// Keys that token t of request b sees.
+__device__ __forceinline__ int64_t seen_by(const PromptArgs& a, int64_t b, int64_t t) {
+  const int64_t held = a.width * a.cache.page;
+  const int64_t n = (int64_t)a.lens[b] - a.cu[b + 1] + t + 1;
+  return n < 0 ? 0 : (n < held ? n : held);
+}
+
+// One row (token t, query head h) of request b over keys j0 .. j1 - 1, any size, stride and
+// alignment, by one wave: a lane holds every 64th element of the sums o.
+template <int DT, int EPL>
+__device__ __forceinline__ void row_sums(const PromptArgs& a, int64_t b, int64_t t, int64_t h, int64_t j0,
+                                         int64_t j1, float& m, float& l, float (&o)[EPL]) {
+  using E = typename Val<DT>::type;
+  const int lane = threadIdx.x & 63;
+  const fk_kv_cache_t& c = a.cache;
+  const int D = (int)c.dim;
+  const int64_t hk = h / (a.Hq / c.heads);
+  const E* q = (const E*)a.q + t * a.q_stride[0] + h * a.q_stride[1];
+  float qf[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + 64 * i;
+    qf[i] = e < D ? Val<DT>::get(q + e) : 0.f;
+    o[i] = 0.f;
+  }
+  m = -INFINITY, l = 0.f;
+  for (int64_t j = j0; j < j1; ++j) {
+    const int64_t page = a.table[b * a.ld_table + j / c.page], tok = j % c.page;
+    if (page < 0 || page >= c.pages) continue;
+    float bias = 0.f;
+    if (c.key_bias) {
+      bias = c.key_bias[page * c.bias_stride[0] + tok * c.bias_stride[1] + hk * c.bias_stride[2]];
+      if (bias == -INFINITY) continue;
+    }
+    const E* k = (const E*)c.k + page * c.k_stride[0] + tok * c.k_stride[1] + hk * c.k_stride[2];
+    const E* v = (const E*)c.v + page * c.v_stride[0] + tok * c.v_stride[1] + hk * c.v_stride[2];
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane + 64 * i;
+      if (e < D) s = fmaf(qf[i], Val<DT>::get(k + e), s);
+    }
+    s = wave_sum(s) * a.scale;
+    if (a.softcap > 0.f) s = capped(s, a.softcap, 1.f / a.softcap);
+    s += bias;
+    const float mn = fmaxf(m, s);
+    const float alpha = m == -INFINITY ? 0.f : fast_exp2((m - mn) * kLog2e);
+    const float p = s == -INFINITY ? 0.f : fast_exp2((s - mn) * kLog2e);   // NaN stays NaN
+    l = l * alpha + p;
+    m = mn;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane + 64 * i;
+      if (e < D) o[i] = fmaf(p, Val<DT>::get(v + e), o[i] * alpha);
+    }
+  }
+}
+
+// A row's result.
+template <int DT, int EPL>
+__device__ __forceinline__ void put_row(const PromptArgs& a, int64_t row, float m, float l,
+                                        const float (&o)[EPL]) {
+  const int lane = threadIdx.x & 63, D = (int)a.cache.dim;
+  const bool any = l != 0.f;             // true for NaN: it has to reach the result
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + 64 * i;
+    if (e < D) Val<DT>::put((typename Val<DT>::type*)a.out + row * D + e, any ? o[i] / l : 0.f);
+  }
+  if (a.lse && lane == 0) a.lse[row] = any ? m + logf(l) : -INFINITY;
+}
+
+// ---------------------------------------------------------------------------
+// Matrix-core kernel of 16-bit caches: rows of at most 256 elements in whole 16-byte units
+// ---------------------------------------------------------------------------
+// The G query heads of a cache head see the same keys, so row r of a request is head r % G
+// of token r / G, and a tile is kRows rows in a run. A block takes one tile of one cache head
+// over a range of keys, a wave 32 of its rows, 64 keys a step.
+//
+// Lane (n = lane & 31, h = lane >> 5) of a wave. Scores are S^T = K Q^T with v_mfma 32x32x16:
+// register i of the lane holds the score of query row n with key (i & 3) + 8 (i >> 2) + 4 h of
+// 32. The values enter as O^T = V^T P^T: the contraction runs over keys, whose order is
+// free, so the eight probabilities a lane gives to a product are those it holds, of keys 4 h +
+// 0..3 and 8 + 4 h + 0..3 of 16, and V^T comes from LDS in that order by transposing reads
+// (four keys of one element a lane each). Nothing but keys and values goes through LDS.
+//
+// Keys and values go from the cache's pages straight to LDS, 16 bytes a lane, two buffers in
+// turn. Each wave brings 64 / waves rows a step; their addresses are found for as many
+// steps at once as make up 64, and table entries and biases are asked for two such groups ahead.
+typedef const __attribute__((address_space(1))) uint32_t* gptr32;
+typedef __attribute__((address_space(3))) uint32_t* lptr32;
+
+// Waves of a block: 8 share the keys of a step; wide rows need the registers of 4.
+constexpr int tile_waves(int DC) { return DC > 128 ? 4 : 8; }
+
+template <int DT, int DC> struct Tile {
+  static constexpr int eb = Val<DT>::bytes;
+  static constexpr int pitch = DC <= 64 ? 64 : (DC <= 128 ? 128 : 256);    // elements of a row in LDS
+  static constexpr int rb = pitch * eb;                   // and bytes
+  static constexpr int waves = tile_waves(DC);
+  static constexpr int rows = waves * 32;
+  static constexpr int step = rb > 512 ? 32 : 64;         // keys a step: two buffers fit the LDS
+  static constexpr int key_tiles = step / 32;
+  static constexpr int unit = 16 / eb;                    // elements of 16 bytes
+  static constexpr int units = pitch / unit;              // 16-byte units of a row
+  static constexpr int per_load = 64 / units;             // rows a wave brings with one load
+  static constexpr int share = step / waves;              // rows a wave brings a step
+  static constexpr int loads = share / per_load;
+  static constexpr int group = 64 / share;                // steps whose rows a wave finds at once
+  static constexpr int dt = DC / 32, kt = DC / (2 * unit);        // tiles of the output, units of a score
+};
+
+// Where unit u of row r lies in its LDS row. Scores read one unit of 32 rows at once: 16
+// neighbouring rows are 16 different units. Transposing reads take two units of four
+// rows, or four of them: the rows are put 2 and 4 units apart, mod 8 and mod 16. fp32 values are
+// read 32 elements of two rows at once, four rows apart: one of them 8 units on.
+template <class L> __device__ __forceinline__ int key_swizzle(int r) { return r & (L::units - 1) & 15; }
+template <class L> __device__ __forceinline__ int value_swizzle(int r) {
+  if constexpr (L::eb == 4) return (r & 4) << 1;
+  if constexpr (L::units == 8) return (r & 1) << 1 | (r & 2) << 1;
+  return (r & 1) << 2 | (r & 2) << 2 | (r & 2);
+}
+
+// Both halves' numbers of a wave, in every lane: (of lanes 0..31, of lanes 32..63).
+__device__ __forceinline__ floatx2_t both_halves(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t lo = r.x, hi = r.y;       // (a bit cast of an element itself takes the first one's)
+  return floatx2_t{__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
+}
+__device__ __forceinline__ float max_halves(float x) {
+  const floatx2_t r = both_halves(x);
+  return fmaxf(r.x, r.y);
+}
+__device__ __forceinline__ float sum_halves(float x) {
+  const floatx2_t r = both_halves(x);
+  return r.x + r.y;
+}
+
+// Four keys of one element each, 16 lanes a 4 x 16 block that lies in LDS key by key.
+__device__ __forceinline__ uint2 read_transposed(const char* at) {
+  typedef short s4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s4* lp;
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)at));
+}
+
+// The tile of a block: requests are taken from the last one on, their tiles likewise, so that
+// the longest rows of a prompt come first and the chip does not wait for one at the end.
+struct Where {
+  int64_t b;          // request, -1: none
+  int tile;           // tile of its rows
+};
+__device__ __forceinline__ Where find_tile(const PromptArgs& a, int G, int rows, uint32_t order) {
+  const int lane = threadIdx.x & 63;
+  uint32_t before = 0;
+  for (int64_t last = a.B - 1; last >= 0; last -= 64) {
+    const int64_t b = last - lane;
+    uint32_t mine = 0;
+    if (b >= 0) {
+      const int64_t n = (int64_t)a.cu[b + 1] - a.cu[b];
+      mine = n > 0 ? (uint32_t)((n * G + rows - 1) / rows) : 0;
+    }
+    uint32_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const uint32_t o = __shfl_up(incl, off, 64);
+      if (lane >= off) incl += o;
+    }
+    const uint32_t total = __builtin_amdgcn_readlane(incl, 63);
+    if (order < before + total) {
+      const int at = __popcll(__ballot(before + incl <= order));
+      const uint32_t end = before + __builtin_amdgcn_readlane(incl, at);
+      return {last - at, (int)(end - 1 - order)};
+    }
+    before += total;
+  }
+  return {-1, 0};
+}
+
+// fp16 probabilities are scaled by 2^13, and may pass the running maximum's by 2^2, bf16 by 2^8:
+// the sums are scaled anew only when a maximum grows by more.
+template <int DT> constexpr float prob_shift = DT == FK_F16 ? 13.f : 0.f;
+template <int DT> constexpr float prob_slack = DT == FK_F16 ? 2.f : 8.f;
+
+// Which of a lane's sums are not finite, a bit each.
+template <int N> struct NotFinite { uint32_t bits[(N + 1) / 2]; };
+template <int N> __device__ __forceinline__ NotFinite<N> not_finite(const floatx16_t (&o)[N]) {
+  NotFinite<N> r = {};
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) r.bits[i / 2] |= (o[i][j] - o[i][j] == 0.f ? 0u : 1u) << ((i & 1) * 16 + j);
+  return r;
+}
+template <int N> __device__ __forceinline__ bool all_finite(const floatx16_t (&o)[N]) {
+  float x = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x = fmaf(o[i][j], 0.f, x);
+  return x == 0.f;
+}
+template <int N> __device__ __forceinline__ bool newly(const NotFinite<N>& now, const NotFinite<N>& before) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < (N + 1) / 2; ++i) r |= now.bits[i] & ~before.bits[i];
+  return r != 0;
+}
+
+struct PromptPlan {
+  int heads, G, parts, chunk;     // cache heads, query heads of each, parts of a row's keys, steps of a part
+  FastDiv page, by_heads, by_parts, by_G;
+  float* o;                       // (parts, T, Hq, D) partial sums
+  float* ml;                      // (parts, T, Hq, 2) their maximum and sum
+};
+
+template <int DT, int DC, bool EXTRA>
+__global__ __launch_bounds__(tile_waves(DC) * 64, tile_waves(DC) / 4)
+void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
+  using L = Tile<DT, DC>;
+  constexpr int W = L::waves, rb = L::rb, eb = L::eb, kStep = L::step, KT = L::key_tiles, GS = L::group;
+  __shared__ __attribute__((aligned(1024))) char lk[2][kStep * rb], lv[2][kStep * rb];
+  __shared__ uint64_t row_k[W][64], row_v[W][64];
+  __shared__ uint64_t valid[2][GS];                    // keys of a step that count, a bit each
+  __shared__ float biases[EXTRA ? 2 : 1][EXTRA ? GS : 1][kStep];
+  __shared__ NotFinite<L::dt> broken[W * 64];          // sums that were not finite before hidden keys came
+  const fk_kv_cache_t& c = a.cache;
+  const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int D = (int)c.dim;
+
+  const uint32_t rest = div_by(blockIdx.x, p.by_heads), hk = blockIdx.x - rest * p.heads;
+  const uint32_t order = div_by(rest, p.by_parts), part = rest - order * p.parts;
+  const Where at = find_tile(a, p.G, L::rows, order);
+  if (at.b < 0) return;
+  const int64_t b = uniform(at.b);
+  const int64_t cu0 = a.cu[b], cu1 = a.cu[b + 1], len = a.lens[b];
+  const int rows = (int)min((cu1 - cu0) * p.G - (int64_t)at.tile * L::rows, (int64_t)L::rows);
+  const int64_t held = min(a.width * c.page, (int64_t)0x7FFFFFC0);
+  // keys that row r of the tile sees
+  const auto seen = [&](int r) {
+    const int64_t t = div_by((uint32_t)(at.tile * L::rows + r), p.by_G);
+    return (int)max((int64_t)0, min(len - (cu1 - cu0) + t + 1, held));
+  };
+  const int most = __builtin_amdgcn_readfirstlane(seen(rows - 1));      // of the tile's last row
+  const int steps = (int)(((uint32_t)most + kStep - 1) / kStep);
+  const int t0 = (int)part * p.chunk, t1 = (int)part == p.parts - 1 ? steps : min(steps, t0 + p.chunk);
+  if (t0 >= t1 && part > 0) return;                    // (part 0 leaves the results of empty rows)
+
+  // queries; rows past the tile's end are zero, see everything and are not stored
+  const int r = w * 32 + n;
+  const bool mine = r < rows;
+  const uint32_t rr = at.tile * L::rows + min(r, rows - 1);
+  const int64_t tok = div_by(rr, p.by_G);
+  const int64_t t = cu0 + tok, qh = (int64_t)hk * p.G + (rr - tok * p.G);
+  const int limit = mine ? seen(r) : 0x7FFFFFFF;
+  const int wave_rows = min(rows - w * 32, 32);        // none or fewer: nothing to do
+  const int low = wave_rows > 0 ? __builtin_amdgcn_readfirstlane(seen(w * 32)) : 0;
+  const int high = wave_rows > 0 ? __builtin_amdgcn_readfirstlane(seen(w * 32 + wave_rows - 1)) : 0;
+  uint4 q[L::kt];
+  {
+    const uint64_t qp = (uint64_t)a.q + (uint64_t)(t * a.q_stride[0] + qh * a.q_stride[1]) * eb;
+#pragma unroll
+    for (int i = 0; i < L::kt; ++i) {
+      const int e = (2 * i + h) * L::unit;
+      q[i] = load16(e < D && mine && t >= 0 && t < a.T ? qp + e * eb : (uint64_t)zero_row);
+    }
+  }
+
+  // rows of keys: lane (s, j) looks after row j of this wave's share in step s of a group
+  constexpr int share = L::share;
+  const int gs = lane / share, gj = w * share + lane % share;
+  const uint64_t table = (uint64_t)(a.table + b * a.ld_table);
+  const uint64_t kbase = (uint64_t)c.k + (uint64_t)hk * c.k_stride[2] * eb;
+  const uint64_t vbase = (uint64_t)c.v + (uint64_t)hk * c.v_stride[2] * eb;
+  const uint64_t bbase = (uint64_t)c.key_bias + (uint64_t)hk * c.bias_stride[2] * 4;
+  const uint64_t zero = (uint64_t)zero_row;
+  const bool has_bias = EXTRA && c.key_bias && c.pages > 0;
+  const auto key_of = [&](int group) { return (uint32_t)(t0 + group * GS + gs) * kStep + gj; };
+  const auto entry = [&](int group) -> int32_t {       // page of the lane's key, -1: none
+    const uint32_t key = key_of(group), last = most > 0 ? most - 1 : 0;
+    const uint32_t pos = min(key, last);
+    const int32_t pg = most > 0 ? *(gptr_i32)(table + 4 * (uint64_t)div_by(pos, p.page)) : -1;
+    return key == pos && (uint32_t)pg < (uint32_t)c.pages ? pg : -1;
+  };
+  const auto bias_of = [&](int group, int32_t pg) -> float {
+    float x = 0.f;
+    if (has_bias) {
+      const uint32_t key = min(key_of(group), (uint32_t)most);
+      const uint32_t tk = key - div_by(key, p.page) * p.page.d;
+      x = *(gptr_f32)(bbase + (uint64_t)((pg < 0 ? 0 : pg) * c.bias_stride[0] + tk * c.bias_stride[1]) * 4);
+    }
+    return pg < 0 ? -INFINITY : x;
+  };
+  const auto put_rows = [&](int group, int32_t pg, float bias) {
+    const uint32_t key = key_of(group);
+    const uint32_t tk = key - div_by(key, p.page) * p.page.d;
+    const bool live = bias != -INFINITY;
+    const uint64_t ka = kbase + (uint64_t)(pg * c.k_stride[0] + tk * c.k_stride[1]) * eb;
+    const uint64_t va = vbase + (uint64_t)(pg * c.v_stride[0] + tk * c.v_stride[1]) * eb;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    row_k[w][lane] = live ? ka : zero;
+    row_v[w][lane] = live ? va : zero;
+    const uint64_t ok = __ballot(live);
+    if (lane < GS) {
+      char* to = (char*)&valid[group & 1][lane];
+      if constexpr (share == 8) ((uint8_t*)to)[w] = (uint8_t)(ok >> (lane * 8));
+      else ((uint16_t*)to)[w] = (uint16_t)(ok >> (lane * 16));
+    }
+    if constexpr (EXTRA) biases[group & 1][gs][gj] = bias;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  };
+  const int unit = lane % L::units, sub = lane / L::units;
+  const auto load_step = [&](int s, int buf) {         // keys and values of step s of its group
+#pragma unroll
+    for (int i = 0; i < L::loads; ++i) {
+      const int j = i * L::per_load + sub;             // row of this wave's share
+      const int row = w * share + j;
+      const uint64_t ka = row_k[w][s * share + j], va = row_v[w][s * share + j];
+      const int ku = unit ^ key_swizzle<L>(row), vu = unit ^ value_swizzle<L>(row);
+      const int dst = (w * share + i * L::per_load) * rb;
+      // (units past DC are never read)
+      if (DC == L::pitch || ku * L::unit < DC)
+        __builtin_amdgcn_global_load_lds((gptr32)((ku * L::unit < D ? ka : zero) + ku * 16), (lptr32)(lk[buf] + dst), 16, 0, 0);
+      if (DC == L::pitch || vu * L::unit < DC)
+        __builtin_amdgcn_global_load_lds((gptr32)((vu * L::unit < D ? va : zero) + vu * 16), (lptr32)(lv[buf] + dst), 16, 0, 0);
+    }
+  };
+
+  floatx16_t o[L::dt];
+#pragma unroll
+  for (int i = 0; i < L::dt; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  bool looked = false, broken_before = false;
+  const float unit_log2 = EXTRA ? kLog2e : a.scale * kLog2e;      // of a score as it is held
+  const float cap = a.softcap, inv_cap = cap > 0.f ? 1.f / cap : 0.f;
+  constexpr float shift = prob_shift<DT>, slack = prob_slack<DT>;
+
+  int32_t pg1 = -1, pg2 = -1;
+  float bias1 = -INFINITY;
+  if (t0 < t1) {
+    const int32_t pg0 = entry(0);
+    pg1 = entry(1), pg2 = entry(2);
+    put_rows(0, pg0, bias_of(0, pg0));
+    bias1 = bias_of(1, pg1);
+    load_step(0, 0);
+  }
+  const auto all_valid = [&](int st) {                 // every key of step st counts
+    const int i = st - t0;
+    const uint64_t ok = valid[(i / GS) & 1][i % GS];
+    const uint32_t both = kStep == 32 ? (uint32_t)ok : (uint32_t)(ok & (ok >> 32));
+    return __builtin_amdgcn_readfirstlane(both) == 0xFFFFFFFFu;
+  };
+  // One step: scores, probabilities, sums. masked: some key of it is hidden from some row.
+  const auto compute = [&](int st, auto tag) {
+    constexpr bool masked = decltype(tag)::value;
+    const int i = st - t0, buf = i & 1, key0 = st * kStep;
+    // scores
+    floatx16_t s[KT];
+#pragma unroll
+    for (int u = 0; u < KT; ++u) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[u][j] = 0.f;
+      const char* base = lk[buf] + (u * 32 + n) * rb;
+#pragma unroll
+      for (int k = 0; k < L::kt; ++k) {
+        const uint4 x = *(const uint4*)(base + ((2 * k + h) ^ key_swizzle<L>(n)) * 16);
+        s[u] = Mfma<DT>::run(x, q[k], s[u]);
+      }
+    }
+    if constexpr (EXTRA) {
+#pragma unroll
+      for (int u = 0; u < KT; ++u)
+#pragma unroll
+        for (int j4 = 0; j4 < 4; ++j4) {
+          const float4 bs = *(const float4*)&biases[(i / GS) & 1][i % GS][u * 32 + j4 * 8 + h * 4];
+          const float bb[4] = {bs.x, bs.y, bs.z, bs.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float x = s[u][j4 * 4 + j] * a.scale;
+            if (cap > 0.f) x = capped(x, cap, inv_cap);
+            s[u][j4 * 4 + j] = bb[j] == -INFINITY ? -INFINITY : x + bb[j];
+          }
+        }
+    }
+    if constexpr (masked) {
+      const uint64_t ok = valid[(i / GS) & 1][i % GS];
+#pragma unroll
+      for (int u = 0; u < KT; ++u)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int key = u * 32 + (j & 3) + 8 * (j >> 2) + 4 * h;
+          const bool live = key0 + key < limit && (EXTRA || ((ok >> key) & 1));
+          s[u][j] = live ? s[u][j] : -INFINITY;
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int u = 0; u < KT; ++u)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = fmaxf(top, s[u][j]);
+    top = max_halves(top);
+    if (__any((top - m) * unit_log2 > slack)) {
+      const float mn = fmaxf(m, top);
+      const float f = m == -INFINITY ? 0.f : fast_exp2((m - mn) * unit_log2);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < L::dt; ++d)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[d][j] *= f;
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    const float off = fmaf(-ref, unit_log2, shift);
+    float sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < KT; ++u)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        float x;
+        if constexpr (DT == FK_F32) x = prob<DT>(s[u][j] - ref);
+        else if constexpr (EXTRA) x = fast_exp2(fmaf(s[u][j] - ref, kLog2e, shift));
+        else x = fast_exp2(fmaf(s[u][j], unit_log2, off));
+        s[u][j] = x;
+        sum += x;
+      }
+    l += sum;
+    // values
+    if constexpr (DT == FK_F32) {
+#pragma unroll
+      for (int u = 0; u < KT; ++u)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int vr = u * 32 + (j & 3) + 8 * (j >> 2) + 4 * h;
+#pragma unroll
+          for (int d = 0; d < L::dt; ++d) {
+            const int un = (d * 8 + (n >> 2)) ^ value_swizzle<L>(4 * h);
+            const float x = *(const float*)(lv[buf] + vr * rb + un * 16 + (n & 3) * 4);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, s[u][j], o[d], 0, 0, 0);
+          }
+        }
+    } else {
+#pragma unroll
+      for (int u = 0; u < KT; ++u)
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb) {
+          typedef typename Val<DT>::arith T;
+          typedef T T8 __attribute__((ext_vector_type(8)));
+          T8 pt;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) pt[j] = (T)s[u][sb * 8 + j];
+          // an infinite value times a probability that rounds to 0 would be NaN; in steps
+          // that hide no key 2^-24 (2^-37 of the largest one) stands for those
+          if constexpr (DT == FK_F16)
+            if (!masked) pt = __builtin_elementwise_max(pt, (T8)(T)0x1p-24f);
+          const uint4 pr = __builtin_bit_cast(uint4, pt);
+          const int l16 = lane & 15, vr = u * 32 + sb * 16 + 4 * h + (l16 >> 2);
+#pragma unroll
+          for (int d = 0; d < L::dt; ++d) {
+            const int un = (d * 4 + ((lane >> 4) & 1) * 2 + ((l16 & 3) >> 1)) ^ value_swizzle<L>(l16 >> 2);
+            const char* at_v = lv[buf] + vr * rb + un * 16 + (l16 & 1) * 8;
+            const uint2 lo = read_transposed(at_v), hi = read_transposed(at_v + 8 * rb);
+            o[d] = Mfma<DT>::run(make_uint4(lo.x, lo.y, hi.x, hi.y), pr, o[d]);
+          }
+        }
+    }
+  };
+  // Waits for the rows of step st and asks for the next one's.
+  const auto arrive = [&](int st) {
+    const int i = st - t0, buf = i & 1;
+    __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0): this wave's rows are in
+    __syncthreads();                                   // and everyone's; the last step's are done with
+    if (st + 1 < t1) {
+      const int next = i + 1;
+      if (next % GS == 0) {
+        put_rows(next / GS, pg1, bias1);
+        pg1 = pg2;
+        bias1 = bias_of(next / GS + 1, pg1);
+        pg2 = entry(next / GS + 2);
+      }
+      load_step(next % GS, buf ^ 1);
+    }
+  };
+  // Steps that every row sees whole, then the others: every wave changes over in its own time
+  // (a barrier counts waves, wherever they stand). fp32 products take longer than the
+  // masks.
+  int st = t0;
+  if constexpr (DT != FK_F32) {
+    for (; st < t1 && (st + 1) * kStep <= low; ++st) {
+      arrive(st);
+      if (!EXTRA && !all_valid(st)) break;
+      compute(st, std::false_type());
+    }
+  }
+  // (a step that was found to have keys missing has arrived)
+  bool here = !EXTRA && DT != FK_F32 && st < t1 && (st + 1) * kStep <= low;
+  for (; st < t1; ++st, here = false) {
+    if (!here) arrive(st);
+    const int key0 = st * kStep;
+    if (key0 >= high) continue;
+    if (!looked && key0 + kStep > low) {
+      looked = true;
+      broken_before = __any(!all_finite<L::dt>(o));
+      if (broken_before) broken[threadIdx.x] = not_finite<L::dt>(o);
+    }
+    compute(st, std::true_type());
+  }
+  l = sum_halves(l);
+  const int64_t row = t * a.Hq + qh;
+  const float m_nat = EXTRA ? m : m * a.scale;
+  const bool cut = p.parts > 1 && steps > p.chunk;
+  const bool put = mine && t >= 0 && t < a.T;
+  const int64_t at_o = (int64_t)part * a.T * a.Hq + row;
+  if (put && cut) {
+#pragma unroll
+    for (int d = 0; d < L::dt; ++d)
+#pragma unroll
+      for (int j4 = 0; j4 < 4; ++j4) {
+        const int e = d * 32 + j4 * 8 + h * 4;
+        if (e < D) *(float4*)(p.o + at_o * D + e) = make_float4(o[d][j4 * 4], o[d][j4 * 4 + 1], o[d][j4 * 4 + 2], o[d][j4 * 4 + 3]);
+      }
+    if (h == 0) p.ml[at_o * 2] = l == 0.f ? -INFINITY : m_nat, p.ml[at_o * 2 + 1] = l;
+  } else if (put) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int d = 0; d < L::dt; ++d)
+#pragma unroll
+      for (int j4 = 0; j4 < 4; ++j4) {
+        const int e = d * 32 + j4 * 8 + h * 4;
+        const float x[4] = {o[d][j4 * 4] * inv, o[d][j4 * 4 + 1] * inv, o[d][j4 * 4 + 2] * inv, o[d][j4 * 4 + 3] * inv};
+        if (e < D) store4<DT>(a.out, row * D + e, x);
+      }
+    if (a.lse && h == 0) a.lse[row] = l == 0.f ? -INFINITY : m_nat + (logf(l) - shift * kLn2);
+  }
+  // A hidden key's probability is 0, but 0 times an infinity or NaN of its value is NaN. Rows whose
+  // sums stopped being finite in steps that hide keys are done again, key by key.
+  bool again = put && l - l == 0.f && !all_finite<L::dt>(o);
+  if (broken_before && __any(again)) again = again && newly<L::dt>(not_finite<L::dt>(o), broken[threadIdx.x]);
+  uint64_t todo = __ballot(again);
+  todo = (todo | todo >> 32) & 0xFFFFFFFFu;
+  constexpr int EPL = (DC + 63) / 64;
+  while (todo) {
+    const int i = __builtin_ctzll(todo);
+    todo &= todo - 1;
+    const int64_t t2 = __shfl(t, i, 64), h2 = __shfl(qh, i, 64), row2 = t2 * a.Hq + h2;
+    const int64_t end = min((int64_t)__shfl(limit, i, 64), (int64_t)t1 * kStep);
+    float m2, l2, o2[EPL];
+    row_sums<DT, EPL>(a, b, t2, h2, (int64_t)t0 * kStep, end, m2, l2, o2);
+    if (!cut) {
+      put_row<DT, EPL>(a, row2, m2, l2, o2);
+      continue;
+    }
+    const int64_t at2 = (int64_t)part * a.T * a.Hq + row2;
+    const float f = 1 << (int)shift;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e)
+      if (lane + 64 * e < D) p.o[at2 * D + lane + 64 * e] = o2[e] * f;
+    if (lane == 0) p.ml[at2 * 2] = m2, p.ml[at2 * 2 + 1] = l2 * f;
+  }
+}
+
+// Joins the partial results of rows whose keys were cut, a row a wave.
+template <int DT, int DC>
+__global__ __launch_bounds__(kWaves * 64) void prompt_join_kernel(PromptArgs a, PromptPlan p) {
+  constexpr int EPL = (DC + 63) / 64, rows = Tile<DT, DC>::rows, kStep = Tile<DT, DC>::step;
+  const int64_t r = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int64_t t = r / a.Hq, b = t < a.T ? request_of(a, t) : -1;
+  if (b < 0) return;
+  const int lane = threadIdx.x & 63, D = (int)a.cache.dim;
+  // steps of the row's tile, by its last row
+  const int64_t n = (a.cu[b + 1] - a.cu[b]) * (int64_t)p.G;
+  const int64_t own = (t - a.cu[b]) * p.G + (r - t * a.Hq) % p.G;
+  const int64_t last = min((own / rows + 1) * rows, n) - 1;
+  const int64_t steps = (seen_by(a, b, a.cu[b] + last / p.G) + kStep - 1) / kStep;
+  if (steps <= p.chunk) return;
+  const int parts = (int)min((int64_t)p.parts, (steps + p.chunk - 1) / p.chunk);
+  const int64_t every = a.T * a.Hq;
+  float m = -INFINITY, l = 0.f, o[EPL];
+  for (int i = 0; i < parts; ++i) m = fmaxf(m, p.ml[(i * every + r) * 2]);
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    const float2 ml = *(const float2*)(p.ml + (i * every + r) * 2);
+    const float f = join_factor(ml.x, ml.y, m);
+    l = fmaf(f, ml.y, l);
+#pragma unroll
+    for (int e = 0; e < EPL; ++e)
+      if (lane + 64 * e < D) o[e] = fmaf(f, p.o[(i * every + r) * D + lane + 64 * e], o[e]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < EPL; ++e)
+    if (lane + 64 * e < D)
+      Val<DT>::put((typename Val<DT>::type*)a.out + r * D + lane + 64 * e, o[e] * inv);
+  if (a.lse && lane == 0) a.lse[r] = l == 0.f ? -INFINITY : m + (logf(l) - prob_shift<DT> * kLn2);
+}
+
+// Parts that a row's keys may be cut into: two rounds of blocks over the chip at most.
+int64_t most_parts(int64_t T, int64_t G, int64_t heads, int64_t rows) {
+  const int64_t units = (T * G + rows - 1) / rows * heads;
+  const int64_t n = 2 * kMaxCus / (units < 1 ? 1 : units);
+  return n < 1 ? 1 : (n > 64 ? 64 : n);
+}
+
+// Parts of a call: the number with the shortest estimate, in steps of one block. A block spends
+// about 4 steps' time before and after its steps, and 4 more on a partial result.
+int parts_of_call(int64_t units, int64_t cus, int64_t longest, double mean, int64_t most) {
+  int best = 1;
+  double least = 1e300;
+  for (int64_t n = 1; n <= most && (n == 1 || longest / n >= 8); ++n) {
+    const double fixed = n > 1 ? 8 : 4, one = (double)((longest + n - 1) / n) + fixed;
+    double time = one;
+    if (units * n > cus) {
+      const double all = (double)units * (mean + n * fixed) / cus;
+      time = (all > one ? all : one) + 0.5 * one;
+    }
+    if (time < least) least = time, best = (int)n;
+  }
+  return best;
+}
+
+template <int DT, int DC> hipError_t run_mfma(const PromptArgs& a, void* ws, hipStream_t s) {
+  PromptPlan p{};
+  p.heads = (int)a.cache.heads;
+  p.G = (int)(a.Hq / a.cache.heads);
+  constexpr int rows = Tile<DT, DC>::rows, kStep = Tile<DT, DC>::step;
+  const int64_t full = (a.T * p.G + rows - 1) / rows;      // at least so many tiles
+  const int64_t tiles = full + a.B - 1;                    // and at most so many
+  const int64_t most = longest(a), longest_steps = (most + kStep - 1) / kStep;
+  // mean keys of a row: all but half the tokens, as far as is known here
+  const double mean = most <= 0 ? 0. : (most - 0.5 * (double)(a.T / a.B < most ? a.T / a.B : most)) / kStep;
+  p.parts = parts_of_call((full > a.B ? full : a.B) * p.heads, device_cus(), longest_steps, mean,
+                          most_parts(a.T, p.G, p.heads, rows));
+  p.chunk = p.parts == 1 ? 0x7FFFFFFF / kStep : (int)((longest_steps + p.parts - 1) / p.parts);
+  p.o = (float*)ws;
+  p.ml = p.o + (int64_t)p.parts * a.T * a.Hq * a.cache.dim;
+  p.page = fast_div((uint32_t)a.cache.page);
+  p.by_heads = fast_div((uint32_t)p.heads);
+  p.by_parts = fast_div((uint32_t)p.parts);
+  p.by_G = fast_div((uint32_t)p.G);
+  const int64_t blocks = tiles * p.heads * p.parts;
+  if (blocks > 0x7FFFFF || a.T * p.G > 0x7FFFFFFF - 512) return hipErrorInvalidConfiguration;
+  auto kernel = prompt_mfma_kernel<DT, DC, true>;
+  if constexpr (DT != FK_F32)
+    if (a.softcap == 0.f && !a.cache.key_bias && a.scale > 0.f) kernel = prompt_mfma_kernel<DT, DC, false>;
+  kernel<<<(unsigned)blocks, Tile<DT, DC>::waves * 64, 0, s>>>(a, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.parts == 1) return e;
+  prompt_join_kernel<DT, DC><<<(unsigned)((a.T * a.Hq + kWaves - 1) / kWaves), kWaves * 64, 0, s>>>(a, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace fk
