@@ -111,15 +111,19 @@ __device__ __forceinline__ void put_row(const PromptArgs& a, int64_t row, float 
 // steps at once as make up 64, and table entries and biases are asked for two such groups ahead.
 typedef const __attribute__((address_space(1))) uint32_t* gptr32;
 typedef __attribute__((address_space(3))) uint32_t* lptr32;
+typedef __attribute__((address_space(3))) char* lptr8;
+typedef const __attribute__((address_space(3))) char* lptr8c;
+typedef const __attribute__((address_space(3))) u32x4* lptr16c;
+typedef const __attribute__((address_space(3))) uint32_t* lptr32c;
 
 // Waves of a block: 8 share the keys of a step; wide rows need the registers of 4.
-constexpr int tile_waves(int DC) { return DC > 128 ? 4 : 8; }
+constexpr int tile_waves(int dt, int DC) { return DC > (dt == FK_F32 ? 64 : 128) ? 4 : 8; }
 
 template <int DT, int DC> struct Tile {
   static constexpr int eb = Val<DT>::bytes;
   static constexpr int pitch = DC <= 64 ? 64 : (DC <= 128 ? 128 : 256);    // elements of a row in LDS
   static constexpr int rb = pitch * eb;                   // and bytes
-  static constexpr int waves = tile_waves(DC);
+  static constexpr int waves = tile_waves(DT, DC);
   static constexpr int rows = waves * 32;
   static constexpr int step = rb > 512 ? 32 : 64;         // keys a step: two buffers fit the LDS
   static constexpr int key_tiles = step / 32;
@@ -160,7 +164,7 @@ __device__ __forceinline__ float sum_halves(float x) {
 }
 
 // Four keys of one element each, 16 lanes a 4 x 16 block that lies in LDS key by key.
-__device__ __forceinline__ uint2 read_transposed(const char* at) {
+__device__ __forceinline__ uint2 read_transposed(lptr8c at) {
   typedef short s4 __attribute__((ext_vector_type(4)));
   typedef __attribute__((address_space(3))) s4* lp;
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)at));
@@ -229,6 +233,18 @@ template <int N> __device__ __forceinline__ bool newly(const NotFinite<N>& now, 
   return r != 0;
 }
 
+// 16 bytes a lane from its address straight to LDS, lane after lane from `to` on (the same in
+// every lane). Written out, as the compiler would let every later read of LDS wait for
+// the bytes, whatever it reads; what waits is s_waitcnt vmcnt(0) before the
+// barrier after which they are read. No register is written, and the address is
+// read when the instruction is issued. m0, which nothing else here uses, takes a wait
+// state before it is read.
+__device__ __forceinline__ void load_to_lds(uint64_t from, lptr8 to) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :: "s"(at), "v"(from) : "memory");
+}
+
 struct PromptPlan {
   int heads, G, parts, chunk;     // cache heads, query heads of each, parts of a row's keys, steps of a part
   FastDiv page, by_heads, by_parts, by_G;
@@ -237,12 +253,12 @@ struct PromptPlan {
 };
 
 template <int DT, int DC, bool EXTRA>
-__global__ __launch_bounds__(tile_waves(DC) * 64, tile_waves(DC) / 4)
+__global__ __launch_bounds__(tile_waves(DT, DC) * 64, tile_waves(DT, DC) / 4)
 void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   using L = Tile<DT, DC>;
   constexpr int W = L::waves, rb = L::rb, eb = L::eb, kStep = L::step, KT = L::key_tiles, GS = L::group;
   __shared__ __attribute__((aligned(1024))) char lk[2][kStep * rb], lv[2][kStep * rb];
-  __shared__ uint64_t row_k[W][64], row_v[W][64];
+  __shared__ uint64_t row_k[W][64], row_v[2][W][64];   // (values are asked for two steps after their keys)
   __shared__ uint64_t valid[2][GS];                    // keys of a step that count, a bit each
   __shared__ float biases[EXTRA ? 2 : 1][EXTRA ? GS : 1][kStep];
   __shared__ NotFinite<L::dt> broken[W * 64];          // sums that were not finite before hidden keys came
@@ -322,7 +338,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
     const uint64_t va = vbase + (uint64_t)(pg * c.v_stride[0] + tk * c.v_stride[1]) * eb;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     row_k[w][lane] = live ? ka : zero;
-    row_v[w][lane] = live ? va : zero;
+    row_v[group & 1][w][lane] = live ? va : zero;
     const uint64_t ok = __ballot(live);
     if (lane < GS) {
       char* to = (char*)&valid[group & 1][lane];
@@ -333,20 +349,22 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
   const int unit = lane % L::units, sub = lane / L::units;
-  const auto load_step = [&](int s, int buf) {         // keys and values of step s of its group
+  // Rows of step st to LDS. (Units past DC are never read.)
+  const auto load_rows = [&](int st, const uint64_t* rows, auto swizzle, lptr8 to) {
+    const int s = (st - t0) % GS;
+    uint64_t ad[L::loads];
+#pragma unroll
+    for (int i = 0; i < L::loads; ++i) ad[i] = rows[s * share + i * L::per_load + sub];
 #pragma unroll
     for (int i = 0; i < L::loads; ++i) {
-      const int j = i * L::per_load + sub;             // row of this wave's share
-      const int row = w * share + j;
-      const uint64_t ka = row_k[w][s * share + j], va = row_v[w][s * share + j];
-      const int ku = unit ^ key_swizzle<L>(row), vu = unit ^ value_swizzle<L>(row);
-      const int dst = (w * share + i * L::per_load) * rb;
-      // (units past DC are never read)
-      if (DC == L::pitch || ku * L::unit < DC)
-        __builtin_amdgcn_global_load_lds((gptr32)((ku * L::unit < D ? ka : zero) + ku * 16), (lptr32)(lk[buf] + dst), 16, 0, 0);
-      if (DC == L::pitch || vu * L::unit < DC)
-        __builtin_amdgcn_global_load_lds((gptr32)((vu * L::unit < D ? va : zero) + vu * 16), (lptr32)(lv[buf] + dst), 16, 0, 0);
+      const int u = unit ^ swizzle(w * share + i * L::per_load + sub);
+      if (DC == L::pitch || u * L::unit < DC)
+        load_to_lds((u * L::unit < D ? ad[i] : zero) + u * 16, to + (w * share + i * L::per_load) * rb);
     }
+  };
+  const auto load_k = [&](int st, lptr8 to) { load_rows(st, row_k[w], key_swizzle<L>, to); };
+  const auto load_v = [&](int st, lptr8 to) {
+    load_rows(st, row_v[((st - t0) / GS) & 1][w], value_swizzle<L>, to);
   };
 
   floatx16_t o[L::dt];
@@ -360,174 +378,270 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   const float cap = a.softcap, inv_cap = cap > 0.f ? 1.f / cap : 0.f;
   constexpr float shift = prob_shift<DT>, slack = prob_slack<DT>;
 
-  int32_t pg1 = -1, pg2 = -1;
-  float bias1 = -INFINITY;
-  if (t0 < t1) {
-    const int32_t pg0 = entry(0);
-    pg1 = entry(1), pg2 = entry(2);
-    put_rows(0, pg0, bias_of(0, pg0));
-    bias1 = bias_of(1, pg1);
-    load_step(0, 0);
-  }
+  // One step of the pipeline: the products of step st - 1's probabilities with its values and the
+  // scores of step st + 1 keep the matrix units busy while the vector units make step st's
+  // probabilities of its scores. A wave issues both in turn: after each product some of
+  // the work on probabilities, which the product takes longer than; what the products read from LDS is
+  // asked for two of them ahead. Loads for later steps go to the other buffers; the
+  // pointers are restricted so that reads do not wait for them. masked: some key of the
+  // step is hidden from some row.
+  uint4 pr[DT == FK_F32 ? 1 : KT][2];                  // probabilities, 16 bits
+  float pf[DT == FK_F32 ? KT : 1][16];                 // and fp32
+  float grown = 1.f;                                   // what the sums have to be scaled by, and
+  bool grew = false;                                   // whether any have
+
+  constexpr int PV = DT == FK_F32 ? KT * 16 * L::dt : KT * 2 * L::dt, QK = KT * L::kt;
+  const int l16 = lane & 15;
+  // Lane's place in the rows of keys and values; other units lie at the place with bits flipped
+  // (a row's length is a multiple of what is flipped).
+  uint32_t key_place = n * rb + (h ^ key_swizzle<L>(n)) * 16;
+  uint32_t value_place = DT == FK_F32
+      ? 4 * h * rb + ((n >> 2) ^ value_swizzle<L>(4 * h)) * 16 + (n & 3) * 4
+      : (4 * h + (l16 >> 2)) * rb + ((((lane >> 4) & 1) * 2 + ((l16 & 3) >> 1)) ^ value_swizzle<L>(l16 >> 2)) * 16 + (l16 & 1) * 8;
+  const auto value_at = [&](lptr8c v_in, uint32_t place, int i) -> uint4 {        // of product i, tiles d within keys
+    const int d = i % L::dt, ks = i / L::dt;
+    if constexpr (DT == FK_F32) {
+      const int row = (ks >> 4) * 32 + (ks & 3) + 8 * ((ks & 15) >> 2);
+      return make_uint4(*(lptr32c)(v_in + row * rb + (place ^ (d * 128))), 0, 0, 0);
+    } else {
+      lptr8c at_v = v_in + ks * 16 * rb + (place ^ (d * 64));
+      const uint2 lo = read_transposed(at_v), hi = read_transposed(at_v + 8 * rb);
+      return make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+  };
+  const auto add_value = [&](const uint4& x, int i) {
+    const int d = i % L::dt, ks = i / L::dt;
+    if constexpr (DT == FK_F32)
+      o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(float, x.x), pf[ks >> 4][ks & 15], o[d], 0, 0, 0);
+    else
+      o[d] = Mfma<DT>::run(x, pr[ks >> 1][ks & 1], o[d]);
+  };
+  const auto key_at = [&](lptr8c k_in, uint32_t place, int i) -> uint4 {          // of product i, halves of the keys in turn
+    const int u = i % KT, k = i / KT;
+    const u32x4 y = *(lptr16c)(k_in + u * 32 * rb + (place ^ (k * 32)));
+    return __builtin_bit_cast(uint4, y);
+  };
+  const auto clear = [](floatx16_t (&x)[KT]) {
+#pragma unroll
+    for (int u = 0; u < KT; ++u)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[u][j] = 0.f;
+  };
+  const auto advance = [&](int st, auto tag, floatx16_t (&s)[KT], floatx16_t (&next)[KT],
+                           const lptr8c __restrict k_in, const lptr8c __restrict v_in,
+                           const lptr8 __restrict k_out, const lptr8 __restrict v_out) {
+    constexpr bool masked = decltype(tag)::value;
+    const int i = st - t0, key0 = st * kStep;
+    if (st + 2 < t1) load_k(st + 2, k_out);
+    load_v(st, v_out);
+    if (grew) {
+#pragma unroll
+      for (int d = 0; d < L::dt; ++d)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[d][j] *= grown;
+    }
+    clear(next);
+    // (as new numbers every step, so that the flipped places are not kept in registers)
+    asm volatile("" : "+v"(key_place), "+v"(value_place));
+    uint64_t ok = 0;
+    if constexpr (masked && !EXTRA) ok = valid[(i / GS) & 1][i % GS];
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, ref = 0.f, off = 0.f, f = 1.f;
+    bool grows = false;
+    uint32_t made[KT][8];
+    // the work on probabilities in pieces: scores four by four, the maximum, pairs
+    constexpr int prep = KT * 4, pieces = prep + 1 + KT * 8;
+    const auto piece = [&](int at) {
+      if (at < prep) {
+        const int u = at / 4, j4 = at % 4;
+        float bb[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (EXTRA) {
+          const float4 bs = *(const float4*)&biases[(i / GS) & 1][i % GS][u * 32 + j4 * 8 + h * 4];
+          bb[0] = bs.x, bb[1] = bs.y, bb[2] = bs.z, bb[3] = bs.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x = s[u][j4 * 4 + j];
+          if constexpr (EXTRA) {
+            x *= a.scale;
+            if (cap > 0.f) x = capped(x, cap, inv_cap);
+            x = bb[j] == -INFINITY ? -INFINITY : x + bb[j];
+          }
+          if constexpr (masked) {
+            const int key = u * 32 + j4 * 8 + h * 4 + j;
+            x = key0 + key < limit && (EXTRA || ((ok >> key) & 1)) ? x : -INFINITY;
+          }
+          s[u][j4 * 4 + j] = x;
+          top[j & 1] = fmaxf(top[j & 1], x);
+        }
+      } else if (at == prep) {
+        const float t = max_halves(fmaxf(top[0], top[1]));
+        grows = (t - m) * unit_log2 > slack;
+        const float mn = grows ? fmaxf(m, t) : m;
+        f = grows ? fast_exp2((m - mn) * unit_log2) : 1.f;
+        m = mn;
+        ref = m == -INFINITY ? 0.f : m;
+        off = fmaf(-ref, unit_log2, shift);
+      } else {
+        const int pair = at - prep - 1, u = pair / 8, j0 = pair % 8 * 2;
+#pragma unroll
+        for (int j = j0; j < j0 + 2; ++j) {
+          float x;
+          if constexpr (DT == FK_F32) x = prob<DT>(s[u][j] - ref);
+          else if constexpr (EXTRA) x = fast_exp2(fmaf(s[u][j] - ref, kLog2e, shift));
+          else x = fast_exp2(fmaf(s[u][j], unit_log2, off));
+          s[u][j] = x;
+          sum[j & 1] += x;
+        }
+        if constexpr (DT != FK_F32) {
+          typedef typename Val<DT>::arith T;
+          typedef T T2 __attribute__((ext_vector_type(2)));
+          T2 two = {(T)s[u][j0], (T)s[u][j0 + 1]};
+          // an infinite value times a probability that rounds to 0 would be NaN; in steps
+          // that hide no key 2^-24 (2^-37 of the largest one) stands for those
+          if constexpr (DT == FK_F16 && !masked) two = __builtin_elementwise_max(two, (T2)(T)0x1p-24f);
+          uint32_t word = __builtin_bit_cast(uint32_t, two);
+          asm volatile("" : "+v"(word));               // made here, not where it is used
+          made[u][pair % 8] = word;
+        }
+      }
+    };
+    if constexpr (DT == FK_F32) {                      // (products that take 2 or 8 times as long: in turn)
+#pragma unroll
+      for (int ks = 0; ks < KT * 16; ++ks)
+#pragma unroll
+        for (int d = 0; d < L::dt; ++d) add_value(value_at(v_in, value_place, ks * L::dt + d), ks * L::dt + d);
+#pragma unroll
+      for (int at = 0; at < QK; ++at)
+        next[at % KT] = Mfma<DT>::run(key_at(k_in, key_place, at), q[at / KT], next[at % KT]);
+#pragma unroll
+      for (int w2 = 0; w2 < pieces; ++w2) piece(w2);
+    } else {
+      constexpr int products = PV + QK, ahead = 2;
+      uint4 in[ahead + 1];
+      const auto input = [&](int at) {
+        return at < PV ? value_at(v_in, value_place, at) : key_at(k_in, key_place, at - PV);
+      };
+#pragma unroll
+      for (int at = 0; at < ahead; ++at) in[at] = input(at);
+#pragma unroll
+      for (int at = 0; at < products; ++at) {
+        if (at + ahead < products) in[(at + ahead) % (ahead + 1)] = input(at + ahead);
+        const uint4 x = in[at % (ahead + 1)];
+        if (at < PV) add_value(x, at);
+        else next[(at - PV) % KT] = Mfma<DT>::run(x, q[(at - PV) / KT], next[(at - PV) % KT]);
+#pragma unroll
+        for (int w2 = at * pieces / products; w2 < (at + 1) * pieces / products; ++w2) piece(w2);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    l = fmaf(l, f, sum[0] + sum[1]);
+    grown = f, grew = __any(grows);
+#pragma unroll
+    for (int u = 0; u < KT; ++u) {
+      if constexpr (DT == FK_F32) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) pf[u][j] = s[u][j];
+      } else {
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb)
+          pr[u][sb] = make_uint4(made[u][sb * 4], made[u][sb * 4 + 1], made[u][sb * 4 + 2], made[u][sb * 4 + 3]);
+      }
+    }
+  };
   const auto all_valid = [&](int st) {                 // every key of step st counts
     const int i = st - t0;
     const uint64_t ok = valid[(i / GS) & 1][i % GS];
     const uint32_t both = kStep == 32 ? (uint32_t)ok : (uint32_t)(ok & (ok >> 32));
     return __builtin_amdgcn_readfirstlane(both) == 0xFFFFFFFFu;
   };
-  // One step: scores, probabilities, sums. masked: some key of it is hidden from some row.
-  const auto compute = [&](int st, auto tag) {
-    constexpr bool masked = decltype(tag)::value;
-    const int i = st - t0, buf = i & 1, key0 = st * kStep;
-    // scores
-    floatx16_t s[KT];
+
+  floatx16_t sa[KT], sb[KT];                           // scores of a step and of the next, in turn
+  int32_t pg1 = -1, pg2 = -1;
+  float bias1 = -INFINITY;
+  const auto find_rows = [&](int st) {                 // before the keys of step st are asked for
+    const int i = st - t0;
+    if (i % GS != 0 || st >= t1) return;
+    put_rows(i / GS, pg1, bias1);
+    pg1 = pg2;
+    bias1 = bias_of(i / GS + 1, pg1);
+    pg2 = entry(i / GS + 2);
+  };
+  const auto meet = [&] {                              // rows asked for are in, earlier steps are done with
+    __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0)
+    __syncthreads();
+  };
+  const int own_end = min(t1, (int)(((uint32_t)high + kStep - 1) / kStep));     // steps of this wave
+  if (t0 < t1) {
+    pg1 = entry(0), pg2 = entry(1);
+    bias1 = bias_of(0, pg1);
+    find_rows(t0);
+    load_k(t0, (lptr8)lk[0]);
+    if (t0 + 1 < t1) {
+      find_rows(t0 + 1);
+      load_k(t0 + 1, (lptr8)lk[1]);
+    }
+    // the pipeline starts with no values and no probabilities
+    for (int i = threadIdx.x; i < kStep * rb / 16; i += W * 64) ((uint4*)lv[1])[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int u = 0; u < KT; ++u) {
+      if constexpr (DT != FK_F32) pr[u][0] = pr[u][1] = make_uint4(0, 0, 0, 0);
+      else
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s[u][j] = 0.f;
-      const char* base = lk[buf] + (u * 32 + n) * rb;
-#pragma unroll
-      for (int k = 0; k < L::kt; ++k) {
-        const uint4 x = *(const uint4*)(base + ((2 * k + h) ^ key_swizzle<L>(n)) * 16);
-        s[u] = Mfma<DT>::run(x, q[k], s[u]);
-      }
+        for (int j = 0; j < 16; ++j) pf[u][j] = 0.f;
     }
-    if constexpr (EXTRA) {
+    meet();
+    clear(sa);
 #pragma unroll
-      for (int u = 0; u < KT; ++u)
-#pragma unroll
-        for (int j4 = 0; j4 < 4; ++j4) {
-          const float4 bs = *(const float4*)&biases[(i / GS) & 1][i % GS][u * 32 + j4 * 8 + h * 4];
-          const float bb[4] = {bs.x, bs.y, bs.z, bs.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float x = s[u][j4 * 4 + j] * a.scale;
-            if (cap > 0.f) x = capped(x, cap, inv_cap);
-            s[u][j4 * 4 + j] = bb[j] == -INFINITY ? -INFINITY : x + bb[j];
-          }
-        }
-    }
-    if constexpr (masked) {
-      const uint64_t ok = valid[(i / GS) & 1][i % GS];
-#pragma unroll
-      for (int u = 0; u < KT; ++u)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int key = u * 32 + (j & 3) + 8 * (j >> 2) + 4 * h;
-          const bool live = key0 + key < limit && (EXTRA || ((ok >> key) & 1));
-          s[u][j] = live ? s[u][j] : -INFINITY;
-        }
-    }
-    float top = s[0][0];
-#pragma unroll
-    for (int u = 0; u < KT; ++u)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) top = fmaxf(top, s[u][j]);
-    top = max_halves(top);
-    if (__any((top - m) * unit_log2 > slack)) {
-      const float mn = fmaxf(m, top);
-      const float f = m == -INFINITY ? 0.f : fast_exp2((m - mn) * unit_log2);
-      m = mn;
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < L::dt; ++d)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[d][j] *= f;
-    }
-    const float ref = m == -INFINITY ? 0.f : m;
-    const float off = fmaf(-ref, unit_log2, shift);
-    float sum = 0.f;
-#pragma unroll
-    for (int u = 0; u < KT; ++u)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float x;
-        if constexpr (DT == FK_F32) x = prob<DT>(s[u][j] - ref);
-        else if constexpr (EXTRA) x = fast_exp2(fmaf(s[u][j] - ref, kLog2e, shift));
-        else x = fast_exp2(fmaf(s[u][j], unit_log2, off));
-        s[u][j] = x;
-        sum += x;
-      }
-    l += sum;
-    // values
-    if constexpr (DT == FK_F32) {
-#pragma unroll
-      for (int u = 0; u < KT; ++u)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int vr = u * 32 + (j & 3) + 8 * (j >> 2) + 4 * h;
-#pragma unroll
-          for (int d = 0; d < L::dt; ++d) {
-            const int un = (d * 8 + (n >> 2)) ^ value_swizzle<L>(4 * h);
-            const float x = *(const float*)(lv[buf] + vr * rb + un * 16 + (n & 3) * 4);
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, s[u][j], o[d], 0, 0, 0);
-          }
-        }
-    } else {
-#pragma unroll
-      for (int u = 0; u < KT; ++u)
-#pragma unroll
-        for (int sb = 0; sb < 2; ++sb) {
-          typedef typename Val<DT>::arith T;
-          typedef T T8 __attribute__((ext_vector_type(8)));
-          T8 pt;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) pt[j] = (T)s[u][sb * 8 + j];
-          // an infinite value times a probability that rounds to 0 would be NaN; in steps
-          // that hide no key 2^-24 (2^-37 of the largest one) stands for those
-          if constexpr (DT == FK_F16)
-            if (!masked) pt = __builtin_elementwise_max(pt, (T8)(T)0x1p-24f);
-          const uint4 pr = __builtin_bit_cast(uint4, pt);
-          const int l16 = lane & 15, vr = u * 32 + sb * 16 + 4 * h + (l16 >> 2);
-#pragma unroll
-          for (int d = 0; d < L::dt; ++d) {
-            const int un = (d * 4 + ((lane >> 4) & 1) * 2 + ((l16 & 3) >> 1)) ^ value_swizzle<L>(l16 >> 2);
-            const char* at_v = lv[buf] + vr * rb + un * 16 + (l16 & 1) * 8;
-            const uint2 lo = read_transposed(at_v), hi = read_transposed(at_v + 8 * rb);
-            o[d] = Mfma<DT>::run(make_uint4(lo.x, lo.y, hi.x, hi.y), pr, o[d]);
-          }
-        }
-    }
-  };
-  // Waits for the rows of step st and asks for the next one's.
-  const auto arrive = [&](int st) {
-    const int i = st - t0, buf = i & 1;
-    __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0): this wave's rows are in
-    __syncthreads();                                   // and everyone's; the last step's are done with
-    if (st + 1 < t1) {
-      const int next = i + 1;
-      if (next % GS == 0) {
-        put_rows(next / GS, pg1, bias1);
-        pg1 = pg2;
-        bias1 = bias_of(next / GS + 1, pg1);
-        pg2 = entry(next / GS + 2);
-      }
-      load_step(next % GS, buf ^ 1);
-    }
-  };
+    for (int at = 0; at < QK; ++at)
+      sa[at % KT] = Mfma<DT>::run(key_at((lptr8c)lk[0], key_place, at), q[at / KT], sa[at % KT]);
+  }
   // Steps that every row sees whole, then the others: every wave changes over in its own time
   // (a barrier counts waves, wherever they stand). fp32 products take longer than the
   // masks.
   int st = t0;
+  bool here = false;                                   // step st has met already
   if constexpr (DT != FK_F32) {
-    for (; st < t1 && (st + 1) * kStep <= low; ++st) {
-      arrive(st);
-      if (!EXTRA && !all_valid(st)) break;
-      compute(st, std::false_type());
+    const int whole = min(t1, low / kStep);
+    for (; st + 2 <= whole; st += 2) {                 // two at a time, so that scores and buffers change places
+      meet();
+      if (!EXTRA && !(all_valid(st) && all_valid(st + 1))) {
+        here = true;
+        break;
+      }
+      find_rows(st + 2);
+      advance(st, std::false_type(), sa, sb, (lptr8c)lk[1], (lptr8c)lv[1], (lptr8)lk[0], (lptr8)lv[0]);
+      meet();
+      find_rows(st + 3);
+      advance(st + 1, std::false_type(), sb, sa, (lptr8c)lk[0], (lptr8c)lv[0], (lptr8)lk[1], (lptr8)lv[1]);
     }
   }
-  // (a step that was found to have keys missing has arrived)
-  bool here = !EXTRA && DT != FK_F32 && st < t1 && (st + 1) * kStep <= low;
-  for (; st < t1; ++st, here = false) {
-    if (!here) arrive(st);
-    const int key0 = st * kStep;
-    if (key0 >= high) continue;
-    if (!looked && key0 + kStep > low) {
+  for (; st < own_end; ++st, here = false) {
+    const int buf = (st - t0) & 1;
+    if (!here) meet();
+    find_rows(st + 2);
+    advance(st, std::true_type(), sa, sb, (lptr8c)lk[buf ^ 1], (lptr8c)lv[buf ^ 1], (lptr8)lk[buf], (lptr8)lv[buf]);
+#pragma unroll
+    for (int u = 0; u < KT; ++u) sa[u] = sb[u];
+    if (!looked && (st + 1) * kStep > low) {           // (its hidden values have not been added yet)
       looked = true;
       broken_before = __any(!all_finite<L::dt>(o));
       if (broken_before) broken[threadIdx.x] = not_finite<L::dt>(o);
     }
-    compute(st, std::true_type());
+  }
+  for (; st <= t1 && t0 < t1; ++st, here = false) {    // the last values, and the other waves' steps
+    const int buf = (st - t0) & 1;
+    if (!here) meet();
+    if (st == own_end) {
+#pragma unroll
+      for (int d = 0; d < L::dt; ++d)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[d][j] *= grown;
+#pragma unroll
+      for (int at = 0; at < PV; ++at) add_value(value_at((lptr8c)lv[buf ^ 1], value_place, at), at);
+    }
+    find_rows(st + 2);
+    if (st + 2 < t1) load_k(st + 2, (lptr8)lk[buf]);
+    if (st < t1) load_v(st, (lptr8)lv[buf]);
   }
   l = sum_halves(l);
   const int64_t row = t * a.Hq + qh;
