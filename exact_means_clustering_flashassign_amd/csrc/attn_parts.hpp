@@ -319,6 +319,120 @@ constexpr int waves_per_simd(int64_t D) {
 }
 constexpr int kMaxParts = kMaxCus * 4;
 
+// Rows narrower than the tile, rows that fill it, and rows that fill it and whole
+// 128-byte lines that no other wave reads, by streaming loads.
+enum { kNarrow, kWhole, kStream };
+
+// State of one wave over a run of steps.
+template <class S, int HT> struct Acc {
+  float m[HT], l[HT];                  // of lane m's head of each tile; l: this lane's share
+  floatx4_t o[HT][S::nu * S::ve];
+};
+
+// The kernel around an operator Op, which says how a wave attends to a run of steps (Op::attend)
+// and in what shape (Op::S).
+template <class Op, int KIND, int W>
+__global__ __launch_bounds__(W * 64, W == kWaves ? waves_per_simd(Op::DP) : W / 4)
+void attn_mfma_kernel(typename Op::Args a, Plan p) {
+  using S = typename Op::S;
+  constexpr int DT = Op::DT, DP = Op::DP, HT = Op::HT;
+  __shared__ typename Op::Rows rows[W][2];
+  __shared__ float so[W][kHeadTile][S::ldo];
+  __shared__ float sm[W][kHeadTile], sl[W][kHeadTile];
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // Waves k0 .. k1 - 1 of this block are one team; its teams take neighbouring heads.
+  const int k0 = w >> p.team_log << p.team_log, k1 = k0 + p.team, teams = W >> p.team_log;
+  const uint32_t unit =
+      (uint32_t)xcd_remap(blockIdx.x, gridDim.x) * teams + (w >> p.team_log);
+  const uint32_t rest = div_by(unit, p.by_tiles), at_head = div_by(rest, p.by_heads);
+  const int ht = (int)(unit - rest * p.tiles), hk = (int)(rest - at_head * p.heads);
+  const int64_t part = at_head;
+  const int D = KIND == kNarrow ? (int)a.cache.dim : DP;
+
+  Start st;
+  const bool cut = W == kWaves && p.parts > 0;
+  if (cut) {
+    // the same for the block: held in scalar registers through the steps, which
+    // have none to spare among the others
+    st = find_start<S::keys>(a, p, (int)part);
+    st.lo = uniform(st.lo), st.hi = uniform(st.hi);
+    st.b = uniform(st.b), st.before = uniform(st.before);
+    if (st.lo >= st.hi) return;
+  } else {
+    st.lo = 0, st.hi = 1, st.b = part, st.before = 0;
+  }
+  const bool idle = !cut && part >= a.B;     // a wave past the last request
+  for (int64_t b = st.b, at = st.before; at < st.hi;) {
+    const int len = idle ? 0 : __builtin_amdgcn_readfirstlane(len_of(a, b));
+    const int steps = steps_of<S::keys>(len);
+    int t0 = 0, t1 = steps;
+    if (cut) {
+      const int64_t first = at + p.team;
+      t0 = (int)max((int64_t)0, min(st.lo - first, (int64_t)steps));
+      t1 = (int)max((int64_t)0, min(st.hi - first, (int64_t)steps));
+    }
+    const bool starts = at >= st.lo;           // the request begins in this part
+    if (t0 < t1 || (steps == 0 && starts)) {
+      Acc<S, HT> acc;
+      Op::template attend<KIND>(a, p, b, hk, ht, len, t0 + w - k0, p.team, t1, rows[w], acc);
+      const bool whole = t0 == 0 && t1 == steps;
+      const int slot = t0 == 0 ? 1 : 0;
+      const int64_t ps = (((part * p.heads + hk) * p.tiles + ht) * 2 + slot) * p.hr;
+#pragma unroll
+      for (int h2 = 0; h2 < HT; ++h2) {
+        const int h0 = (ht * HT + h2) * kHeadTile;        // first head of this tile
+        const int nh = min(kHeadTile, p.G - h0);
+        __syncthreads();                       // the last results are out
+        if (m < nh) {
+          if (g == 0) sm[w][m] = acc.m[h2], sl[w][m] = acc.l[h2];
+#pragma unroll
+          for (int u = 0; u < S::nu; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int t = 0; t < S::ve; ++t)
+                so[w][m][u * 16 * S::ve + S::ve * (4 * g + i) + t] = acc.o[h2][u * S::ve + t][i];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x - k0 * 64; i < nh * (DP / 4) && !idle; i += p.team * 64) {
+          const int h = i / (DP / 4), e = (i - h * (DP / 4)) * 4;
+          float top = -INFINITY;
+          for (int k = k0; k < k1; ++k) top = fmaxf(top, sm[k][h]);
+          float x[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+          for (int k = k0; k < k1; ++k) {
+            const float f = join_factor(sm[k][h], sl[k][h], top);
+            l = fmaf(f, sl[k][h], l);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = fmaf(f, so[k][h][e + j], x[j]);
+          }
+          if (e >= D) continue;
+          if (whole) {
+            const int64_t row = b * a.Hq + hk * p.G + h0 + h;
+            const float r = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] *= r;
+            store4<DT>(a.out, row * D + e, x);
+            if (e == 0 && a.lse)
+              a.lse[row] = l == 0.f ? -INFINITY : top + (logf(l) - kProbShift<DT> * kLn2);
+          } else {
+            const int64_t pr = ps + h2 * kHeadTile + h;
+            *(float4*)(p.o + pr * D + e) = make_float4(x[0], x[1], x[2], x[3]);
+            if (e == 0) p.ml[pr * 2] = top, p.ml[pr * 2 + 1] = l;
+          }
+        }
+      }
+      if (cut && hk == 0 && ht == 0 && threadIdx.x == 0) {
+        if (t0 == 0) p.cover[2 * b] = (int32_t)part;
+        if (t1 == steps) p.cover[2 * b + 1] = (int32_t)part;
+      }
+    }
+    if (!cut) break;
+    at += p.team + steps;
+    ++b;
+  }
+}
+
 constexpr int kJoin = 256;        // threads of a joining block
 
 // Joins the partial results of a request that was cut: slot 1 of its first part,
@@ -416,6 +530,87 @@ int64_t chip_blocks(int64_t cus, int64_t D) {
 // Waves a head when requests are cut: the block's waves take as many neighbouring
 // heads as divide them evenly.
 int team_of(int64_t units) { return units % 4 == 0 ? 1 : (units % 2 == 0 ? 2 : 4); }
+
+// How a call is run.
+struct Choice {
+  Plan p;
+  bool cut, eight;      // requests cut into parts; blocks of 8 waves, else of kWaves
+  int W;
+  int64_t most, blocks; // (0 blocks: too many for a launch)
+};
+
+// keys: of a wave's step; HT head tiles a wave; DP: elements of a row's tile.
+inline Choice choose(const AttnArgs& a, int keys, int HT, int DP, void* ws) {
+  Choice c{};
+  Plan& p = c.p;
+  p.heads = (int)a.cache.heads;
+  p.G = (int)(a.Hq / a.cache.heads);
+  p.width = HT * kHeadTile;
+  p.tiles = (p.G + p.width - 1) / p.width;
+  p.hr = p.G < p.width ? p.G : p.width;
+  p.page = fast_div((uint32_t)a.cache.page);
+  const int64_t units = (int64_t)p.heads * p.tiles;
+  const int64_t most = c.most = longest(a);
+  // Cutting costs a second launch and a trip through memory. Up to 512 keys a request is
+  // done faster whole (32 requests of 400 keys: 14.7 us, cut 21.4), unless there are
+  // many, whose lengths may differ: one wave each is best up to 8 steps, and beyond that
+  // cutting evens them out (256 requests up to 512 keys, spread over the logarithm: 35 us
+  // cut, 50 whole; all alike: 91 and 87).
+  const int64_t resident = chip_blocks(device_cus(), DP);
+  const bool many = units * a.B >= 2 * resident;
+  // Where every block has a CU to itself and half the CUs have one, 8 waves do up to 64 steps
+  // whole (6 requests of 607 keys, 32 heads of 64: 12.6 us, cut 20.9; 16 of 1500, 8 heads of
+  // 128: 23 and 27). With fewer blocks a CU's own rate is the bound, and more of them the
+  // remedy (4 of 2000, 8 heads: 26, cut 17).
+  const int64_t cus = device_cus(), rows = units * a.B;
+  const bool eight = c.eight = DP <= 128 && most > 512 && most <= 64 * keys &&
+                     rows <= cus && 2 * rows >= cus;
+  const bool cut = c.cut = !eight && (most > 512 || (many && most > 8 * keys));
+  if (cut) {
+    // Where there are steps enough for every wave of the chip, a block's waves take
+    // neighbouring heads, whose rows lie side by side in the cache, instead of one
+    // head's steps in turn: the block reads 4 rows' length in one piece (the 4.43 GB
+    // above: 774 us with 1 head a block, 697 with 2, 670 with 4). With fewer steps the
+    // waves share them and join in LDS, not through memory.
+    const double steps = (double)units * a.B * ((most + keys - 1) / keys);
+    p.team = steps >= 4.0 * kWaves * resident ? team_of(units) : kWaves;
+    const int64_t groups = units * p.team / kWaves;       // blocks that make one part
+    p.parts = (int)parts_of(resident, groups);
+    const int64_t slots = units * p.parts * 2 * p.hr;
+    char* w = (char*)ws;
+    p.o = (float*)w;
+    p.ml = (float*)(w + slots * a.cache.dim * 4);
+    p.cover = (int32_t*)(w + slots * a.cache.dim * 4 + slots * 8);
+  } else {
+    // One wave each where that alone fills the chip, or where a second wave would
+    // find nothing to do (222 requests of 3 keys, 32 heads: 19 us, 40 with four waves).
+    p.team = eight ? 8 : (many || most <= keys ? 1 : kWaves);
+  }
+  const int W = c.W = eight ? 8 : kWaves;
+  p.team_log = p.team == 8 ? 3 : (p.team == 4 ? 2 : p.team - 1);
+  p.by_tiles = fast_div((uint32_t)p.tiles);
+  p.by_heads = fast_div((uint32_t)p.heads);
+  if (units * a.B + W <= 0x7FFFFFFF && a.B * a.Hq <= 0x7FFFFFFF - 4)
+    c.blocks = (units * (cut ? p.parts : a.B) * p.team + W - 1) / W;
+  return c;
+}
+
+// Joins what a call cut.
+template <int DT> hipError_t join_parts(const AttnArgs& a, const Plan& p, hipStream_t s) {
+  const int64_t cus = device_cus();
+  // Many rows: most were not cut or have few parts, and a wave is enough for one.
+  const int64_t outs = a.B * a.Hq;
+  if (outs >= 8 * cus) {
+    attn_join_kernel<DT, 4><<<(unsigned)((outs + 3) / 4), kJoin, 0, s>>>(a, p, 1);
+    return hipGetLastError();
+  }
+  // Few rows have many parts: as many blocks a row as there are CUs for, down to 64 bytes
+  // of a partial result (one request of 131072 keys, 32 query heads: 95.9 -> 94.5 us).
+  int slices = 1;
+  while (2 * slices * outs <= cus && a.cache.dim / (2 * slices) >= 16) slices *= 2;
+  attn_join_kernel<DT, 1><<<(unsigned)(outs * slices), kJoin, 0, s>>>(a, p, slices);
+  return hipGetLastError();
+}
 
 }  // namespace
 }  // namespace fk

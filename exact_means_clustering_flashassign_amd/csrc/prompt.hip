@@ -50,7 +50,7 @@ template <int DT> hipError_t run(const PromptArgs& a, void* ws, hipStream_t s) {
 
 size_t prompt_ws_bytes(int dt, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   if (D > 256) return 0;
-  const int64_t rows = D <= 128 ? Tile<FK_F32, 128>::rows : Tile<FK_F32, 256>::rows;
+  const int64_t rows = tile_waves(dt, (int)D) * 32;
   const int64_t parts = most_parts(T, Hq / Hkv, Hkv, rows);
   return parts == 1 ? 0 : (size_t)(parts * T * Hq) * (D + 2) * 4;
 }

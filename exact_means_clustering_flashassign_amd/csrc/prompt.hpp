@@ -116,8 +116,11 @@ typedef const __attribute__((address_space(3))) char* lptr8c;
 typedef const __attribute__((address_space(3))) u32x4* lptr16c;
 typedef const __attribute__((address_space(3))) uint32_t* lptr32c;
 
-// Waves of a block: 8 share the keys of a step; wide rows need the registers of 4.
-constexpr int tile_waves(int dt, int DC) { return DC > (dt == FK_F32 ? 64 : 128) ? 4 : 8; }
+// Waves of a block: 8 share the keys of a step; wide rows need the registers of 4. fp32 products
+// are an eighth as fast, so that smaller tiles, which more CUs share, cost nothing.
+constexpr int tile_waves(int dt, int DC) { return dt == FK_F32 || DC > 128 ? 4 : 8; }
+// Blocks that a CU holds at once: 64 rows of 64 fp32 elements twice, for keys and for values, are half its LDS.
+constexpr int tile_blocks(int dt, int DC) { return dt == FK_F32 && DC <= 64 ? 2 : 1; }
 
 template <int DT, int DC> struct Tile {
   static constexpr int eb = Val<DT>::bytes;
@@ -253,7 +256,7 @@ struct PromptPlan {
 };
 
 template <int DT, int DC, bool EXTRA>
-__global__ __launch_bounds__(tile_waves(DT, DC) * 64, tile_waves(DT, DC) / 4)
+__global__ __launch_bounds__(tile_waves(DT, DC) * 64, tile_waves(DT, DC) / 4 * tile_blocks(DT, DC))
 void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   using L = Tile<DT, DC>;
   constexpr int W = L::waves, rb = L::rb, eb = L::eb, kStep = L::step, KT = L::key_tiles, GS = L::group;
@@ -740,16 +743,17 @@ int64_t most_parts(int64_t T, int64_t G, int64_t heads, int64_t rows) {
   return n < 1 ? 1 : (n > 64 ? 64 : n);
 }
 
-// Parts of a call: the number with the shortest estimate, in steps of one block. A block spends
-// about 4 steps' time before and after its steps, and 4 more on a partial result.
-int parts_of_call(int64_t units, int64_t cus, int64_t longest, double mean, int64_t most) {
+// Parts of a call: the number with the shortest estimate, in steps of one block, where `slots`
+// blocks run at once. A block spends `fixed` steps' time before and after its steps, and as
+// much again on a partial result.
+int parts_of_call(int64_t units, int64_t slots, int64_t longest, double mean, int64_t most, double fixed) {
   int best = 1;
   double least = 1e300;
-  for (int64_t n = 1; n <= most && (n == 1 || longest / n >= 8); ++n) {
-    const double fixed = n > 1 ? 8 : 4, one = (double)((longest + n - 1) / n) + fixed;
+  for (int64_t n = 1; n <= most && (n == 1 || longest >= n * 2 * fixed); ++n) {
+    const double over = n > 1 ? 2 * fixed : fixed, one = (double)((longest + n - 1) / n) + over;
     double time = one;
-    if (units * n > cus) {
-      const double all = (double)units * (mean + n * fixed) / cus;
+    if (units * n > slots) {
+      const double all = (double)units * (mean + n * over) / slots;
       time = (all > one ? all : one) + 0.5 * one;
     }
     if (time < least) least = time, best = (int)n;
@@ -767,8 +771,8 @@ template <int DT, int DC> hipError_t run_mfma(const PromptArgs& a, void* ws, hip
   const int64_t most = longest(a), longest_steps = (most + kStep - 1) / kStep;
   // mean keys of a row: all but half the tokens, as far as is known here
   const double mean = most <= 0 ? 0. : (most - 0.5 * (double)(a.T / a.B < most ? a.T / a.B : most)) / kStep;
-  p.parts = parts_of_call((full > a.B ? full : a.B) * p.heads, device_cus(), longest_steps, mean,
-                          most_parts(a.T, p.G, p.heads, rows));
+  p.parts = parts_of_call((full > a.B ? full : a.B) * p.heads, device_cus() * tile_blocks(DT, DC), longest_steps,
+                          mean, most_parts(a.T, p.G, p.heads, rows), DT == FK_F32 ? 0.5 : 4.0);
   p.chunk = p.parts == 1 ? 0x7FFFFFFF / kStep : (int)((longest_steps + p.parts - 1) / p.parts);
   p.o = (float*)ws;
   p.ml = p.o + (int64_t)p.parts * a.T * a.Hq * a.cache.dim;
