@@ -3,6 +3,7 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "attn_parts.hpp"
 
@@ -128,7 +129,7 @@ template <int DT, int DC> struct Tile {
   static constexpr int rb = pitch * eb;                   // and bytes
   static constexpr int waves = tile_waves(DT, DC);
   static constexpr int rows = waves * 32;
-  static constexpr int step = rb > 512 ? 32 : 64;         // keys a step: two buffers fit the LDS
+  static constexpr int step = eb == 4 && DC > 64 ? 32 : 64;      // keys a step: two buffers fit the LDS
   static constexpr int key_tiles = step / 32;
   static constexpr int unit = 16 / eb;                    // elements of 16 bytes
   static constexpr int units = pitch / unit;              // 16-byte units of a row
@@ -246,6 +247,14 @@ __device__ __forceinline__ void load_to_lds(uint64_t from, lptr8 to) {
   const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :: "s"(at), "v"(from) : "memory");
+}
+
+// f(0), ..., f(N - 1), each with its number as a type.
+template <class F, int... I> __device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, const F& f) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, class F> __device__ __forceinline__ void each(const F& f) {
+  each_of(std::make_integer_sequence<int, N>(), f);
 }
 
 struct PromptPlan {
@@ -453,9 +462,10 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
     uint32_t made[KT][8];
     // the work on probabilities in pieces: scores four by four, the maximum, pairs
     constexpr int prep = KT * 4, pieces = prep + 1 + KT * 8;
-    const auto piece = [&](int at) {
-      if (at < prep) {
-        const int u = at / 4, j4 = at % 4;
+    const auto piece = [&](auto number) {
+      constexpr int at = decltype(number)::value;
+      if constexpr (at < prep) {
+        constexpr int u = at / 4, j4 = at % 4;
         float bb[4] = {0.f, 0.f, 0.f, 0.f};
         if constexpr (EXTRA) {
           const float4 bs = *(const float4*)&biases[(i / GS) & 1][i % GS][u * 32 + j4 * 8 + h * 4];
@@ -476,7 +486,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
           s[u][j4 * 4 + j] = x;
           top[j & 1] = fmaxf(top[j & 1], x);
         }
-      } else if (at == prep) {
+      } else if constexpr (at == prep) {
         const float t = max_halves(fmaxf(top[0], top[1]));
         grows = (t - m) * unit_log2 > slack;
         const float mn = grows ? fmaxf(m, t) : m;
@@ -485,7 +495,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
         ref = m == -INFINITY ? 0.f : m;
         off = fmaf(-ref, unit_log2, shift);
       } else {
-        const int pair = at - prep - 1, u = pair / 8, j0 = pair % 8 * 2;
+        constexpr int pair = at - prep - 1, u = pair / 8, j0 = pair % 8 * 2;
 #pragma unroll
         for (int j = j0; j < j0 + 2; ++j) {
           float x;
@@ -508,35 +518,23 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
         }
       }
     };
-    if constexpr (DT == FK_F32) {                      // (products that take 2 or 8 times as long: in turn)
+    constexpr int products = PV + QK, ahead = DT == FK_F32 ? 4 : 2;
+    uint4 in[ahead + 1];
+    const auto input = [&](int at) {
+      return at < PV ? value_at(v_in, value_place, at) : key_at(k_in, key_place, at - PV);
+    };
 #pragma unroll
-      for (int ks = 0; ks < KT * 16; ++ks)
-#pragma unroll
-        for (int d = 0; d < L::dt; ++d) add_value(value_at(v_in, value_place, ks * L::dt + d), ks * L::dt + d);
-#pragma unroll
-      for (int at = 0; at < QK; ++at)
-        next[at % KT] = Mfma<DT>::run(key_at(k_in, key_place, at), q[at / KT], next[at % KT]);
-#pragma unroll
-      for (int w2 = 0; w2 < pieces; ++w2) piece(w2);
-    } else {
-      constexpr int products = PV + QK, ahead = 2;
-      uint4 in[ahead + 1];
-      const auto input = [&](int at) {
-        return at < PV ? value_at(v_in, value_place, at) : key_at(k_in, key_place, at - PV);
-      };
-#pragma unroll
-      for (int at = 0; at < ahead; ++at) in[at] = input(at);
-#pragma unroll
-      for (int at = 0; at < products; ++at) {
-        if (at + ahead < products) in[(at + ahead) % (ahead + 1)] = input(at + ahead);
-        const uint4 x = in[at % (ahead + 1)];
-        if (at < PV) add_value(x, at);
-        else next[(at - PV) % KT] = Mfma<DT>::run(x, q[(at - PV) / KT], next[(at - PV) % KT]);
-#pragma unroll
-        for (int w2 = at * pieces / products; w2 < (at + 1) * pieces / products; ++w2) piece(w2);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
+    for (int at = 0; at < ahead; ++at) in[at] = input(at);
+    each<products>([&](auto number) {
+      constexpr int at = decltype(number)::value;
+      if constexpr (at + ahead < products) in[(at + ahead) % (ahead + 1)] = input(at + ahead);
+      const uint4 x = in[at % (ahead + 1)];
+      if constexpr (at < PV) add_value(x, at);
+      else next[(at - PV) % KT] = Mfma<DT>::run(x, q[(at - PV) / KT], next[(at - PV) % KT]);
+      constexpr int from = at * pieces / products, to = (at + 1) * pieces / products;
+      each<to - from>([&](auto more) { piece(std::integral_constant<int, from + decltype(more)::value>()); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
     l = fmaf(l, f, sum[0] + sum[1]);
     grown = f, grew = __any(grows);
 #pragma unroll
@@ -639,8 +637,10 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
       for (int d = 0; d < L::dt; ++d)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[d][j] *= grown;
-#pragma unroll
-      for (int at = 0; at < PV; ++at) add_value(value_at((lptr8c)lv[buf ^ 1], value_place, at), at);
+      each<PV>([&](auto number) {
+        constexpr int at = decltype(number)::value;
+        add_value(value_at((lptr8c)lv[buf ^ 1], value_place, at), at);
+      });
     }
     find_rows(st + 2);
     if (st + 2 < t1) load_k(st + 2, (lptr8)lk[buf]);
