@@ -2,6 +2,8 @@
 // the matrix cores.
 #include "prompt.hpp"
 
+#include <algorithm>
+
 namespace fk {
 namespace {
 
@@ -50,8 +52,8 @@ template <int DT> hipError_t run(const PromptArgs& a, void* ws, hipStream_t s) {
 
 size_t prompt_ws_bytes(int dt, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   if (D > 256) return 0;
-  const int64_t rows = tile_waves(dt, (int)D) * 32;
-  const int64_t parts = most_parts(T, Hq / Hkv, Hkv, rows);
+  int64_t parts = most_parts(T, Hq / Hkv, Hkv, 128);
+  if (!only_four(dt, (int)D)) parts = std::max(parts, most_parts(T, Hq / Hkv, Hkv, 256));
   return parts == 1 ? 0 : (size_t)(parts * T * Hq) * (D + 2) * 4;
 }
 

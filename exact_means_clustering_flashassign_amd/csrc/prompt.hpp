@@ -117,24 +117,23 @@ typedef const __attribute__((address_space(3))) char* lptr8c;
 typedef const __attribute__((address_space(3))) u32x4* lptr16c;
 typedef const __attribute__((address_space(3))) uint32_t* lptr32c;
 
-// Waves of a block: 8 share the keys of a step; wide rows need the registers of 4. fp32 products
-// are an eighth as fast, so that smaller tiles, which more CUs share, cost nothing.
-constexpr int tile_waves(int dt, int DC) { return dt == FK_F32 || DC > 128 ? 4 : 8; }
-// Blocks that a CU holds at once: 64 rows of 64 fp32 elements twice, for keys and for values, are half its LDS.
-constexpr int tile_blocks(int dt, int DC) { return dt == FK_F32 && DC <= 64 ? 2 : 1; }
+// W waves of a block, 8 or 4, share the keys of a step. Wide rows need the registers of 4, and
+// fp32 products are an eighth as fast, so that smaller tiles, which more CUs share, cost
+// nothing. Blocks of 4 have a CU to themselves where rows are wide, else two run on it.
+constexpr bool only_four(int dt, int DC) { return dt == FK_F32 || DC > 128; }
+constexpr int tile_blocks(int dt, int DC, int W) { return W == 4 && (dt == FK_F32 ? DC <= 64 : DC <= 128) ? 2 : 1; }
 
-template <int DT, int DC> struct Tile {
+template <int DT, int DC, int W> struct Tile {
   static constexpr int eb = Val<DT>::bytes;
   static constexpr int pitch = DC <= 64 ? 64 : (DC <= 128 ? 128 : 256);    // elements of a row in LDS
   static constexpr int rb = pitch * eb;                   // and bytes
-  static constexpr int waves = tile_waves(DT, DC);
-  static constexpr int rows = waves * 32;
+  static constexpr int rows = W * 32;
   static constexpr int step = eb == 4 && DC > 64 ? 32 : 64;      // keys a step: two buffers fit the LDS
   static constexpr int key_tiles = step / 32;
   static constexpr int unit = 16 / eb;                    // elements of 16 bytes
   static constexpr int units = pitch / unit;              // 16-byte units of a row
   static constexpr int per_load = 64 / units;             // rows a wave brings with one load
-  static constexpr int share = step / waves;              // rows a wave brings a step
+  static constexpr int share = step / W;              // rows a wave brings a step
   static constexpr int loads = share / per_load;
   static constexpr int group = 64 / share;                // steps whose rows a wave finds at once
   static constexpr int dt = DC / 32, kt = DC / (2 * unit);        // tiles of the output, units of a score
@@ -257,6 +256,13 @@ template <int N, class F> __device__ __forceinline__ void each(const F& f) {
   each_of(std::make_integer_sequence<int, N>(), f);
 }
 
+// cap * tanh(s / cap) within a few 2^-24 of the cap: enough where probabilities are rounded to
+// 16 bits, and a third of capped()'s instructions.
+__device__ __forceinline__ float cap_16bit(float s, float cap, float inv_cap) {
+  const float e = fast_exp2(s * (inv_cap * (2.f * kLog2e)));
+  return fmaf(-2.f * cap, __builtin_amdgcn_rcpf(e + 1.f), cap);
+}
+
 struct PromptPlan {
   int heads, G, parts, chunk;     // cache heads, query heads of each, parts of a row's keys, steps of a part
   FastDiv page, by_heads, by_parts, by_G;
@@ -264,11 +270,11 @@ struct PromptPlan {
   float* ml;                      // (parts, T, Hq, 2) their maximum and sum
 };
 
-template <int DT, int DC, bool EXTRA>
-__global__ __launch_bounds__(tile_waves(DT, DC) * 64, tile_waves(DT, DC) / 4 * tile_blocks(DT, DC))
+template <int DT, int DC, int W, bool EXTRA>
+__global__ __launch_bounds__(W * 64, W / 4 * tile_blocks(DT, DC, W))
 void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
-  using L = Tile<DT, DC>;
-  constexpr int W = L::waves, rb = L::rb, eb = L::eb, kStep = L::step, KT = L::key_tiles, GS = L::group;
+  using L = Tile<DT, DC, W>;
+  constexpr int rb = L::rb, eb = L::eb, kStep = L::step, KT = L::key_tiles, GS = L::group;
   __shared__ __attribute__((aligned(1024))) char lk[2][kStep * rb], lv[2][kStep * rb];
   __shared__ uint64_t row_k[W][64], row_v[2][W][64];   // (values are asked for two steps after their keys)
   __shared__ uint64_t valid[2][GS];                    // keys of a step that count, a bit each
@@ -476,7 +482,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
           float x = s[u][j4 * 4 + j];
           if constexpr (EXTRA) {
             x *= a.scale;
-            if (cap > 0.f) x = capped(x, cap, inv_cap);
+            if (cap > 0.f) x = DT == FK_F32 ? capped(x, cap, inv_cap) : cap_16bit(x, cap, inv_cap);
             x = bb[j] == -INFINITY ? -INFINITY : x + bb[j];
           }
           if constexpr (masked) {
@@ -701,9 +707,9 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
 }
 
 // Joins the partial results of rows whose keys were cut, a row a wave.
-template <int DT, int DC>
+template <int DT, int DC, int W>
 __global__ __launch_bounds__(kWaves * 64) void prompt_join_kernel(PromptArgs a, PromptPlan p) {
-  constexpr int EPL = (DC + 63) / 64, rows = Tile<DT, DC>::rows, kStep = Tile<DT, DC>::step;
+  constexpr int EPL = (DC + 63) / 64, rows = Tile<DT, DC, W>::rows, kStep = Tile<DT, DC, W>::step;
   const int64_t r = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
   const int64_t t = r / a.Hq, b = t < a.T ? request_of(a, t) : -1;
   if (b < 0) return;
@@ -761,19 +767,40 @@ int parts_of_call(int64_t units, int64_t slots, int64_t longest, double mean, in
   return best;
 }
 
-template <int DT, int DC> hipError_t run_mfma(const PromptArgs& a, void* ws, hipStream_t s) {
+// What is known of a call without its lengths: tiles of so many rows at least, steps of a row at
+// most and in the mean (all keys but half the tokens).
+struct Outline {
+  int64_t tiles, longest;
+  double mean;
+};
+inline Outline outline(const PromptArgs& a, int64_t rows, int64_t step) {
+  const int64_t G = a.Hq / a.cache.heads, full = (a.T * G + rows - 1) / rows, most = longest(a);
+  const double each = (double)(a.T / a.B < most ? a.T / a.B : most);
+  return {full > a.B ? full : a.B, (most + step - 1) / step, most <= 0 ? 0. : (most - 0.5 * each) / (double)step};
+}
+
+// 256 rows a tile rather than 128 where their steps are many and either there are tiles for
+// every CU twice or rows see about as many keys as each other, unless most of such a tile
+// would be empty. (16-bit, 32 heads of 128 on 8, 4096 tokens: 182 us, 197 with 128 rows; 16384: 2340 and
+// 2510; 512: 30 and 24; 8192 tokens of 8 heads on 8: 278 and 212; 64 requests of one token
+// over 8192 keys: 341 and 238.)
+inline bool wide_tiles(const PromptArgs& a) {
+  const Outline o = outline(a, 256, 64);
+  const bool many = o.tiles * a.cache.heads >= 2 * (int64_t)device_cus();
+  const bool empty = a.T * (a.Hq / a.cache.heads) < 128 * a.B;
+  return o.mean >= 32 && (many ? !empty : o.mean >= 0.75 * (double)o.longest);
+}
+
+template <int DT, int DC, int W> hipError_t run_tiles(const PromptArgs& a, void* ws, hipStream_t s) {
+  using L = Tile<DT, DC, W>;
   PromptPlan p{};
   p.heads = (int)a.cache.heads;
   p.G = (int)(a.Hq / a.cache.heads);
-  constexpr int rows = Tile<DT, DC>::rows, kStep = Tile<DT, DC>::step;
-  const int64_t full = (a.T * p.G + rows - 1) / rows;      // at least so many tiles
-  const int64_t tiles = full + a.B - 1;                    // and at most so many
-  const int64_t most = longest(a), longest_steps = (most + kStep - 1) / kStep;
-  // mean keys of a row: all but half the tokens, as far as is known here
-  const double mean = most <= 0 ? 0. : (most - 0.5 * (double)(a.T / a.B < most ? a.T / a.B : most)) / kStep;
-  p.parts = parts_of_call((full > a.B ? full : a.B) * p.heads, device_cus() * tile_blocks(DT, DC), longest_steps,
-                          mean, most_parts(a.T, p.G, p.heads, rows), DT == FK_F32 ? 0.5 : 4.0);
-  p.chunk = p.parts == 1 ? 0x7FFFFFFF / kStep : (int)((longest_steps + p.parts - 1) / p.parts);
+  const Outline o = outline(a, L::rows, L::step);
+  const int64_t tiles = (a.T * p.G + L::rows - 1) / L::rows + a.B - 1;     // at most so many
+  p.parts = parts_of_call(o.tiles * p.heads, device_cus() * tile_blocks(DT, DC, W), o.longest, o.mean,
+                          most_parts(a.T, p.G, p.heads, L::rows), DT == FK_F32 ? 0.5 : 4.0);
+  p.chunk = p.parts == 1 ? 0x7FFFFFFF / L::step : (int)((o.longest + p.parts - 1) / p.parts);
   p.o = (float*)ws;
   p.ml = p.o + (int64_t)p.parts * a.T * a.Hq * a.cache.dim;
   p.page = fast_div((uint32_t)a.cache.page);
@@ -782,14 +809,20 @@ template <int DT, int DC> hipError_t run_mfma(const PromptArgs& a, void* ws, hip
   p.by_G = fast_div((uint32_t)p.G);
   const int64_t blocks = tiles * p.heads * p.parts;
   if (blocks > 0x7FFFFF || a.T * p.G > 0x7FFFFFFF - 512) return hipErrorInvalidConfiguration;
-  auto kernel = prompt_mfma_kernel<DT, DC, true>;
+  auto kernel = prompt_mfma_kernel<DT, DC, W, true>;
   if constexpr (DT != FK_F32)
-    if (a.softcap == 0.f && !a.cache.key_bias && a.scale > 0.f) kernel = prompt_mfma_kernel<DT, DC, false>;
-  kernel<<<(unsigned)blocks, Tile<DT, DC>::waves * 64, 0, s>>>(a, p);
+    if (a.softcap == 0.f && !a.cache.key_bias && a.scale > 0.f) kernel = prompt_mfma_kernel<DT, DC, W, false>;
+  kernel<<<(unsigned)blocks, W * 64, 0, s>>>(a, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.parts == 1) return e;
-  prompt_join_kernel<DT, DC><<<(unsigned)((a.T * a.Hq + kWaves - 1) / kWaves), kWaves * 64, 0, s>>>(a, p);
+  prompt_join_kernel<DT, DC, W><<<(unsigned)((a.T * a.Hq + kWaves - 1) / kWaves), kWaves * 64, 0, s>>>(a, p);
   return hipGetLastError();
+}
+
+template <int DT, int DC> hipError_t run_mfma(const PromptArgs& a, void* ws, hipStream_t s) {
+  if constexpr (!only_four(DT, DC))
+    if (wide_tiles(a)) return run_tiles<DT, DC, 8>(a, ws, s);
+  return run_tiles<DT, DC, 4>(a, ws, s);
 }
 
 }  // namespace
