@@ -16,8 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfkmeans.so")
 SOURCES = ["norms.hip", "assign.hip", "assign_splitd.hip", "update.hip", "api.hip",
-           "kvtables.hip", "qkrope.hip", "attn.hip", "prompt.hip", "prompt_wide.hip",
-           "cache8.hip", "attn8.hip", "api_kv.hip"]
+           "kvtables.hip", "qkrope.hip", "attn.hip", "prompt.hip", "prompt_f16.hip",
+           "prompt_bf16.hip", "prompt_f32.hip", "prompt_wide.hip", "cache8.hip", "attn8.hip", "api_kv.hip"]
 # The contrast baselines (materialised-distance assign, scatter-atomic
 # update) are a library of their own, linked against rocBLAS for the GEMM,
 # so the Lloyd library itself depends on nothing but the HIP runtime.
@@ -29,12 +29,14 @@ ROCM_LIB = "/opt/rocm/lib"
 # MFMA accumulators live in VGPRs, which the argmax reads without AGPR copies.
 # assign_splitd.hip keeps the default (accumulators in AGPRs): its 256
 # accumulator registers per lane would not fit the VGPR file.
-# attn.hip and attn8.hip rescale their accumulators every step and prompt.hip reads
-# its scores, so they live in VGPRs too; prompt_wide.hip's do not fit there.
+# attn.hip and attn8.hip rescale their accumulators every step and the prompt units
+# read their scores, so they live in VGPRs too; prompt_wide.hip's do not fit there.
 FILE_FLAGS = {"assign.hip": ["-fno-honor-nans", "-mllvm", "-amdgpu-mfma-vgpr-form"],
               "attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
               "attn8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-              "prompt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+              "prompt_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+              "prompt_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+              "prompt_f32.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 ARCH = "gfx950"
 
 FLAGS = [

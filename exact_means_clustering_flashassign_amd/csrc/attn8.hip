@@ -362,7 +362,7 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
           const int at = 16 * u + 4 * g + i;
           const float bias = now.bias[at];
           float x = s[h][u][i] * now.ks[at];
-          if (cap) x = capped(x, a.softcap, inv_cap);
+          if (cap) x = DT == FK_F32 ? capped(x, a.softcap, inv_cap) : cap_16bit(x, a.softcap, inv_cap);
           s[h][u][i] = bias == -INFINITY ? bias : (EXTRA ? x + bias : x);
           top = fmaxf(top, s[h][u][i]);
         }

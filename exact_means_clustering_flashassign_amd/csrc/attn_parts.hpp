@@ -30,6 +30,13 @@ __device__ __forceinline__ float capped(float s, float cap, float inv_cap) {
   return s == s ? r : s;     // the clamp drops a NaN
 }
 
+// cap * tanh(s / cap) within a few 2^-24 of the cap: enough where probabilities are rounded to
+// 16 bits, and a third of capped()'s instructions.
+__device__ __forceinline__ float cap_16bit(float s, float cap, float inv_cap) {
+  const float e = fast_exp2(s * (inv_cap * (2.f * kLog2e)));
+  return fmaf(-2.f * cap, __builtin_amdgcn_rcpf(e + 1.f), cap);
+}
+
 // Scale of a partial result (m, l) under the common maximum.
 __device__ __forceinline__ float join_factor(float m, float l, float top) {
   return l == 0.f ? 0.f : fast_exp2((m - top) * kLog2e);

@@ -120,6 +120,11 @@ struct PromptArgs {
 };
 size_t prompt_ws_bytes(int dt, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
 hipError_t launch_prompt_attn(const PromptArgs& a, int dt, void* ws, hipStream_t s);
-hipError_t launch_prompt_wide(const PromptArgs& a, int dt, void* ws, hipStream_t s);   // rows of 129 to 256
+// rows of up to 128 elements (a unit for each type), and of 129 to 256
+template <int DT> hipError_t launch_prompt_narrow(const PromptArgs& a, void* ws, hipStream_t s);
+template <> hipError_t launch_prompt_narrow<FK_F16>(const PromptArgs& a, void* ws, hipStream_t s);
+template <> hipError_t launch_prompt_narrow<FK_BF16>(const PromptArgs& a, void* ws, hipStream_t s);
+template <> hipError_t launch_prompt_narrow<FK_F32>(const PromptArgs& a, void* ws, hipStream_t s);
+hipError_t launch_prompt_wide(const PromptArgs& a, int dt, void* ws, hipStream_t s);
 
 }  // namespace fk

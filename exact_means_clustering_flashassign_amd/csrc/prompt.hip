@@ -1,5 +1,4 @@
-// Attention of a step's prompts: rows of any layout, and rows of up to 128 elements on
-// the matrix cores.
+// Attention of a step's prompts: rows of any layout, and the choice of kernel.
 #include "prompt.hpp"
 
 #include <algorithm>
@@ -41,11 +40,7 @@ bool aligned16(const PromptArgs& a, int eb) {
 template <int DT> hipError_t run(const PromptArgs& a, void* ws, hipStream_t s) {
   const int64_t D = a.cache.dim;
   if (D > 256 || !aligned16(a, Val<DT>::bytes)) return run_any<DT>(a, s);
-  return D <= 32    ? run_mfma<DT, 32>(a, ws, s)
-         : D <= 64  ? run_mfma<DT, 64>(a, ws, s)
-         : D <= 96  ? run_mfma<DT, 96>(a, ws, s)
-         : D <= 128 ? run_mfma<DT, 128>(a, ws, s)
-                    : launch_prompt_wide(a, DT, ws, s);
+  return D <= 128 ? launch_prompt_narrow<DT>(a, ws, s) : launch_prompt_wide(a, DT, ws, s);
 }
 
 }  // namespace

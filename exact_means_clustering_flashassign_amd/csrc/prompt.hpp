@@ -1,5 +1,5 @@
 // Attention of a step's prompts over a paged key-value cache: every new token over
-// its request's keys up to itself. The kernels; prompt.hip and prompt_wide.hip build them.
+// its request's keys up to itself. The kernels; the other prompt units build them.
 #pragma once
 
 #include <type_traits>
@@ -256,13 +256,6 @@ template <int N, class F> __device__ __forceinline__ void each(const F& f) {
   each_of(std::make_integer_sequence<int, N>(), f);
 }
 
-// cap * tanh(s / cap) within a few 2^-24 of the cap: enough where probabilities are rounded to
-// 16 bits, and a third of capped()'s instructions.
-__device__ __forceinline__ float cap_16bit(float s, float cap, float inv_cap) {
-  const float e = fast_exp2(s * (inv_cap * (2.f * kLog2e)));
-  return fmaf(-2.f * cap, __builtin_amdgcn_rcpf(e + 1.f), cap);
-}
-
 struct PromptPlan {
   int heads, G, parts, chunk;     // cache heads, query heads of each, parts of a row's keys, steps of a part
   FastDiv page, by_heads, by_parts, by_G;
@@ -270,10 +263,14 @@ struct PromptPlan {
   float* ml;                      // (parts, T, Hq, 2) their maximum and sum
 };
 
-template <int DT, int DC, int W, bool EXTRA>
+// What a score takes part in: the scale alone; scale and bias; cap as well.
+enum { kPlainScore, kBiasScore, kCapScore };
+
+template <int DT, int DC, int W, int SCORE>
 __global__ __launch_bounds__(W * 64, W / 4 * tile_blocks(DT, DC, W))
 void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   using L = Tile<DT, DC, W>;
+  constexpr bool EXTRA = SCORE != kPlainScore;
   constexpr int rb = L::rb, eb = L::eb, kStep = L::step, KT = L::key_tiles, GS = L::group;
   __shared__ __attribute__((aligned(1024))) char lk[2][kStep * rb], lv[2][kStep * rb];
   __shared__ uint64_t row_k[W][64], row_v[2][W][64];   // (values are asked for two steps after their keys)
@@ -321,6 +318,20 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
       const int e = (2 * i + h) * L::unit;
       q[i] = load16(e < D && mine && t >= 0 && t < a.T ? qp + e * eb : (uint64_t)zero_row);
     }
+  }
+
+  bool finite = true;                                  // every query of the wave
+  if constexpr (EXTRA && DT != FK_F32) {
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < L::kt; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        constexpr uint32_t top = DT == FK_F16 ? 0x7C00u : 0x7F80u;      // of a number that is not finite
+        const uint32_t x = word(q[i], j);
+        bad |= (x & top) == top || ((x >> 16) & top) == top;
+      }
+    finite = !__any(bad);
   }
 
   // rows of keys: lane (s, j) looks after row j of this wave's share in step s of a group
@@ -480,11 +491,16 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float x = s[u][j4 * 4 + j];
-          if constexpr (EXTRA) {
+          if constexpr (SCORE == kCapScore) {
             x *= a.scale;
-            if (cap > 0.f) x = DT == FK_F32 ? capped(x, cap, inv_cap) : cap_16bit(x, cap, inv_cap);
-            x = bb[j] == -INFINITY ? -INFINITY : x + bb[j];
+            if (DT != FK_F32 || cap > 0.f) x = DT == FK_F32 ? capped(x, cap, inv_cap) : cap_16bit(x, cap, inv_cap);
+            x += bb[j];
+          } else if constexpr (EXTRA) {
+            x = fmaf(x, a.scale, bb[j]);
           }
+          // (a key that is out has a score of 0, or NaN where the query is not finite:
+          // then all steps are masked ones)
+          if constexpr (EXTRA && masked) x = bb[j] == -INFINITY ? -INFINITY : x;
           if constexpr (masked) {
             const int key = u * 32 + j4 * 8 + h * 4 + j;
             x = key0 + key < limit && (EXTRA || ((ok >> key) & 1)) ? x : -INFINITY;
@@ -608,7 +624,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   int st = t0;
   bool here = false;                                   // step st has met already
   if constexpr (DT != FK_F32) {
-    const int whole = min(t1, low / kStep);
+    const int whole = finite ? min(t1, low / kStep) : t0;
     for (; st + 2 <= whole; st += 2) {                 // two at a time, so that scores and buffers change places
       meet();
       if (!EXTRA && !(all_valid(st) && all_valid(st + 1))) {
@@ -809,9 +825,12 @@ template <int DT, int DC, int W> hipError_t run_tiles(const PromptArgs& a, void*
   p.by_G = fast_div((uint32_t)p.G);
   const int64_t blocks = tiles * p.heads * p.parts;
   if (blocks > 0x7FFFFF || a.T * p.G > 0x7FFFFFFF - 512) return hipErrorInvalidConfiguration;
-  auto kernel = prompt_mfma_kernel<DT, DC, W, true>;
-  if constexpr (DT != FK_F32)
-    if (a.softcap == 0.f && !a.cache.key_bias && a.scale > 0.f) kernel = prompt_mfma_kernel<DT, DC, W, false>;
+  auto kernel = prompt_mfma_kernel<DT, DC, W, kCapScore>;
+  if constexpr (DT != FK_F32) {
+    if (a.softcap == 0.f)
+      kernel = a.cache.key_bias || !(a.scale > 0.f) ? prompt_mfma_kernel<DT, DC, W, kBiasScore>
+                                                    : prompt_mfma_kernel<DT, DC, W, kPlainScore>;
+  }
   kernel<<<(unsigned)blocks, W * 64, 0, s>>>(a, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.parts == 1) return e;
