@@ -135,6 +135,9 @@ template <int DT, int DC, int W> struct Tile {
   static constexpr int per_load = 64 / units;             // rows a wave brings with one load
   static constexpr int share = step / W;              // rows a wave brings a step
   static constexpr int loads = share / per_load;
+  // Steps of keys and of values in LDS: as many as there is room for, up to three, so that a step's
+  // rows have two steps' time to come.
+  static constexpr int held = 3 * 2 * step * rb * tile_blocks(DT, DC, W) <= 144 * 1024 ? 3 : 2;
   static constexpr int group = 64 / share;                // steps whose rows a wave finds at once
   static constexpr int dt = DC / 32, kt = DC / (2 * unit);        // tiles of the output, units of a score
 };
@@ -271,8 +274,8 @@ __global__ __launch_bounds__(W * 64, W / 4 * tile_blocks(DT, DC, W))
 void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   using L = Tile<DT, DC, W>;
   constexpr bool EXTRA = SCORE != kPlainScore;
-  constexpr int rb = L::rb, eb = L::eb, kStep = L::step, KT = L::key_tiles, GS = L::group;
-  __shared__ __attribute__((aligned(1024))) char lk[2][kStep * rb], lv[2][kStep * rb];
+  constexpr int rb = L::rb, eb = L::eb, kStep = L::step, KT = L::key_tiles, GS = L::group, NB = L::held;
+  __shared__ __attribute__((aligned(1024))) char lk[NB][kStep * rb], lv[NB][kStep * rb];
   __shared__ uint64_t row_k[W][64], row_v[2][W][64];   // (values are asked for two steps after their keys)
   __shared__ uint64_t valid[2][GS];                    // keys of a step that count, a bit each
   __shared__ float biases[EXTRA ? 2 : 1][EXTRA ? GS : 1][kStep];
@@ -318,6 +321,10 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
       const int e = (2 * i + h) * L::unit;
       q[i] = load16(e < D && mine && t >= 0 && t < a.T ? qp + e * eb : (uint64_t)zero_row);
     }
+    // (waited for here, or every step would wait for loads as if these were on their way)
+#pragma unroll
+    for (int i = 0; i < L::kt; ++i)
+      asm volatile("" : "+v"(q[i].x), "+v"(q[i].y), "+v"(q[i].z), "+v"(q[i].w));
   }
 
   bool finite = true;                                  // every query of the wave
@@ -461,8 +468,8 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
                            const lptr8 __restrict k_out, const lptr8 __restrict v_out) {
     constexpr bool masked = decltype(tag)::value;
     const int i = st - t0, key0 = st * kStep;
-    if (st + 2 < t1) load_k(st + 2, k_out);
-    load_v(st, v_out);
+    if (st + NB < t1) load_k(st + NB, k_out);
+    if (st + NB - 2 < t1) load_v(st + NB - 2, v_out);
     if (grew) {
 #pragma unroll
       for (int d = 0; d < L::dt; ++d)
@@ -589,22 +596,34 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
     bias1 = bias_of(i / GS + 1, pg1);
     pg2 = entry(i / GS + 2);
   };
-  const auto meet = [&] {                              // rows asked for are in, earlier steps are done with
-    __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0)
-    __syncthreads();
+  // Rows asked for are in, but for those of the last step where there are three buffers and it
+  // asked for a whole one (loads come back in order); earlier steps are done with.
+  const auto meet = [&](bool all) {
+    constexpr int last = NB == 3 ? 2 * L::loads : 0;
+    if (NB == 2 || all) __builtin_amdgcn_s_waitcnt(0x0F70);                              // vmcnt(0)
+    else __builtin_amdgcn_s_waitcnt(0x0F70 | (last & 15) | (last >> 4) << 14);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
   };
+  // Buffer of step st's keys and values.
+  int buf = 0;                                         // of the step that is at
+  const auto after = [&](int k) { return NB == 2 ? buf ^ (k & 1) : (buf + k) % 3; };
+  const auto keys_of = [&](int k) { return (lptr8)(lk[0]) + after(k) * (kStep * rb); };
+  const auto values_of = [&](int k) { return (lptr8)(lv[0]) + after(k) * (kStep * rb); };
   const int own_end = min(t1, (int)(((uint32_t)high + kStep - 1) / kStep));     // steps of this wave
   if (t0 < t1) {
     pg1 = entry(0), pg2 = entry(1);
     bias1 = bias_of(0, pg1);
-    find_rows(t0);
-    load_k(t0, (lptr8)lk[0]);
-    if (t0 + 1 < t1) {
-      find_rows(t0 + 1);
-      load_k(t0 + 1, (lptr8)lk[1]);
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      if (t0 + k >= t1) break;
+      find_rows(t0 + k);
+      load_k(t0 + k, keys_of(k));
     }
+    if (NB == 3) load_v(t0, values_of(0));
     // the pipeline starts with no values and no probabilities
-    for (int i = threadIdx.x; i < kStep * rb / 16; i += W * 64) ((uint4*)lv[1])[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < kStep * rb / 16; i += W * 64) ((uint4*)lv[NB - 1])[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int u = 0; u < KT; ++u) {
       if constexpr (DT != FK_F32) pr[u][0] = pr[u][1] = make_uint4(0, 0, 0, 0);
@@ -612,7 +631,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) pf[u][j] = 0.f;
     }
-    meet();
+    meet(true);
     clear(sa);
 #pragma unroll
     for (int at = 0; at < QK; ++at)
@@ -623,26 +642,29 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   // masks.
   int st = t0;
   bool here = false;                                   // step st has met already
+  const auto few = [&] { return st + NB - 1 >= t1 || st == t0; };       // the last step asked for less than a whole one
   if constexpr (DT != FK_F32) {
     const int whole = finite ? min(t1, low / kStep) : t0;
-    for (; st + 2 <= whole; st += 2) {                 // two at a time, so that scores and buffers change places
-      meet();
+    for (; st + 2 <= whole; st += 2) {                 // two at a time, so that scores change places
+      meet(few());
       if (!EXTRA && !(all_valid(st) && all_valid(st + 1))) {
         here = true;
         break;
       }
-      find_rows(st + 2);
-      advance(st, std::false_type(), sa, sb, (lptr8c)lk[1], (lptr8c)lv[1], (lptr8)lk[0], (lptr8)lv[0]);
-      meet();
-      find_rows(st + 3);
-      advance(st + 1, std::false_type(), sb, sa, (lptr8c)lk[0], (lptr8c)lv[0], (lptr8)lk[1], (lptr8)lv[1]);
+      find_rows(st + NB);
+      advance(st, std::false_type(), sa, sb, keys_of(1), values_of(NB - 1), keys_of(0), values_of(NB - 2));
+      buf = after(1);
+      meet(st + NB >= t1);
+      find_rows(st + 1 + NB);
+      advance(st + 1, std::false_type(), sb, sa, keys_of(1), values_of(NB - 1), keys_of(0), values_of(NB - 2));
+      buf = after(1);
     }
   }
   for (; st < own_end; ++st, here = false) {
-    const int buf = (st - t0) & 1;
-    if (!here) meet();
-    find_rows(st + 2);
-    advance(st, std::true_type(), sa, sb, (lptr8c)lk[buf ^ 1], (lptr8c)lv[buf ^ 1], (lptr8)lk[buf], (lptr8)lv[buf]);
+    if (!here) meet(few());
+    find_rows(st + NB);
+    advance(st, std::true_type(), sa, sb, keys_of(1), values_of(NB - 1), keys_of(0), values_of(NB - 2));
+    buf = after(1);
 #pragma unroll
     for (int u = 0; u < KT; ++u) sa[u] = sb[u];
     if (!looked && (st + 1) * kStep > low) {           // (its hidden values have not been added yet)
@@ -652,8 +674,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
     }
   }
   for (; st <= t1 && t0 < t1; ++st, here = false) {    // the last values, and the other waves' steps
-    const int buf = (st - t0) & 1;
-    if (!here) meet();
+    if (!here) meet(few());
     if (st == own_end) {
 #pragma unroll
       for (int d = 0; d < L::dt; ++d)
@@ -661,12 +682,13 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
         for (int j = 0; j < 16; ++j) o[d][j] *= grown;
       each<PV>([&](auto number) {
         constexpr int at = decltype(number)::value;
-        add_value(value_at((lptr8c)lv[buf ^ 1], value_place, at), at);
+        add_value(value_at((lptr8c)values_of(NB - 1), value_place, at), at);
       });
     }
-    find_rows(st + 2);
-    if (st + 2 < t1) load_k(st + 2, (lptr8)lk[buf]);
-    if (st < t1) load_v(st, (lptr8)lv[buf]);
+    find_rows(st + NB);
+    if (st + NB < t1) load_k(st + NB, keys_of(0));
+    if (st + NB - 2 < t1) load_v(st + NB - 2, values_of(NB - 2));
+    buf = after(1);
   }
   l = sum_halves(l);
   const int64_t row = t * a.Hq + qh;
