@@ -123,6 +123,11 @@ typedef const __attribute__((address_space(3))) uint32_t* lptr32c;
 constexpr bool only_four(int dt, int DC) { return dt == FK_F32 || DC > 128; }
 constexpr int tile_blocks(int dt, int DC, int W) { return W == 4 && (dt == FK_F32 ? DC <= 64 : DC <= 128) ? 2 : 1; }
 
+// fp16 probabilities are scaled by 2^13, and may pass the running maximum's by 2^2, bf16 by 2^8:
+// the sums are scaled anew only when a maximum grows by more.
+template <int DT> constexpr float prob_shift = DT == FK_F16 ? 13.f : 0.f;
+template <int DT> constexpr float prob_slack = DT == FK_F16 ? 2.f : 8.f;
+
 template <int DT, int DC, int W> struct Tile {
   static constexpr int eb = Val<DT>::bytes;
   static constexpr int pitch = DC <= 64 ? 64 : (DC <= 128 ? 128 : 256);    // elements of a row in LDS
@@ -181,17 +186,16 @@ __device__ __forceinline__ uint2 read_transposed(lptr8c at) {
 struct Where {
   int64_t b;          // request, -1: none
   int tile;           // tile of its rows
+  int cu0, cu1, len;  // its tokens and keys
 };
 __device__ __forceinline__ Where find_tile(const PromptArgs& a, int G, int rows, uint32_t order) {
   const int lane = threadIdx.x & 63;
   uint32_t before = 0;
   for (int64_t last = a.B - 1; last >= 0; last -= 64) {
-    const int64_t b = last - lane;
-    uint32_t mine = 0;
-    if (b >= 0) {
-      const int64_t n = (int64_t)a.cu[b + 1] - a.cu[b];
-      mine = n > 0 ? (uint32_t)((n * G + rows - 1) / rows) : 0;
-    }
+    const int64_t b = max(last - lane, (int64_t)0);
+    const int cu0 = a.cu[b], cu1 = a.cu[b + 1], len = a.lens[b];
+    const int64_t n = (int64_t)cu1 - cu0;
+    const uint32_t mine = last - lane >= 0 && n > 0 ? (uint32_t)((n * G + rows - 1) / rows) : 0;
     uint32_t incl = mine;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -202,17 +206,13 @@ __device__ __forceinline__ Where find_tile(const PromptArgs& a, int G, int rows,
     if (order < before + total) {
       const int at = __popcll(__ballot(before + incl <= order));
       const uint32_t end = before + __builtin_amdgcn_readlane(incl, at);
-      return {last - at, (int)(end - 1 - order)};
+      return {last - at, (int)(end - 1 - order), (int)__builtin_amdgcn_readlane(cu0, at),
+              (int)__builtin_amdgcn_readlane(cu1, at), (int)__builtin_amdgcn_readlane(len, at)};
     }
     before += total;
   }
-  return {-1, 0};
+  return {-1, 0, 0, 0, 0};
 }
-
-// fp16 probabilities are scaled by 2^13, and may pass the running maximum's by 2^2, bf16 by 2^8:
-// the sums are scaled anew only when a maximum grows by more.
-template <int DT> constexpr float prob_shift = DT == FK_F16 ? 13.f : 0.f;
-template <int DT> constexpr float prob_slack = DT == FK_F16 ? 2.f : 8.f;
 
 // Which of a lane's sums are not finite, a bit each.
 template <int N> struct NotFinite { uint32_t bits[(N + 1) / 2]; };
@@ -290,7 +290,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   const Where at = find_tile(a, p.G, L::rows, order);
   if (at.b < 0) return;
   const int64_t b = uniform(at.b);
-  const int64_t cu0 = a.cu[b], cu1 = a.cu[b + 1], len = a.lens[b];
+  const int64_t cu0 = at.cu0, cu1 = at.cu1, len = at.len;
   const int rows = (int)min((cu1 - cu0) * p.G - (int64_t)at.tile * L::rows, (int64_t)L::rows);
   const int64_t held = min(a.width * c.page, (int64_t)0x7FFFFFC0);
   // keys that row r of the tile sees
@@ -314,32 +314,6 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   const int low = wave_rows > 0 ? __builtin_amdgcn_readfirstlane(seen(w * 32)) : 0;
   const int high = wave_rows > 0 ? __builtin_amdgcn_readfirstlane(seen(w * 32 + wave_rows - 1)) : 0;
   uint4 q[L::kt];
-  {
-    const uint64_t qp = (uint64_t)a.q + (uint64_t)(t * a.q_stride[0] + qh * a.q_stride[1]) * eb;
-#pragma unroll
-    for (int i = 0; i < L::kt; ++i) {
-      const int e = (2 * i + h) * L::unit;
-      q[i] = load16(e < D && mine && t >= 0 && t < a.T ? qp + e * eb : (uint64_t)zero_row);
-    }
-    // (waited for here, or every step would wait for loads as if these were on their way)
-#pragma unroll
-    for (int i = 0; i < L::kt; ++i)
-      asm volatile("" : "+v"(q[i].x), "+v"(q[i].y), "+v"(q[i].z), "+v"(q[i].w));
-  }
-
-  bool finite = true;                                  // every query of the wave
-  if constexpr (EXTRA && DT != FK_F32) {
-    uint32_t bad = 0;
-#pragma unroll
-    for (int i = 0; i < L::kt; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        constexpr uint32_t top = DT == FK_F16 ? 0x7C00u : 0x7F80u;      // of a number that is not finite
-        const uint32_t x = word(q[i], j);
-        bad |= (x & top) == top || ((x >> 16) & top) == top;
-      }
-    finite = !__any(bad);
-  }
 
   // rows of keys: lane (s, j) looks after row j of this wave's share in step s of a group
   constexpr int share = L::share;
@@ -611,9 +585,16 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   const auto after = [&](int k) { return NB == 2 ? buf ^ (k & 1) : (buf + k) % 3; };
   const auto keys_of = [&](int k) { return (lptr8)(lk[0]) + after(k) * (kStep * rb); };
   const auto values_of = [&](int k) { return (lptr8)(lv[0]) + after(k) * (kStep * rb); };
+  bool finite = true;                                  // every query of the wave
   const int own_end = min(t1, (int)(((uint32_t)high + kStep - 1) / kStep));     // steps of this wave
   if (t0 < t1) {
     pg1 = entry(0), pg2 = entry(1);
+    const uint64_t qp = (uint64_t)a.q + (uint64_t)(t * a.q_stride[0] + qh * a.q_stride[1]) * eb;
+#pragma unroll
+    for (int i = 0; i < L::kt; ++i) {
+      const int e = (2 * i + h) * L::unit;
+      q[i] = load16(e < D && mine && t >= 0 && t < a.T ? qp + e * eb : (uint64_t)zero_row);
+    }
     bias1 = bias_of(0, pg1);
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
@@ -630,6 +611,22 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
       else
 #pragma unroll
         for (int j = 0; j < 16; ++j) pf[u][j] = 0.f;
+    }
+    // (waited for here, or every step would wait for loads as if these were on their way)
+#pragma unroll
+    for (int i = 0; i < L::kt; ++i)
+      asm volatile("" : "+v"(q[i].x), "+v"(q[i].y), "+v"(q[i].z), "+v"(q[i].w));
+    if constexpr (EXTRA && DT != FK_F32) {
+      uint32_t bad = 0;
+#pragma unroll
+      for (int i = 0; i < L::kt; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          constexpr uint32_t top = DT == FK_F16 ? 0x7C00u : 0x7F80u;      // of a number that is not finite
+          const uint32_t x = word(q[i], j);
+          bad |= (x & top) == top || ((x >> 16) & top) == top;
+        }
+      finite = !__any(bad);
     }
     meet(true);
     clear(sa);
@@ -760,17 +757,31 @@ __global__ __launch_bounds__(kWaves * 64) void prompt_join_kernel(PromptArgs a, 
   if (steps <= p.chunk) return;
   const int parts = (int)min((int64_t)p.parts, (steps + p.chunk - 1) / p.chunk);
   const int64_t every = a.T * a.Hq;
-  float m = -INFINITY, l = 0.f, o[EPL];
-  for (int i = 0; i < parts; ++i) m = fmaxf(m, p.ml[(i * every + r) * 2]);
+  // a part a lane (there are 64 at most), then eight parts' rows at a time
+  const float2 ml = lane < parts ? *(const float2*)(p.ml + (lane * every + r) * 2) : make_float2(-INFINITY, 0.f);
+  float m = ml.x;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  const float f = join_factor(ml.x, ml.y, m), l = wave_sum(f * ml.y);
+  float o[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-  for (int i = 0; i < parts; ++i) {
-    const float2 ml = *(const float2*)(p.ml + (i * every + r) * 2);
-    const float f = join_factor(ml.x, ml.y, m);
-    l = fmaf(f, ml.y, l);
+  for (int i0 = 0; i0 < parts; i0 += 8) {
+    float x[8][EPL];
 #pragma unroll
-    for (int e = 0; e < EPL; ++e)
-      if (lane + 64 * e < D) o[e] = fmaf(f, p.o[(i * every + r) * D + lane + 64 * e], o[e]);
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        const int64_t at = (min(i0 + i, parts - 1) * every + r) * D + lane + 64 * e;
+        x[i][e] = lane + 64 * e < D ? p.o[at] : 0.f;
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float g = __shfl(f, min(i0 + i, 63), 64);          // (0 past the last part)
+      // (a part without keys has left no row: what is there is not to be used)
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] = g == 0.f ? o[e] : fmaf(g, x[i][e], o[e]);
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -787,24 +798,6 @@ int64_t most_parts(int64_t T, int64_t G, int64_t heads, int64_t rows) {
   return n < 1 ? 1 : (n > 64 ? 64 : n);
 }
 
-// Parts of a call: the number with the shortest estimate, in steps of one block, where `slots`
-// blocks run at once. A block spends `fixed` steps' time before and after its steps, and as
-// much again on a partial result.
-int parts_of_call(int64_t units, int64_t slots, int64_t longest, double mean, int64_t most, double fixed) {
-  int best = 1;
-  double least = 1e300;
-  for (int64_t n = 1; n <= most && (n == 1 || longest >= n * 2 * fixed); ++n) {
-    const double over = n > 1 ? 2 * fixed : fixed, one = (double)((longest + n - 1) / n) + over;
-    double time = one;
-    if (units * n > slots) {
-      const double all = (double)units * (mean + n * over) / slots;
-      time = (all > one ? all : one) + 0.5 * one;
-    }
-    if (time < least) least = time, best = (int)n;
-  }
-  return best;
-}
-
 // What is known of a call without its lengths: tiles of so many rows at least, steps of a row at
 // most and in the mean (all keys but half the tokens).
 struct Outline {
@@ -817,27 +810,57 @@ inline Outline outline(const PromptArgs& a, int64_t rows, int64_t step) {
   return {full > a.B ? full : a.B, (most + step - 1) / step, most <= 0 ? 0. : (most - 0.5 * each) / (double)step};
 }
 
-// 256 rows a tile rather than 128 where their steps are many and either there are tiles for
-// every CU twice or rows see about as many keys as each other, unless most of such a tile
-// would be empty. (16-bit, 32 heads of 128 on 8, 4096 tokens: 182 us, 197 with 128 rows; 16384: 2340 and
-// 2510; 512: 30 and 24; 8192 tokens of 8 heads on 8: 278 and 212; 64 requests of one token
-// over 8192 keys: 341 and 238.)
-inline bool wide_tiles(const PromptArgs& a) {
-  const Outline o = outline(a, 256, 64);
-  const bool many = o.tiles * a.cache.heads >= 2 * (int64_t)device_cus();
-  const bool empty = a.T * (a.Hq / a.cache.heads) < 128 * a.B;
-  return o.mean >= 32 && (many ? !empty : o.mean >= 0.75 * (double)o.longest);
+// Microseconds of a call whose keys are cut into `parts`, from what was measured: products at
+// 1000 (16-bit) or 150 TFLOP/s over the chip, 5% less for two blocks a CU; 15 us of a block before and
+// after its steps and 3 for a partial result; 6 us and 4 TB/s to join them. Blocks are taken longest first. A block of
+// 4 waves alone on its CU is 1.6 times as fast as next to another. Rows that see unlike numbers of
+// keys leave CUs free for each other; where all are alike, a last round is as long as any.
+inline double estimate(int dt, int DC, int W, int step, const PromptArgs& a, const Outline& o, int64_t parts) {
+  const double cus = device_cus(), slots = cus * tile_blocks(dt, DC, W), rows = W * 32;
+  const double together = (slots > cus ? 1.05 : 1.) * 4. * rows * step * DC / ((dt == FK_F32 ? 150e6 : DC <= 64 ? 700e6 : 1000e6) / slots);
+  const double blocks = (double)o.tiles * a.cache.heads * parts;
+  const double alone = slots > cus ? together / 1.6 : together;
+  const double fixed = parts > 1 ? 18. : 15., alike = o.longest > 0 ? 2. * (o.mean / o.longest - 0.5) : 1.;
+  const double last = (double)((o.longest + parts - 1) / parts);
+  double us;
+  if (blocks <= slots) {
+    // next to another block until that ends
+    const double both = blocks > cus ? 0.5 * (last + o.mean / parts) * together : 0.;
+    us = (last * alone > both ? last * alone : both) + fixed;
+  } else {
+    const double one = last * together + fixed, all = blocks * (o.mean / parts * together + fixed) / slots;
+    const double uneven = (all > one ? all : one) + 0.2 * one, even = ceil(blocks / slots) * one;
+    const double u = alike < 0. ? 0. : (alike > 1. ? 1. : alike);
+    us = (1. - u) * uneven + u * even;
+  }
+  if (parts > 1) us += 6. + (double)(a.T * a.Hq) * parts * (a.cache.dim + 2) * 8. / 4e6;
+  return us;
 }
 
-template <int DT, int DC, int W> hipError_t run_tiles(const PromptArgs& a, void* ws, hipStream_t s) {
+// The number of parts with the shortest estimate.
+struct Best {
+  double us;
+  int parts;
+};
+inline Best best_parts(int dt, int DC, int W, int step, const PromptArgs& a) {
+  const Outline o = outline(a, W * 32, step);
+  const int64_t most = most_parts(a.T, a.Hq / a.cache.heads, a.cache.heads, W * 32);
+  Best best{1e300, 1};
+  for (int64_t n = 1; n <= most && (n == 1 || o.longest >= 4 * n); ++n) {
+    const double us = estimate(dt, DC, W, step, a, o, n);
+    if (us < best.us) best = {us, (int)n};
+  }
+  return best;
+}
+
+template <int DT, int DC, int W> hipError_t run_tiles(const PromptArgs& a, int parts, void* ws, hipStream_t s) {
   using L = Tile<DT, DC, W>;
   PromptPlan p{};
   p.heads = (int)a.cache.heads;
   p.G = (int)(a.Hq / a.cache.heads);
   const Outline o = outline(a, L::rows, L::step);
   const int64_t tiles = (a.T * p.G + L::rows - 1) / L::rows + a.B - 1;     // at most so many
-  p.parts = parts_of_call(o.tiles * p.heads, device_cus() * tile_blocks(DT, DC, W), o.longest, o.mean,
-                          most_parts(a.T, p.G, p.heads, L::rows), DT == FK_F32 ? 0.5 : 4.0);
+  p.parts = parts;
   p.chunk = p.parts == 1 ? 0x7FFFFFFF / L::step : (int)((o.longest + p.parts - 1) / p.parts);
   p.o = (float*)ws;
   p.ml = p.o + (int64_t)p.parts * a.T * a.Hq * a.cache.dim;
@@ -860,10 +883,16 @@ template <int DT, int DC, int W> hipError_t run_tiles(const PromptArgs& a, void*
   return hipGetLastError();
 }
 
+// Tiles of 256 rows or of 128, of which two blocks share a CU. (16-bit, 32 heads of 128 on 8, 4096
+// tokens: 182 us, 197 with 128 rows; 16384: 2340 and 2510; 512: 30 and 24; 8192 tokens of 8
+// heads on 8: 278 and 212; 64 requests of one token over 8192 keys: 341 and 238.)
 template <int DT, int DC> hipError_t run_mfma(const PromptArgs& a, void* ws, hipStream_t s) {
-  if constexpr (!only_four(DT, DC))
-    if (wide_tiles(a)) return run_tiles<DT, DC, 8>(a, ws, s);
-  return run_tiles<DT, DC, 4>(a, ws, s);
+  const Best four = best_parts(DT, DC, 4, Tile<DT, DC, 4>::step, a);
+  if constexpr (!only_four(DT, DC)) {
+    const Best eight = best_parts(DT, DC, 8, Tile<DT, DC, 8>::step, a);
+    if (eight.us < 0.97 * four.us) return run_tiles<DT, DC, 8>(a, eight.parts, ws, s);
+  }
+  return run_tiles<DT, DC, 4>(a, four.parts, ws, s);
 }
 
 }  // namespace
