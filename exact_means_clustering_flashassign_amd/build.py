@@ -30,13 +30,14 @@ ROCM_LIB = "/opt/rocm/lib"
 # assign_splitd.hip keeps the default (accumulators in AGPRs): its 256
 # accumulator registers per lane would not fit the VGPR file.
 # attn.hip and attn8.hip rescale their accumulators every step and the prompt units
-# read their scores, so they live in VGPRs too; prompt_wide.hip's do not fit there.
+# read their scores, so they live in VGPRs too.
 FILE_FLAGS = {"assign.hip": ["-fno-honor-nans", "-mllvm", "-amdgpu-mfma-vgpr-form"],
               "attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
               "attn8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
               "prompt_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
               "prompt_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-              "prompt_f32.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+              "prompt_f32.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+              "prompt_wide.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 ARCH = "gfx950"
 
 FLAGS = [

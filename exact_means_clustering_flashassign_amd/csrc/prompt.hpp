@@ -521,7 +521,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
         }
       }
     };
-    constexpr int products = PV + QK, ahead = DT == FK_F32 ? 4 : 2;
+    constexpr int products = PV + QK, ahead = DT == FK_F32 || DC > 128 ? 4 : 2;
     uint4 in[ahead + 1];
     const auto input = [&](int at) {
       return at < PV ? value_at(v_in, value_place, at) : key_at(k_in, key_place, at - PV);

@@ -1,6 +1,4 @@
-// Attention of a step's prompts on the matrix cores: rows of 129 to 256 elements. A unit of
-// its own, as its accumulators fill the accumulation registers (the other unit's are
-// vector registers).
+// Attention of a step's prompts on the matrix cores: rows of 129 to 256 elements.
 #include "prompt.hpp"
 
 namespace fk {
