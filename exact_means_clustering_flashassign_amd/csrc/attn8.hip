@@ -293,18 +293,15 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
   uint4 kf[S::tiles][S::nc];
-  auto load_k = [&](const Rows8& r) {
+  auto load_k = [&](const Rows8& r, int s) {
+    const uint64_t ad = r.k[16 * s + m];
 #pragma unroll
-    for (int s = 0; s < S::tiles; ++s) {
-      const uint64_t ad = r.k[16 * s + m];
-#pragma unroll
-      for (int i = 0; i < S::nc; ++i) kf[s][i] = load_row<16, KIND == kStream>((past(i) ? zero : ad) + koff[i]);
-    }
+    for (int i = 0; i < S::nc; ++i) kf[s][i] = load_row<16, KIND == kStream>((past(i) ? zero : ad) + koff[i]);
   };
   uint4 vf[S::rows][S::nu];            // a load of fewer bytes fills the first words
-  auto load_v = [&](const Rows8& r) {
+  auto load_v = [&](const Rows8& r, int y) {             // of tiles 2 y and 2 y + 1
 #pragma unroll
-    for (int j = 0; j < S::rows; ++j) {
+    for (int j = 8 * y; j < 8 * y + 8; ++j) {
       const uint64_t ad = r.v[16 * (j >> 2) + 4 * g + (j & 3)];
 #pragma unroll
       for (int i = 0; i < S::nu; ++i) vf[j][i] = load_row<S::ve, KIND == kStream>(ad + voff[i]);
@@ -316,8 +313,10 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
   Numbers x1 = numbers(step + stride, pg2);
   pg1 = pg2;
   pg2 = entry(step + 2 * stride);
-  load_k(rows[0]);
-  load_v(rows[0]);
+#pragma unroll
+  for (int u = 0; u < S::tiles; ++u) load_k(rows[0], u);
+#pragma unroll
+  for (int y = 0; y < S::tiles / 2; ++y) load_v(rows[0], y);
   int par = 0;
   for (; step < end; step += stride, par ^= 1) {
     Rows8& now = rows[par];
@@ -343,9 +342,9 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
       for (int h = 0; h < HT; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[h][u][i] = x[h][i];
+      load_k(next, u);                   // the next keys are asked for as soon as these are out of
+      __builtin_amdgcn_sched_barrier(0); // their registers
     }
-    load_k(next);
-    __builtin_amdgcn_sched_barrier(0);   // the next keys are on their way before the softmax
     x1 = numbers(step + 2 * stride, pg2);
     pg1 = pg2;
     pg2 = entry(step + 3 * stride);
@@ -394,7 +393,7 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
       }
     }
 #pragma unroll
-    for (int y = 0; y < S::tiles / 2; ++y)
+    for (int y = 0; y < S::tiles / 2; ++y) {
 #pragma unroll
       for (int u = 0; u < S::nu; ++u)
 #pragma unroll
@@ -419,8 +418,9 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
             }
           }
         }
-    load_v(next);
-    __builtin_amdgcn_sched_barrier(0);
+      load_v(next, y);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
