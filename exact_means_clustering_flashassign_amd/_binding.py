@@ -677,36 +677,28 @@ def _launch(where, index, fn, *args):
         _check(st, where)
 
 
-def _attn_outputs(tc, q, sq, heads, need, out, lse, return_lse, ws, inputs, index):
-    """Outputs and workspace of an attention call, those given checked against each other and
-    the inputs (spans for _apart): out, lse, and the addresses of out, lse and ws with ws's size."""
-    dt, dev, given = q.dtype, q.device, []
-    if need == 0:
-        raise ValueError(f"{q.shape[1]} query heads of {q.shape[2]} do not go with {heads} cache heads")
-    if out is None:
-        out = tc.empty(q.shape, dtype=dt, device=dev)
-        p_out = out.data_ptr()
-    else:
-        p_out = _on(out, "out", dt, q.shape, index)
+def _attn_given(tc, q, need, out, lse, ws, inputs, index):
+    """Checks of the outputs and the workspace that a caller gives to an attention call, against
+    each other and the inputs (name, tensor): addresses of out, lse and ws, and ws's size."""
+    p_out = p_lse = p_ws = None
+    given = []
+    if out is not None:
+        p_out = _on(out, "out", q.dtype, q.shape, index)
         given.append(("out", p_out, p_out + out.numel() * out.element_size()))
-    p_lse = None
     if lse is not None:
         p_lse = _on(lse, "lse", tc.f32, q.shape[:2], index)
         given.append(("lse", p_lse, p_lse + 4 * lse.numel()))
-    elif return_lse:
-        lse = tc.empty(q.shape[:2], dtype=tc.f32, device=dev)
-        p_lse = lse.data_ptr()
-    if ws is None:
-        ws = tc.empty(need, dtype=tc.u8, device=dev)
-        p_ws = ws.data_ptr()
-    else:
+    if ws is not None:
         need = ws.numel()
         p_ws = _on(ws, "ws", tc.u8, (need,), index)
         given.append(("ws", p_ws, p_ws + need))
-    if given:
-        _apart([g for g in given if g[1] < g[2]],
-               [_span(n, t, t.stride(), t.element_size()) for n, t in inputs if t is not None])
-    return out, lse, p_out, p_lse, ws, p_ws, need
+    _apart([g for g in given if g[1] < g[2]],
+           [_span(n, t, t.stride(), t.element_size()) for n, t in inputs if t is not None])
+    return p_out, p_lse, p_ws, need
+
+
+def _no_heads(q, heads):
+    raise ValueError(f"{q.shape[1]} query heads of {q.shape[2]} do not go with {heads} cache heads")
 
 
 @functools.lru_cache(256)
@@ -740,10 +732,22 @@ def fk_prompt_attn(q, k_cache, v_cache, table, lens, cu_tokens, scale: Optional[
     B, width = table.shape
     p_lens = _on(lens, "lens", tc.i32, (B,), index)
     p_cu = _on(cu_tokens, "cu_tokens", tc.i32, (B + 1,), index)
-    out, lse, p_out, p_lse, ws, p_ws, need = _attn_outputs(
-        tc, q, sq, heads, _prompt_ws(code, T, B, Hq, heads, D), out, lse, return_lse, ws,
-        (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("key_bias", key_bias),
-         ("table", table), ("lens", lens), ("cu_tokens", cu_tokens)), index)
+    need = _prompt_ws(code, T, B, Hq, heads, D) or _no_heads(q, heads)
+    p_out = p_lse = p_ws = None
+    if out is not None or lse is not None or ws is not None:
+        p_out, p_lse, p_ws, need = _attn_given(
+            tc, q, need, out, lse, ws,
+            (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("key_bias", key_bias),
+             ("table", table), ("lens", lens), ("cu_tokens", cu_tokens)), index)
+    if p_out is None:
+        out = tc.empty((T, Hq, D), dtype=dt, device=q.device)
+        p_out = out.data_ptr()
+    if p_lse is None and return_lse:
+        lse = tc.empty((T, Hq), dtype=tc.f32, device=q.device)
+        p_lse = lse.data_ptr()
+    if p_ws is None:
+        ws = tc.empty(need, dtype=tc.u8, device=q.device)
+        p_ws = ws.data_ptr()
     _launch("fk_prompt_attn", index, _lib.fk_prompt_attn, q.data_ptr(), _pack2(sq[0], sq[1]), code,
             T, B, Hq, cache, table.data_ptr(), st2[0] if B > 1 else width, width, p_lens, p_cu,
             max_len, D ** -0.5 if scale is None else scale, softcap, p_out, p_lse, p_ws, need,
@@ -781,7 +785,10 @@ def _extent(t, stride):
     p = t.data_ptr()
     if not t.numel():
         return p, p
-    return p, p + (sum((n - 1) * s for n, s in zip(t.shape, stride)) + 1) * t.element_size()
+    last = 1
+    for n, k in zip(t.shape, stride):
+        last += (n - 1) * k
+    return p, p + last * t.element_size()
 
 
 def fk_kv_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, key_bias=None) -> None:
@@ -797,23 +804,26 @@ def fk_kv_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, key_bias=None)
     if code is None:
         code = dtype_code(dt)            # says what is supported
     sk, sv = _rows(k, "k", dt, 3, index), _rows(v, "v", dt, 3, index)
-    if v.shape != k.shape:
-        raise ValueError(f"v must have k's shape {tuple(k.shape)}, got {tuple(v.shape)}")
-    T, H, D = k.shape
+    shape = k.shape
+    if v.shape != shape:
+        raise ValueError(f"v must have k's shape {tuple(shape)}, got {tuple(v.shape)}")
+    T, H, D = shape
     p_slots = _on(slots, "slots", tc.i32, (T,), index)
-    cache, _ = _kv_cache8(k_cache, v_cache, k_scale, v_scale, key_bias, H, D, index)
-    held = [("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale)]
-    if key_bias is not None:
-        held.append(("key_bias", key_bias))
-    held = [(n, *_extent(t, t.stride())) for n, t in held]
-    for name, lo, hi in (("k", *_extent(k, sk)), ("v", *_extent(v, sv)),
-                         ("slots", p_slots, p_slots + 4 * T)):
-        for other, a, b in held:
-            if lo < b and a < hi:
-                raise ValueError(f"{other} overlaps {name}, which the call reads")
-    if held[0][1:] == held[1][1:] and T and k_cache.numel() or \
-            held[2][1:] == held[3][1:] and T and k_scale.numel():
-        raise ValueError("keys and values, and their scales, need tensors of their own")
+    cache, held = _kv_cache8(k_cache, v_cache, k_scale, v_scale, key_bias, H, D, index)
+    if T and held.numel():
+        parts = [("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale)]
+        if key_bias is not None:
+            parts.append(("key_bias", key_bias))
+        k0, k1 = _extent(k, sk)
+        v0, v1 = _extent(v, sv)
+        p_end, at = p_slots + 4 * T, set()
+        for name, t in parts:
+            a, b = _extent(t, t.stride())
+            at.add(a)
+            if k0 < b and a < k1 or v0 < b and a < v1 or p_slots < b and a < p_end:
+                raise ValueError(f"{name} overlaps k, v or slots, which the call reads")
+        if len(at) < len(parts):
+            raise ValueError("keys and values, their scales and biases need tensors of their own")
     _launch("fk_kv_store8", index, _lib.fk_kv_store8, k.data_ptr(), _pack2(sk[0], sk[1]),
             v.data_ptr(), _pack2(sv[0], sv[1]), code, T, p_slots, cache, tc.stream(index))
 
@@ -877,12 +887,24 @@ def fk_paged_attn8(q, k_cache, v_cache, k_scale, v_scale, table, lens,
     if rows != B:
         raise ValueError(f"table must have {B} rows, got {tuple(table.shape)}")
     p_lens = _on(lens, "lens", tc.i32, (B,), index)
-    in_place = out is not None and out.data_ptr() == q.data_ptr() and q.is_contiguous()
-    out, lse, p_out, p_lse, ws, p_ws, need = _attn_outputs(
-        tc, q, sq, shape[2], _attn8_ws(code, B, Hq, shape[2], D), out, lse, return_lse, ws,
-        (("q", None if in_place else q), ("k_cache", k_cache), ("v_cache", v_cache),
-         ("k_scale", k_scale), ("v_scale", v_scale), ("key_bias", key_bias), ("table", table),
-         ("lens", lens)), index)
+    need = _attn8_ws(code, B, Hq, shape[2], D) or _no_heads(q, shape[2])
+    p_out = p_lse = p_ws = None
+    if out is not None or lse is not None or ws is not None:
+        in_place = out is not None and out.data_ptr() == q.data_ptr() and q.is_contiguous()
+        p_out, p_lse, p_ws, need = _attn_given(
+            tc, q, need, out, lse, ws,
+            (("q", None if in_place else q), ("k_cache", k_cache), ("v_cache", v_cache),
+             ("k_scale", k_scale), ("v_scale", v_scale), ("key_bias", key_bias), ("table", table),
+             ("lens", lens)), index)
+    if p_out is None:
+        out = tc.empty((B, Hq, D), dtype=dt, device=q.device)
+        p_out = out.data_ptr()
+    if p_lse is None and return_lse:
+        lse = tc.empty((B, Hq), dtype=tc.f32, device=q.device)
+        p_lse = lse.data_ptr()
+    if p_ws is None:
+        ws = tc.empty(need, dtype=tc.u8, device=q.device)
+        p_ws = ws.data_ptr()
     _launch("fk_paged_attn8", index, _lib.fk_paged_attn8, q.data_ptr(), _pack2(sq[0], sq[1]), code,
             B, Hq, cache, table.data_ptr(), st2[0] if B > 1 else width, width, p_lens, max_len,
             D ** -0.5 if scale is None else scale, softcap, p_out, p_lse, p_ws, need,
