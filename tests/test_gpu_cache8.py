@@ -275,3 +275,122 @@ def test_paged_attn8(fk, case, dtype):
     table = args["table"]                              # room for 2^20 keys a request, most of it unused
     args["table"] = torch.cat([table, table.new_full((table.shape[0], (1 << 20) // case[3]), -1)], 1)
     _check_attn(fk.fk_paged_attn8(**args), want, dtype, case[2], case[6], "wide table")
+
+
+def test_paged_attn8_many_ragged_requests(fk):
+    rng = np.random.default_rng(5)
+    lens = [int(n) for n in np.exp(rng.uniform(0, np.log(3000), 90))]
+    lens[::9] = [0] * len(lens[::9])
+    args, want = _attn_case((4, 2, 64, 16, lens, None, 0.0, "plain"), "bf16", 6)
+    for hint in (0, max(lens)):
+        _check_attn(fk.fk_paged_attn8(max_len=hint, **args), want, "bf16", 64, 0.0)
+    lens = [int(n) for n in np.exp(rng.uniform(0, np.log(600), 700))]
+    lens[::7] = [0] * len(lens[::7])
+    args, want = _attn_case((4, 4, 128, 8, lens, None, 0.0, "plain"), "f16", 7)
+    for hint in (0, 200, 32):
+        _check_attn(fk.fk_paged_attn8(max_len=hint, **args), want, "f16", 128, 0.0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dims", [(4, 2, 64), (40, 2, 96), (2, 1, 256), (3, 3, 33)], ids=["d64", "g20d96", "d256", "d33"])
+def test_paged_attn8_numbers_that_are_not_finite(fk, dims, dtype):
+    """NaN codes that count reach their request, head and element; nothing else does; masked keys and
+    queries of nothing left stay out."""
+    torch = _torch()
+    Hq, Hkv, D = dims
+    lens = [70, 5, 700, 40]
+    args, want = _attn_case((Hq, Hkv, D, 16, lens, None, 0.0, "plain"), dtype, D + 3)
+    table, G = args["table"], Hq // Hkv
+    page, tok = int(table[2, 20]), 9
+    args["v_cache"].view(torch.uint8)[page, tok, Hkv - 1, 5] = 127
+    out, lse = (t.clone() for t in fk.fk_paged_attn8(**args))
+    assert out[2, -G:, 5].isnan().all() and out.isnan().sum() == G
+    out[2, -G:, 5] = torch.from_numpy(want[0][2, -G:, 5]).to(out)
+    _check_attn((out, lse), want, dtype, D, 0.0)
+    args["v_cache"].view(torch.uint8)[page, tok, Hkv - 1, 5] = 0
+    args["k_cache"].view(torch.uint8)[page, tok, 0, D - 1] = 255
+    out, lse = fk.fk_paged_attn8(**args)
+    assert out[2, :G].isnan().all() and lse[2, :G].isnan().all()
+    assert out.isnan().sum() == G * D and lse.isnan().sum() == G
+    # a query that is not finite and has no keys
+    args["q"][1], args["table"][1] = math.nan, -1
+    out, lse = fk.fk_paged_attn8(**args)
+    assert (out[1] == 0).all() and (lse[1] == -math.inf).all()
+    args["q"][3, 0, 0] = math.inf                      # and one that has some
+    out, lse = fk.fk_paged_attn8(**args)
+    assert not out[3, 0].isfinite().any() and out[3, 1:].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [64, 33])
+def test_captured_and_replayed(fk, D, dtype):
+    """Store, read back and attention in one graph, replayed over other rows and lengths, with eager
+    calls between the replays, on a stream of its own."""
+    torch = _torch()
+    B, H, page, T = 3, 2, 8, 40
+    made = []
+    for seed in range(3):
+        rng = np.random.default_rng(seed)
+        rows = [to_dev(_rand(rng, (T, H, D), dtype), dtype) for _ in range(2)]
+        slots = rng.permutation(9 * page)[:T].astype(np.int32)
+        slots[3] = -1
+        lens = rng.integers(0, 3 * page + 1, B).astype(np.int32)
+        table = rng.permutation(9).reshape(B, 3).astype(np.int32)
+        made.append((*rows, _dev(slots), _dev(lens), _dev(table), to_dev(_rand(rng, (B, 4 * H, D), dtype), dtype)))
+    k, v, slots, lens, table, q = (t.clone() for t in made[0])
+
+    def fresh():
+        c = _cache(9, page, H, D, "plain")
+        for t in c[2:]:
+            t.fill_(1.0)
+        return c
+
+    def step(c, k, v, slots, lens, table, q, **kw):
+        fk.fk_kv_store8(k, v, slots, *c)
+        back = fk.fk_kv_load8(slots, *c[:4], k.dtype)
+        return (*back, *fk.fk_paged_attn8(q, *c[:4], table, lens, key_bias=c[4], return_lse=True, **kw))
+
+    held = fresh()
+    ws = torch.empty(fk.fk_workspace_size_attn8(q.dtype, B, 4 * H, H, D), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(held, k, v, slots, lens, table, q, ws=ws)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = step(held, k, v, slots, lens, table, q, ws=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    for i in (1, 0, 2, 2, 1):
+        for a, b in zip((k, v, slots, lens, table, q), made[i]):
+            a.copy_(b)
+        for a, b in zip(held, fresh()):
+            a.view(torch.uint8).copy_(b.view(torch.uint8)) if a.dtype == torch.float8_e4m3fn else a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(fresh(), *made[i])
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i
+
+
+def test_nothing_to_do(fk):
+    torch = _torch()
+    kc, vc, ks, vs, kb = _cache(2, 4, 2, 64, "plain")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x = torch.zeros((0, 2, 64), device="cuda")
+    fk.fk_kv_store8(x, x, torch.zeros(0, **i32), kc, vc, ks, vs, kb)
+    assert ks.isnan().all() and kb.isnan().all()
+    k, v = fk.fk_kv_load8(torch.zeros(0, **i32), kc, vc, ks, vs, torch.float16)
+    assert k.shape == v.shape == (0, 2, 64)
+    none = [t[:0] for t in (kc, vc, ks, vs)]           # a cache without pages
+    y = torch.ones((3, 2, 64), device="cuda")
+    fk.fk_kv_store8(y, y, torch.zeros(3, **i32), *none)
+    k, v = fk.fk_kv_load8(torch.arange(3, **i32), *none, torch.float32)
+    assert (k == 0).all() and (v == 0).all()
+    out, lse = fk.fk_paged_attn8(torch.ones((2, 4, 64), device="cuda"), *none, torch.zeros((2, 3), **i32),
+                                 torch.full((2,), 9, **i32), return_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    out = fk.fk_paged_attn8(torch.ones((0, 4, 64), device="cuda"), kc, vc, ks, vs, torch.zeros((0, 3), **i32),
+                            torch.zeros(0, **i32))
+    assert out.shape == (0, 4, 64)
