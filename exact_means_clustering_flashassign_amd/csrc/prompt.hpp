@@ -47,35 +47,48 @@ __device__ __forceinline__ void row_sums(const PromptArgs& a, int64_t b, int64_t
     o[i] = 0.f;
   }
   m = -INFINITY, l = 0.f;
-  for (int64_t j = j0; j < j1; ++j) {
-    const int64_t page = a.table[b * a.ld_table + j / c.page], tok = j % c.page;
-    if (page < 0 || page >= c.pages) continue;
-    float bias = 0.f;
-    if (c.key_bias) {
-      bias = c.key_bias[page * c.bias_stride[0] + tok * c.bias_stride[1] + hk * c.bias_stride[2]];
-      if (bias == -INFINITY) continue;
-    }
-    const E* k = (const E*)c.k + page * c.k_stride[0] + tok * c.k_stride[1] + hk * c.k_stride[2];
-    const E* v = (const E*)c.v + page * c.v_stride[0] + tok * c.v_stride[1] + hk * c.v_stride[2];
-    float s = 0.f;
+  // A sum in 32 bits stands still after 2^24 terms alike: sums over kRun keys are summed.
+  constexpr int64_t kRun = 1 << 16;
+  for (int64_t start = j0; start < j1; start += kRun) {
+    float mr = -INFINITY, lr = 0.f, r[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + 64 * i;
-      if (e < D) s = fmaf(qf[i], Val<DT>::get(k + e), s);
+    for (int i = 0; i < EPL; ++i) r[i] = 0.f;
+    for (int64_t j = start; j < min(start + kRun, j1); ++j) {
+      const int64_t page = a.table[b * a.ld_table + j / c.page], tok = j % c.page;
+      if (page < 0 || page >= c.pages) continue;
+      float bias = 0.f;
+      if (c.key_bias) {
+        bias = c.key_bias[page * c.bias_stride[0] + tok * c.bias_stride[1] + hk * c.bias_stride[2]];
+        if (bias == -INFINITY) continue;
+      }
+      const E* k = (const E*)c.k + page * c.k_stride[0] + tok * c.k_stride[1] + hk * c.k_stride[2];
+      const E* v = (const E*)c.v + page * c.v_stride[0] + tok * c.v_stride[1] + hk * c.v_stride[2];
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane + 64 * i;
+        if (e < D) s = fmaf(qf[i], Val<DT>::get(k + e), s);
+      }
+      s = wave_sum(s) * a.scale;
+      if (a.softcap > 0.f) s = capped(s, a.softcap, 1.f / a.softcap);
+      s += bias;
+      const float mn = fmaxf(mr, s);
+      const float alpha = mr == -INFINITY ? 0.f : fast_exp2((mr - mn) * kLog2e);
+      const float p = s == -INFINITY ? 0.f : fast_exp2((s - mn) * kLog2e);   // NaN stays NaN
+      lr = lr * alpha + p;
+      mr = mn;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane + 64 * i;
+        if (e < D) r[i] = fmaf(p, Val<DT>::get(v + e), r[i] * alpha);
+      }
     }
-    s = wave_sum(s) * a.scale;
-    if (a.softcap > 0.f) s = capped(s, a.softcap, 1.f / a.softcap);
-    s += bias;
-    const float mn = fmaxf(m, s);
-    const float alpha = m == -INFINITY ? 0.f : fast_exp2((m - mn) * kLog2e);
-    const float p = s == -INFINITY ? 0.f : fast_exp2((s - mn) * kLog2e);   // NaN stays NaN
-    l = l * alpha + p;
+    const float mn = fmaxf(m, mr);
+    const float f = m == mn ? 1.f : fast_exp2((m - mn) * kLog2e), g = mr == mn ? 1.f : fast_exp2((mr - mn) * kLog2e);
+    l = l * f + lr * g;
     m = mn;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + 64 * i;
-      if (e < D) o[i] = fmaf(p, Val<DT>::get(v + e), o[i] * alpha);
-    }
+    for (int i = 0; i < EPL; ++i) o[i] = start == j0 ? r[i] : fmaf(r[i], g, o[i] * f);
   }
 }
 
@@ -94,22 +107,32 @@ __device__ __forceinline__ void put_row(const PromptArgs& a, int64_t row, float 
 }
 
 // ---------------------------------------------------------------------------
-// Matrix-core kernel of 16-bit caches: rows of at most 256 elements in whole 16-byte units
+// Matrix-core kernel: rows of at most 256 elements in whole 16-byte units
 // ---------------------------------------------------------------------------
 // The G query heads of a cache head see the same keys, so row r of a request is head r % G
-// of token r / G, and a tile is kRows rows in a run. A block takes one tile of one cache head
-// over a range of keys, a wave 32 of its rows, 64 keys a step.
+// of token r / G, and a tile is 256 or 128 rows in a run. A block takes one tile of one cache head
+// over a range of keys, a wave 32 of its rows, 64 keys a step (32 for wide fp32 rows).
 //
 // Lane (n = lane & 31, h = lane >> 5) of a wave. Scores are S^T = K Q^T with v_mfma 32x32x16:
 // register i of the lane holds the score of query row n with key (i & 3) + 8 (i >> 2) + 4 h of
 // 32. The values enter as O^T = V^T P^T: the contraction runs over keys, whose order is
 // free, so the eight probabilities a lane gives to a product are those it holds, of keys 4 h +
 // 0..3 and 8 + 4 h + 0..3 of 16, and V^T comes from LDS in that order by transposing reads
-// (four keys of one element a lane each). Nothing but keys and values goes through LDS.
+// (four keys of one element a lane each). fp32 products take two keys each, one a half of the
+// wave: those a lane's two halves hold in the same register. Only keys and values go through LDS.
 //
-// Keys and values go from the cache's pages straight to LDS, 16 bytes a lane, two buffers in
-// turn. Each wave brings 64 / waves rows a step; their addresses are found for as many
+// Keys and values go from the cache's pages straight to LDS, 16 bytes a lane, two or three buffers in
+// turn. Each wave brings its share of a step's rows; their addresses are found for as many
 // steps at once as make up 64, and table entries and biases are asked for two such groups ahead.
+//
+// What bounds it: with 32 rows a wave a product of 32 cycles reads 1 KB of LDS, of which a CU
+// gives four SIMDs 128 bytes a cycle, so products and reads would both fill their time at
+// the peak; before that, power: 53% of the matrix units' cycles are used at a clock of
+// 1.85 GHz (2.1 where the units wait more). Measured: 32768 tokens, 32 heads of 128 on 8, bf16, 8.45 to
+// 8.7 ms, 1010 to 1040 TFLOP/s (a large library product on random numbers reaches 1142 on the
+// same card); with probabilities and products in turn instead of together 9.6 ms, and
+// with reads that wait for all loads on their way 9.8. Short prompts are bound by a block's start and
+// end, 15 us of dependent loads and stores around a few steps of 2.
 typedef const __attribute__((address_space(1))) uint32_t* gptr32;
 typedef __attribute__((address_space(3))) uint32_t* lptr32;
 typedef __attribute__((address_space(3))) char* lptr8;
@@ -138,7 +161,7 @@ template <int DT, int DC, int W> struct Tile {
   static constexpr int unit = 16 / eb;                    // elements of 16 bytes
   static constexpr int units = pitch / unit;              // 16-byte units of a row
   static constexpr int per_load = 64 / units;             // rows a wave brings with one load
-  static constexpr int share = step / W;              // rows a wave brings a step
+  static constexpr int share = step / W;                  // rows a wave brings a step
   static constexpr int loads = share / per_load;
   // Steps of keys and of values in LDS: as many as there is room for, up to three, so that a step's
   // rows have two steps' time to come.
@@ -181,37 +204,36 @@ __device__ __forceinline__ uint2 read_transposed(lptr8c at) {
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)at));
 }
 
-// The tile of a block: requests are taken from the last one on, their tiles likewise, so that
-// the longest rows of a prompt come first and the chip does not wait for one at the end.
+// The tile of a block. Request b's tiles have the numbers floor(cu_tokens[b] G / rows) + b on: they
+// are never more than there are numbers up to the next request's, so that a tile's request is
+// found by a search (64 requests a round) instead of sums over all before it; a number
+// left over is a block without work. The last number comes first: the longest rows of a
+// prompt are not what the chip waits for at the end.
 struct Where {
   int64_t b;          // request, -1: none
   int tile;           // tile of its rows
   int cu0, cu1, len;  // its tokens and keys
 };
-__device__ __forceinline__ Where find_tile(const PromptArgs& a, int G, int rows, uint32_t order) {
+template <int ROWS> __device__ __forceinline__ Where find_tile(const PromptArgs& a, int G, uint32_t order) {
   const int lane = threadIdx.x & 63;
-  uint32_t before = 0;
-  for (int64_t last = a.B - 1; last >= 0; last -= 64) {
-    const int64_t b = max(last - lane, (int64_t)0);
-    const int cu0 = a.cu[b], cu1 = a.cu[b + 1], len = a.lens[b];
-    const int64_t n = (int64_t)cu1 - cu0;
-    const uint32_t mine = last - lane >= 0 && n > 0 ? (uint32_t)((n * G + rows - 1) / rows) : 0;
-    uint32_t incl = mine;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const uint32_t o = __shfl_up(incl, off, 64);
-      if (lane >= off) incl += o;
+  const auto first = [&](int64_t b, int cu) { return ((int64_t)cu * G) / ROWS + b; };
+  const int64_t number = first(a.B, max(a.cu[a.B], 0)) - 1 - order;
+  if (number < 0) return {-1, 0, 0, 0, 0};
+  int64_t lo = 0, hi = a.B;
+  for (;;) {
+    const int64_t span = (hi - lo + 63) / 64, b = lo + lane * span, at = min(b, hi - 1);
+    const int cu0 = max(a.cu[at], 0), cu1 = a.cu[at + 1], len = a.lens[at];
+    const int before = __popcll(__ballot(b < hi && first(at, cu0) <= number));
+    if (before == 0) return {-1, 0, 0, 0, 0};
+    lo += (before - 1) * span;
+    if (span == 1) {
+      const int c0 = __builtin_amdgcn_readlane(cu0, before - 1), c1 = __builtin_amdgcn_readlane(cu1, before - 1);
+      const int64_t tile = number - first(lo, c0);
+      if (tile * ROWS >= ((int64_t)c1 - c0) * G) return {-1, 0, 0, 0, 0};
+      return {lo, (int)tile, c0, c1, (int)__builtin_amdgcn_readlane(len, before - 1)};
     }
-    const uint32_t total = __builtin_amdgcn_readlane(incl, 63);
-    if (order < before + total) {
-      const int at = __popcll(__ballot(before + incl <= order));
-      const uint32_t end = before + __builtin_amdgcn_readlane(incl, at);
-      return {last - at, (int)(end - 1 - order), (int)__builtin_amdgcn_readlane(cu0, at),
-              (int)__builtin_amdgcn_readlane(cu1, at), (int)__builtin_amdgcn_readlane(len, at)};
-    }
-    before += total;
+    hi = min(lo + span, hi);
   }
-  return {-1, 0, 0, 0, 0};
 }
 
 // Which of a lane's sums are not finite, a bit each.
@@ -241,7 +263,7 @@ template <int N> __device__ __forceinline__ bool newly(const NotFinite<N>& now, 
 
 // 16 bytes a lane from its address straight to LDS, lane after lane from `to` on (the same in
 // every lane). Written out, as the compiler would let every later read of LDS wait for
-// the bytes, whatever it reads; what waits is s_waitcnt vmcnt(0) before the
+// the bytes, whatever it reads; what waits is an s_waitcnt vmcnt before the
 // barrier after which they are read. No register is written, and the address is
 // read when the instruction is issued. m0, which nothing else here uses, takes a wait
 // state before it is read.
@@ -287,12 +309,12 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
 
   const uint32_t rest = div_by(blockIdx.x, p.by_heads), hk = blockIdx.x - rest * p.heads;
   const uint32_t order = div_by(rest, p.by_parts), part = rest - order * p.parts;
-  const Where at = find_tile(a, p.G, L::rows, order);
+  const Where at = find_tile<L::rows>(a, p.G, order);
   if (at.b < 0) return;
   const int64_t b = uniform(at.b);
   const int64_t cu0 = at.cu0, cu1 = at.cu1, len = at.len;
   const int rows = (int)min((cu1 - cu0) * p.G - (int64_t)at.tile * L::rows, (int64_t)L::rows);
-  const int64_t held = min(a.width * c.page, (int64_t)0x7FFFFFC0);
+  const int64_t held = min(a.width * c.page, (int64_t)0x7FFFFFFF);
   // keys that row r of the tile sees
   const auto seen = [&](int r) {
     const int64_t t = div_by((uint32_t)(at.tile * L::rows + r), p.by_G);
@@ -392,9 +414,8 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   // scores of step st + 1 keep the matrix units busy while the vector units make step st's
   // probabilities of its scores. A wave issues both in turn: after each product some of
   // the work on probabilities, which the product takes longer than; what the products read from LDS is
-  // asked for two of them ahead. Loads for later steps go to the other buffers; the
-  // pointers are restricted so that reads do not wait for them. masked: some key of the
-  // step is hidden from some row.
+  // asked for two of them ahead. Loads for later steps go to the other buffers. masked: some key
+  // of the step is hidden from some row.
   uint4 pr[DT == FK_F32 ? 1 : KT][2];                  // probabilities, 16 bits
   float pf[DT == FK_F32 ? KT : 1][16];                 // and fp32
   float grown = 1.f;                                   // what the sums have to be scaled by, and
@@ -441,7 +462,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
                            const lptr8c __restrict k_in, const lptr8c __restrict v_in,
                            const lptr8 __restrict k_out, const lptr8 __restrict v_out) {
     constexpr bool masked = decltype(tag)::value;
-    const int i = st - t0, key0 = st * kStep;
+    const int i = st - t0, key0 = (int)((uint32_t)st * kStep);
     if (st + NB < t1) load_k(st + NB, k_out);
     if (st + NB - 2 < t1) load_v(st + NB - 2, v_out);
     if (grew) {
@@ -585,6 +606,53 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   const auto after = [&](int k) { return NB == 2 ? buf ^ (k & 1) : (buf + k) % 3; };
   const auto keys_of = [&](int k) { return (lptr8)(lk[0]) + after(k) * (kStep * rb); };
   const auto values_of = [&](int k) { return (lptr8)(lv[0]) + after(k) * (kStep * rb); };
+  // fp32 products add a key or two at a time, and a sum in 32 bits stands still after 2^24 terms
+  // alike (16-bit ones add 16 keys and reach 2^28): the sums over kRun steps are added to the row's
+  // place in the results or the workspace, where they are held scaled to `m_kept`.
+  constexpr int kRun = 1 << 15;
+  bool kept = false;
+  float m_kept = -INFINITY;
+  const auto with_kept = [&](auto each_four) {         // the lane's sums and their place, four by four
+    if (grew) {                                        // (what these sums wait for)
+#pragma unroll
+      for (int d = 0; d < L::dt; ++d)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[d][j] *= grown;
+    }
+    grew = false, grown = 1.f;
+    const float f = m_kept == m ? 1.f : fast_exp2((m_kept - m) * unit_log2);
+    const int64_t row = t * a.Hq + qh;
+    float* to = p.parts > 1 && steps > p.chunk ? p.o + ((int64_t)part * a.T * a.Hq + row) * D : (float*)a.out + row * D;
+    if (!mine || t < 0 || t >= a.T) return;
+#pragma unroll
+    for (int d = 0; d < L::dt; ++d)
+#pragma unroll
+      for (int j4 = 0; j4 < 4; ++j4) {
+        const int e = d * 32 + j4 * 8 + h * 4;
+        if (e < D) each_four((float4*)(to + e), f, d, j4 * 4);
+      }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (waits for keys and values count on no other accesses)
+  };
+  const auto keep = [&] {
+    with_kept([&](float4* to, float f, int d, int j) {
+      float4 x = kept ? *to : make_float4(0.f, 0.f, 0.f, 0.f);
+      x = make_float4(fmaf(x.x, f, o[d][j]), fmaf(x.y, f, o[d][j + 1]), fmaf(x.z, f, o[d][j + 2]), fmaf(x.w, f, o[d][j + 3]));
+      *to = x;
+    });
+#pragma unroll
+    for (int d = 0; d < L::dt; ++d)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[d][j] = 0.f;
+    kept = true, m_kept = m;
+  };
+  const auto take_back = [&] {
+    with_kept([&](float4* to, float f, int d, int j) {
+      const float4 x = *to;
+      o[d][j] = fmaf(x.x, f, o[d][j]), o[d][j + 1] = fmaf(x.y, f, o[d][j + 1]);
+      o[d][j + 2] = fmaf(x.z, f, o[d][j + 2]), o[d][j + 3] = fmaf(x.w, f, o[d][j + 3]);
+    });
+    kept = false;
+  };
   bool finite = true;                                  // every query of the wave
   const int own_end = min(t1, (int)(((uint32_t)high + kStep - 1) / kStep));     // steps of this wave
   if (t0 < t1) {
@@ -664,8 +732,11 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
     buf = after(1);
 #pragma unroll
     for (int u = 0; u < KT; ++u) sa[u] = sb[u];
-    if (!looked && (st + 1) * kStep > low) {           // (its hidden values have not been added yet)
+    if constexpr (DT == FK_F32)
+      if ((st - t0) % kRun == kRun - 1) keep();
+    if (!looked && (uint32_t)(st + 1) * kStep > (uint32_t)low) {           // (its hidden values have not been added yet)
       looked = true;
+      if (DT == FK_F32 && kept) take_back();
       broken_before = __any(!all_finite<L::dt>(o));
       if (broken_before) broken[threadIdx.x] = not_finite<L::dt>(o);
     }
@@ -687,6 +758,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
     if (st + NB - 2 < t1) load_v(st + NB - 2, values_of(NB - 2));
     buf = after(1);
   }
+  if (DT == FK_F32 && kept) take_back();
   l = sum_halves(l);
   const int64_t row = t * a.Hq + qh;
   const float m_nat = EXTRA ? m : m * a.scale;
@@ -716,7 +788,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   }
   // A hidden key's probability is 0, but 0 times an infinity or NaN of its value is NaN. Rows whose
   // sums stopped being finite in steps that hide keys are done again, key by key.
-  bool again = put && l - l == 0.f && !all_finite<L::dt>(o);
+  bool again = looked && put && l - l == 0.f && !all_finite<L::dt>(o);
   if (broken_before && __any(again)) again = again && newly<L::dt>(not_finite<L::dt>(o), broken[threadIdx.x]);
   uint64_t todo = __ballot(again);
   todo = (todo | todo >> 32) & 0xFFFFFFFFu;
@@ -811,13 +883,15 @@ inline Outline outline(const PromptArgs& a, int64_t rows, int64_t step) {
 }
 
 // Microseconds of a call whose keys are cut into `parts`, from what was measured: products at
-// 1000 (16-bit) or 150 TFLOP/s over the chip, 5% less for two blocks a CU; 15 us of a block before and
-// after its steps and 3 for a partial result; 6 us and 4 TB/s to join them. Blocks are taken longest first. A block of
-// 4 waves alone on its CU is 1.6 times as fast as next to another. Rows that see unlike numbers of
-// keys leave CUs free for each other; where all are alike, a last round is as long as any.
+// 1000 TFLOP/s over the chip (16 bits; 700 for rows of 64 and less, 150 for fp32), 5% less for two
+// blocks a CU; 15 us of a block before and after its steps, 3 more for a partial result; 6 us and
+// 4 TB/s to join them. Blocks are taken longest first. A block of 4 waves alone on its
+// CU is 1.6 times as fast as next to another. Rows that see unlike numbers of keys leave
+// CUs free for each other; where all are alike, a last round is as long as any.
 inline double estimate(int dt, int DC, int W, int step, const PromptArgs& a, const Outline& o, int64_t parts) {
   const double cus = device_cus(), slots = cus * tile_blocks(dt, DC, W), rows = W * 32;
-  const double together = (slots > cus ? 1.05 : 1.) * 4. * rows * step * DC / ((dt == FK_F32 ? 150e6 : DC <= 64 ? 700e6 : 1000e6) / slots);
+  const double rate = dt == FK_F32 ? 150e6 : DC <= 64 ? 700e6 : 1000e6;
+  const double together = (slots > cus ? 1.05 : 1.) * 4. * rows * step * DC / (rate / slots);
   const double blocks = (double)o.tiles * a.cache.heads * parts;
   const double alone = slots > cus ? together / 1.6 : together;
   const double fixed = parts > 1 ? 18. : 15., alike = o.longest > 0 ? 2. * (o.mean / o.longest - 0.5) : 1.;
@@ -859,7 +933,7 @@ template <int DT, int DC, int W> hipError_t run_tiles(const PromptArgs& a, int p
   p.heads = (int)a.cache.heads;
   p.G = (int)(a.Hq / a.cache.heads);
   const Outline o = outline(a, L::rows, L::step);
-  const int64_t tiles = (a.T * p.G + L::rows - 1) / L::rows + a.B - 1;     // at most so many
+  const int64_t tiles = a.T * p.G / L::rows + a.B;                         // numbers of tiles
   p.parts = parts;
   p.chunk = p.parts == 1 ? 0x7FFFFFFF / L::step : (int)((o.longest + p.parts - 1) / p.parts);
   p.o = (float*)ws;

@@ -223,3 +223,15 @@ def test_nothing_to_do(fk):
         got, lse = fk.fk_prompt_attn(q, none, none.clone(), torch.zeros((1, width), **i32),
                                      torch.full((1,), 5, **i32), torch.tensor([0, 5], **i32), return_lse=True)
         assert (got == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("dims", [(4, 2, 64), (3, 1, 33)], ids=["d64", "d33"])
+def test_thousands_of_requests(fk, dims):
+    """More requests than one or two rounds of the search for a block's request take, most of them
+    with nothing new."""
+    rng = np.random.default_rng(9)
+    for n in (65, 4097, 9000):
+        reqs = [(int(a), int(b)) for a, b in zip(rng.integers(0, 4, n), rng.integers(-12, 3, n).clip(0))]
+        reqs[n // 2], reqs[-1], reqs[0] = (40, 90), (3, 0), (0, 2)
+        args, want = _case((*dims, 8, reqs, None, 0.0, "plain"), "f16", n)
+        _check(_call(fk, args, "f16"), want, "f16", dims[2], 0.0, f"{n} requests")
