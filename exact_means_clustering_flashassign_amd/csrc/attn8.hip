@@ -122,6 +122,10 @@ hipError_t run_any(const AttnArgs8& a, int64_t most, void* ws, hipStream_t s) {
 //   * probabilities times scales have no bound, so they and the values are bf16 whatever the
 //     queries are, as the sum of two numbers, or three for fp32. fp32 queries are
 //     the sum of three bf16 numbers (24 bits); products of those with codes are exact.
+// Bound by bytes where requests are long: 2.28 GB of codes and scales (32 requests of up to 65536
+// keys, 8 heads of 128) in 397 us, 5.75 TB/s; the conversions' vector instructions keep it from
+// the 6.6 that rows of 192 and 256 reach. Short requests are bound by the launch and
+// the chain of dependent loads (lengths, table, scales, codes): one of 2048 keys takes 17 us.
 template <int DT, int DP_> struct Shape8 {
   static constexpr int DP = DP_, keys = 64, tiles = 4;      // keys per wave and step, 16-key tiles
   static constexpr int nc = DP / 64;                        // 16-byte key loads per row and lane

@@ -18,7 +18,7 @@ __global__ __launch_bounds__(kWaves * 64) void prompt_any_kernel(PromptArgs a) {
 
 template <int DT> hipError_t run_any(const PromptArgs& a, hipStream_t s) {
   const int64_t D = a.cache.dim, blocks = (a.T * a.Hq + kWaves - 1) / kWaves;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (blocks > 0xFFFFFF) return hipErrorInvalidConfiguration;        // (fewer than 2^32 threads)
   const auto kernel = D <= 64    ? prompt_any_kernel<DT, 1>
                       : D <= 128 ? prompt_any_kernel<DT, 2>
                       : D <= 256 ? prompt_any_kernel<DT, 4>

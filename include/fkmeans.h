@@ -246,11 +246,13 @@ size_t fk_workspace_size_host(fk_dtype_t dt, int64_t B, int64_t chunk, int64_t d
  * Paged key-value cache beside the clustering.
  * The pages name sparse-attention routing and KV-cache compression as what
  * clusters of keys are for ([hysenlabs] introduction, [paixiang] use cases,
- * [iaemfoco] applications). The three calls below are the steps around the
+ * [iaemfoco] applications). The calls below are the steps around the
  * clustering of a layer's keys: fk_page_tables says where a step's tokens go,
- * fk_qk_norm_rope makes their queries and keys and stores keys and values, and
- * fk_paged_attn attends over what is stored, tokens as well as cluster centres
- * (a centre that stands for n keys carries the bias log n). They run forward
+ * fk_qk_norm_rope makes their queries and keys and stores keys and values,
+ * fk_prompt_attn attends over what is stored for a step's prompts and
+ * fk_paged_attn for single tokens, over tokens as well as cluster centres
+ * (a centre that stands for n keys carries the bias log n). fk_kv_store8,
+ * fk_kv_load8 and fk_paged_attn8 do so for a cache in 8 bits. All run forward
  * only, as every call of this library.
  *
  * A cache holds `pages` pages of `page` tokens, and in each token `heads` rows
@@ -376,16 +378,19 @@ size_t fk_workspace_size_attn(fk_dtype_t dt, int64_t B, int64_t Hq, int64_t Hkv,
  * Nothing a key holds reaches the rows that do not see it, NaN included.
  *   q (T,Hq,D) dt in, q_stride: elements between tokens and between heads.
  *   table (B,width), lens (B) as in fk_paged_attn; cu_tokens (B+1) int32 in,
- *             not decreasing, from 0 on. Rows of q that no request has are not
- *             read, and their rows of out and lse stay as they were.
+ *             from 0 on, not decreasing, at most T. Rows of q that no request has
+ *             are not read, and their rows of out and lse stay as they were.
  *   max_len: no length is above it (0: not known); it only chooses how the work is split.
  *   out (T,Hq,D) dt out; lse (T,Hq) fp32 out, may be null.
  *   ws: fk_workspace_size_prompt(dt, T, B, Hq, Hkv, D) bytes, 256-byte aligned.
  * Scores, softmax statistics and sums are fp32; with 16-bit caches each
  * probability is rounded to dt before its product with the value, and the result
  * is rounded once. out, lse and ws may not overlap each other or an input.
- * D <= 1024 (FK_ERR_UNSUPPORTED above). The same arguments give the same bits on
- * every run; other requests around one, or another max_len, may change its last bits.
+ * D <= 1024, and T Hq below 2^26 where rows are not on the matrix cores, 2^30 where
+ * they are (FK_ERR_UNSUPPORTED above). The same arguments give the same bits on every
+ * run; other requests around one, or another max_len, may change its last bits.
+ * Rows of at most 256 elements that start at multiples of 16 bytes and hold whole
+ * 16-byte units, in q and out as well, run on the matrix cores.
  */
 fk_status_t fk_prompt_attn(const void* q, const int64_t q_stride[2], fk_dtype_t dt, int64_t T,
                            int64_t B, int64_t Hq, const fk_kv_cache_t* cache,
@@ -402,6 +407,7 @@ size_t fk_workspace_size_prompt(fk_dtype_t dt, int64_t T, int64_t B, int64_t Hq,
  * The cache in 8 bits: keys and values as e4m3 codes (OCP FP8: 4 exponent and 3
  * fraction bits, largest 448, no infinity), with one fp32 scale per slot and head
  * for keys and one for values; a code c of a row with scale s stands for s c.
+ * Scales are finite (fk_kv_store8 writes powers of two; others may be anything finite).
  * Axes and strides as in fk_kv_cache_t, strides of codes in bytes.
  */
 typedef struct {
@@ -418,8 +424,8 @@ typedef struct {
  * Quantises keys and values of T tokens as they are written to their slots.
  * The scale of a row is the smallest power of two s >= 2^-126 with 448 s >= |x|
  * for its finite elements x (1 for a row without any but zeros); a code is x / s
- * rounded to the nearest e4m3 number, ties to even. s being a power of two, x / s is exact and that is the only
- * rounding. Infinities and NaN are stored as NaN.
+ * rounded to the nearest e4m3 number, ties to even. s being a power of two, x / s is
+ * exact and that is the only rounding. Infinities and NaN are stored as NaN.
  *   k, v (T,heads,dim) dt in; *_stride: elements between tokens and between heads.
  *   slots (T) int32 in: as in fk_qk_norm_rope (a key_bias, where the cache has
  *             one, becomes 0; slots outside the cache are skipped, the others have to differ).
