@@ -667,15 +667,12 @@ def fk_paged_attn(q, k_cache, v_cache, table, lens, scale: Optional[float] = Non
     return out if lse is None else (out, lse)
 
 
-def _launch(where, index, fn, *args):
-    """Calls fn on device `index`, made the current one for the call if it is not."""
+def _launch(index, fn, *args):
+    """Status of fn, called with device `index` as the current one."""
     if _tc.device() == index:
-        st = fn(*args)
-    else:
-        with _tc.on_device(index):
-            st = fn(*args)
-    if st:
-        _check(st, where)
+        return fn(*args)
+    with _tc.on_device(index):
+        return fn(*args)
 
 
 def _attn_given(tc, q, need, out, lse, ws, inputs, index):
@@ -741,7 +738,7 @@ def fk_prompt_attn(q, k_cache, v_cache, table, lens, cu_tokens, scale: Optional[
             (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("key_bias", key_bias),
              ("table", table), ("lens", lens), ("cu_tokens", cu_tokens)), index)
     if p_out is None:
-        out = tc.empty((T, Hq, D), dtype=dt, device=q.device)
+        out = tc.empty_like(q) if q.is_contiguous() else tc.empty((T, Hq, D), dtype=dt, device=q.device)
         p_out = out.data_ptr()
     if p_lse is None and return_lse:
         lse = tc.empty((T, Hq), dtype=tc.f32, device=q.device)
@@ -749,47 +746,40 @@ def fk_prompt_attn(q, k_cache, v_cache, table, lens, cu_tokens, scale: Optional[
     if p_ws is None:
         ws = tc.empty(need, dtype=tc.u8, device=q.device)
         p_ws = ws.data_ptr()
-    _launch("fk_prompt_attn", index, _lib.fk_prompt_attn, q.data_ptr(), _pack2(sq[0], sq[1]), code,
-            T, B, Hq, cache, table.data_ptr(), st2[0] if B > 1 else width, width, p_lens, p_cu,
-            max_len, D ** -0.5 if scale is None else scale, softcap, p_out, p_lse, p_ws, need,
-            tc.stream(index))
+    st = _launch(index, _lib.fk_prompt_attn, q.data_ptr(), _pack2(sq[0], sq[1]), code, T, B, Hq,
+                 cache, table.data_ptr(), st2[0] if B > 1 else width, width, p_lens, p_cu, max_len,
+                 D ** -0.5 if scale is None else scale, softcap, p_out, p_lse, p_ws, need,
+                 tc.stream(index))
+    if st:
+        _check(st, "fk_prompt_attn")
     return out if lse is None else (out, lse)
 
 
 def _numbers(t, name, shape, index):
     """Checks of fp32 numbers per slot and head, in any order of memory; address and strides."""
     if t.shape != shape or t.dtype is not _tc.f32 or t.get_device() != index or t.requires_grad:
-        raise ValueError(f"{name} must be float32 of shape {tuple(shape)} on cuda:{index} without "
+        raise ValueError(f"{name} must be float32 of shape {shape} on cuda:{index} without "
                          f"grad, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr(), t.stride()
 
 
 def _kv_cache8(k_cache, v_cache, k_scale, v_scale, key_bias, heads, dim, index):
     """fk_kv_cache8_t (as bytes) of e4m3 tensors (pages, page, heads, dim) and fp32 scales
-    (pages, page, heads), and the shape."""
+    (pages, page, heads); heads and dim."""
     sk = _rows(k_cache, "k_cache", _tc.e4m3, 4, index)
     sv = _rows(v_cache, "v_cache", _tc.e4m3, 4, index)
-    shape = k_cache.shape
-    if v_cache.shape != shape or (dim and shape[3] != dim) or (heads and shape[2] != heads):
+    pages, page, h, d = shape = k_cache.shape
+    if v_cache.shape != shape or (dim and d != dim) or (heads and h != heads):
         raise ValueError(f"k_cache and v_cache must have shape (pages, page, {heads or 'heads'}, "
                          f"{dim or 'dim'}), got {tuple(shape)} and {tuple(v_cache.shape)}")
-    pk, ssk = _numbers(k_scale, "k_scale", shape[:3], index)
-    pv, ssv = _numbers(v_scale, "v_scale", shape[:3], index)
-    pb, sb = (0, (0, 0, 0)) if key_bias is None else \
-        _numbers(key_bias, "key_bias", shape[:3], index)
-    return _pack_cache8(k_cache.data_ptr(), v_cache.data_ptr(), pk, pv, pb, *shape, *sk[:3],
-                        *sv[:3], *ssk, *ssv, *sb), shape
-
-
-def _extent(t, stride):
-    """Address of a tensor's first element and of the byte past its last."""
-    p = t.data_ptr()
-    if not t.numel():
-        return p, p
-    last = 1
-    for n, k in zip(t.shape, stride):
-        last += (n - 1) * k
-    return p, p + last * t.element_size()
+    slots = (pages, page, h)
+    pk, ssk = _numbers(k_scale, "k_scale", slots, index)
+    pv, ssv = _numbers(v_scale, "v_scale", slots, index)
+    pb, sb = (0, (0, 0, 0)) if key_bias is None else _numbers(key_bias, "key_bias", slots, index)
+    k0, k1, k2, _ = sk
+    v0, v1, v2, _ = sv
+    return _pack_cache8(k_cache.data_ptr(), v_cache.data_ptr(), pk, pv, pb, pages, page, h, d,
+                        k0, k1, k2, v0, v1, v2, *ssk, *ssv, *sb), h, d
 
 
 def fk_kv_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, key_bias=None) -> None:
@@ -810,23 +800,33 @@ def fk_kv_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, key_bias=None)
         raise ValueError(f"v must have k's shape {tuple(shape)}, got {tuple(v.shape)}")
     T, H, D = shape
     p_slots = _on(slots, "slots", tc.i32, (T,), index)
-    cache, held = _kv_cache8(k_cache, v_cache, k_scale, v_scale, key_bias, H, D, index)
-    if T and held.numel():
-        parts = [("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale)]
-        if key_bias is not None:
-            parts.append(("key_bias", key_bias))
-        k0, k1 = _extent(k, sk)
-        v0, v1 = _extent(v, sv)
-        p_end, at = p_slots + 4 * T, set()
-        for name, t in parts:
-            a, b = _extent(t, t.stride())
-            at.add(a)
-            if k0 < b and a < k1 or v0 < b and a < v1 or p_slots < b and a < p_end:
-                raise ValueError(f"{name} overlaps k, v or slots, which the call reads")
-        if len(at) < len(parts):
-            raise ValueError("keys and values, their scales and biases need tensors of their own")
-    _launch("fk_kv_store8", index, _lib.fk_kv_store8, k.data_ptr(), _pack2(sk[0], sk[1]),
-            v.data_ptr(), _pack2(sv[0], sv[1]), code, T, p_slots, cache, tc.stream(index))
+    cache, _, _ = _kv_cache8(k_cache, v_cache, k_scale, v_scale, key_bias, H, D, index)
+    pages, page = k_cache.shape[:2]
+    if T and pages:
+        # every tensor from its first to its last byte
+        t1, p1, q1, h1, e = T - 1, pages - 1, page - 1, H - 1, k.element_size()
+        a, (s0, s1, _) = k.data_ptr(), sk
+        b, (u0, u1, _) = v.data_ptr(), sv
+        ins = ((a, a + (t1 * s0 + h1 * s1 + D) * e), (b, b + (t1 * u0 + h1 * u1 + D) * e),
+               (p_slots, p_slots + 4 * T))
+        at = set()
+        for name, t, d, size in (("k_cache", k_cache, D, 1), ("v_cache", v_cache, D, 1),
+                                 ("k_scale", k_scale, 1, 4), ("v_scale", v_scale, 1, 4),
+                                 ("key_bias", key_bias, 1, 4)):
+            if t is None:
+                continue
+            s, lo = t.stride(), t.data_ptr()
+            hi = lo + (p1 * s[0] + q1 * s[1] + h1 * s[2] + d) * size
+            for a, b in ins:
+                if a < hi and lo < b:
+                    raise ValueError(f"{name} overlaps k, v or slots, which the call reads")
+            if lo in at:
+                raise ValueError("keys and values, their scales and biases need tensors of their own")
+            at.add(lo)
+    st = _launch(index, _lib.fk_kv_store8, k.data_ptr(), _pack2(sk[0], sk[1]), v.data_ptr(),
+                 _pack2(sv[0], sv[1]), code, T, p_slots, cache, tc.stream(index))
+    if st:
+        _check(st, "fk_kv_store8")
 
 
 def fk_kv_load8(slots, k_cache, v_cache, k_scale, v_scale, dtype, k_out=None, v_out=None):
@@ -840,14 +840,14 @@ def fk_kv_load8(slots, k_cache, v_cache, k_scale, v_scale, dtype, k_out=None, v_
         code = dtype_code(dtype)         # says what is supported
     T = slots.numel()
     p_slots = _on(slots, "slots", tc.i32, (T,), index)
-    cache, (_, _, H, D) = _kv_cache8(k_cache, v_cache, k_scale, v_scale, None, 0, 0, index)
+    cache, H, D = _kv_cache8(k_cache, v_cache, k_scale, v_scale, None, 0, 0, index)
     shape, given = (T, H, D), []
     if k_out is None:
         k_out = tc.empty(shape, dtype=dtype, device=slots.device)
     else:
         given.append(("k_out", _on(k_out, "k_out", dtype, shape, index), k_out))
     if v_out is None:
-        v_out = tc.empty(shape, dtype=dtype, device=slots.device)
+        v_out = tc.empty_like(k_out)             # (k_out is contiguous)
     else:
         given.append(("v_out", _on(v_out, "v_out", dtype, shape, index), v_out))
     if given:
@@ -855,8 +855,10 @@ def fk_kv_load8(slots, k_cache, v_cache, k_scale, v_scale, dtype, k_out=None, v_
                [_span(n, t, t.stride(), t.element_size()) for n, t in
                 (("slots", slots), ("k_cache", k_cache), ("v_cache", v_cache),
                  ("k_scale", k_scale), ("v_scale", v_scale))])
-    _launch("fk_kv_load8", index, _lib.fk_kv_load8, cache, p_slots, code, T, k_out.data_ptr(),
-            v_out.data_ptr(), tc.stream(index))
+    st = _launch(index, _lib.fk_kv_load8, cache, p_slots, code, T, k_out.data_ptr(),
+                 v_out.data_ptr(), tc.stream(index))
+    if st:
+        _check(st, "fk_kv_load8")
     return k_out, v_out
 
 
@@ -882,13 +884,13 @@ def fk_paged_attn8(q, k_cache, v_cache, k_scale, v_scale, table, lens,
         code = dtype_code(dt)            # says what is supported
     sq = _rows(q, "q", dt, 3, index)
     B, Hq, D = q.shape
-    cache, shape = _kv_cache8(k_cache, v_cache, k_scale, v_scale, key_bias, 0, D, index)
+    cache, heads, _ = _kv_cache8(k_cache, v_cache, k_scale, v_scale, key_bias, 0, D, index)
     st2 = _rows(table, "table", tc.i32, 2, index)
     rows, width = table.shape
     if rows != B:
         raise ValueError(f"table must have {B} rows, got {tuple(table.shape)}")
     p_lens = _on(lens, "lens", tc.i32, (B,), index)
-    need = _attn8_ws(code, B, Hq, shape[2], D) or _no_heads(q, shape[2])
+    need = _attn8_ws(code, B, Hq, heads, D) or _no_heads(q, heads)
     p_out = p_lse = p_ws = None
     if out is not None or lse is not None or ws is not None:
         in_place = out is not None and out.data_ptr() == q.data_ptr() and q.is_contiguous()
@@ -898,7 +900,7 @@ def fk_paged_attn8(q, k_cache, v_cache, k_scale, v_scale, table, lens,
              ("k_scale", k_scale), ("v_scale", v_scale), ("key_bias", key_bias), ("table", table),
              ("lens", lens)), index)
     if p_out is None:
-        out = tc.empty((B, Hq, D), dtype=dt, device=q.device)
+        out = tc.empty_like(q) if q.is_contiguous() else tc.empty((B, Hq, D), dtype=dt, device=q.device)
         p_out = out.data_ptr()
     if p_lse is None and return_lse:
         lse = tc.empty((B, Hq), dtype=tc.f32, device=q.device)
@@ -906,10 +908,12 @@ def fk_paged_attn8(q, k_cache, v_cache, k_scale, v_scale, table, lens,
     if p_ws is None:
         ws = tc.empty(need, dtype=tc.u8, device=q.device)
         p_ws = ws.data_ptr()
-    _launch("fk_paged_attn8", index, _lib.fk_paged_attn8, q.data_ptr(), _pack2(sq[0], sq[1]), code,
-            B, Hq, cache, table.data_ptr(), st2[0] if B > 1 else width, width, p_lens, max_len,
-            D ** -0.5 if scale is None else scale, softcap, p_out, p_lse, p_ws, need,
-            tc.stream(index))
+    st = _launch(index, _lib.fk_paged_attn8, q.data_ptr(), _pack2(sq[0], sq[1]), code, B, Hq,
+                 cache, table.data_ptr(), st2[0] if B > 1 else width, width, p_lens, max_len,
+                 D ** -0.5 if scale is None else scale, softcap, p_out, p_lse, p_ws, need,
+                 tc.stream(index))
+    if st:
+        _check(st, "fk_paged_attn8")
     return out if lse is None else (out, lse)
 
 
