@@ -204,32 +204,56 @@ __device__ __forceinline__ uint2 read_transposed(lptr8c at) {
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)at));
 }
 
-// The tile of a block. Request b's tiles have the numbers floor(cu_tokens[b] G / rows) + b on: they
-// are never more than there are numbers up to the next request's, so that a tile's request is
-// found by a search (64 requests a round) instead of sums over all before it; a number
-// left over is a block without work. The last number comes first: the longest rows of a
-// prompt are not what the chip waits for at the end.
+// The tile of a block, from the last request's last tile on: the longest rows of a prompt come
+// first and the chip does not wait for one at the end.
 struct Where {
   int64_t b;          // request, -1: none
   int tile;           // tile of its rows
   int cu0, cu1, len;  // its tokens and keys
 };
-template <int ROWS> __device__ __forceinline__ Where find_tile(const PromptArgs& a, int G, uint32_t order) {
+constexpr Where kNowhere = {-1, 0, 0, 0, 0};
+
+// Of up to 64 requests: a lane counts one's tiles.
+template <int ROWS> __device__ __forceinline__ Where count_tiles(const PromptArgs& a, int G, uint32_t order) {
+  const int lane = threadIdx.x & 63, b = max((int)a.B - 1 - lane, 0);
+  const int cu0 = a.cu[b], cu1 = a.cu[b + 1], len = a.lens[b];
+  const int64_t n = (int64_t)cu1 - cu0;
+  const uint32_t mine = lane < a.B && n > 0 ? (uint32_t)((n * G + ROWS - 1) / ROWS) : 0;
+  uint32_t incl = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t o = __shfl_up(incl, off, 64);
+    if (lane >= off) incl += o;
+  }
+  const int at = __popcll(__ballot(incl <= order));
+  if (at == 64) return kNowhere;
+  const uint32_t end = __builtin_amdgcn_readlane(incl, at);
+  return {a.B - 1 - at, (int)(end - 1 - order), (int)__builtin_amdgcn_readlane(cu0, at),
+          (int)__builtin_amdgcn_readlane(cu1, at), (int)__builtin_amdgcn_readlane(len, at)};
+}
+
+// Of more requests the tile is searched for, 64 ways a round: request b's tiles have the numbers
+// floor(cu_tokens[b] G / ROWS) + b on, never more than there are up to the next request's. Numbers
+// left over are blocks without work among the others, and as the chip hands blocks to its
+// engines in turn, whatever they have left to do, few requests are better counted. (64
+// requests of one token over 8192 keys: 234 us counted, 254 searched; 256 requests
+// counted in four rounds take 1 to 3% longer, 1024 of 16 tokens 372 us and searched 291.)
+template <int ROWS> __device__ __forceinline__ Where search_tile(const PromptArgs& a, int G, uint32_t order) {
   const int lane = threadIdx.x & 63;
   const auto first = [&](int64_t b, int cu) { return ((int64_t)cu * G) / ROWS + b; };
   const int64_t number = first(a.B, max(a.cu[a.B], 0)) - 1 - order;
-  if (number < 0) return {-1, 0, 0, 0, 0};
+  if (number < 0) return kNowhere;
   int64_t lo = 0, hi = a.B;
   for (;;) {
     const int64_t span = (hi - lo + 63) / 64, b = lo + lane * span, at = min(b, hi - 1);
     const int cu0 = max(a.cu[at], 0), cu1 = a.cu[at + 1], len = a.lens[at];
     const int before = __popcll(__ballot(b < hi && first(at, cu0) <= number));
-    if (before == 0) return {-1, 0, 0, 0, 0};
+    if (before == 0) return kNowhere;
     lo += (before - 1) * span;
     if (span == 1) {
       const int c0 = __builtin_amdgcn_readlane(cu0, before - 1), c1 = __builtin_amdgcn_readlane(cu1, before - 1);
       const int64_t tile = number - first(lo, c0);
-      if (tile * ROWS >= ((int64_t)c1 - c0) * G) return {-1, 0, 0, 0, 0};
+      if (tile * ROWS >= ((int64_t)c1 - c0) * G) return kNowhere;
       return {lo, (int)tile, c0, c1, (int)__builtin_amdgcn_readlane(len, before - 1)};
     }
     hi = min(lo + span, hi);
@@ -283,7 +307,8 @@ template <int N, class F> __device__ __forceinline__ void each(const F& f) {
 
 struct PromptPlan {
   int heads, G, parts, chunk;     // cache heads, query heads of each, parts of a row's keys, steps of a part
-  FastDiv page, by_heads, by_parts, by_G;
+  FastDiv page, by_heads, by_tiles, by_G;
+  uint32_t turn, last;        // of a head's blocks: the first that comes in turned order, and the last
   float* o;                       // (parts, T, Hq, D) partial sums
   float* ml;                      // (parts, T, Hq, 2) their maximum and sum
 };
@@ -308,8 +333,12 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   const int D = (int)c.dim;
 
   const uint32_t rest = div_by(blockIdx.x, p.by_heads), hk = blockIdx.x - rest * p.heads;
-  const uint32_t order = div_by(rest, p.by_parts), part = rest - order * p.parts;
-  const Where at = find_tile<L::rows>(a, p.G, order);
+  // Part after part, a part's tiles longest first: the chip hands blocks to its engines in turn,
+  // so long and short ones that alternate would leave half of it idle (2048 tokens, fp32, cut
+  // in two: 575 us tile after tile, 416 this way).
+  const uint32_t at_order = rest < p.turn ? rest : p.last - (rest - p.turn);
+  const uint32_t part = div_by(at_order, p.by_tiles), order = at_order - part * p.by_tiles.d;
+  const Where at = a.B <= 64 ? count_tiles<L::rows>(a, p.G, order) : search_tile<L::rows>(a, p.G, order);
   if (at.b < 0) return;
   const int64_t b = uniform(at.b);
   const int64_t cu0 = at.cu0, cu1 = at.cu1, len = at.len;
@@ -863,49 +892,58 @@ __global__ __launch_bounds__(kWaves * 64) void prompt_join_kernel(PromptArgs a, 
   if (a.lse && lane == 0) a.lse[r] = l == 0.f ? -INFINITY : m + (logf(l) - prob_shift<DT> * kLn2);
 }
 
-// Parts that a row's keys may be cut into: two rounds of blocks over the chip at most.
+// Parts that a row's keys may be cut into: four blocks a CU at most. (Two of them keep the
+// workspace half as large, and 4 requests of 250 to 999 tokens behind 1056 centres, fp32, take 117 us
+// instead of 106, 1024 tokens of 64 elements 102 instead of 94.)
 int64_t most_parts(int64_t T, int64_t G, int64_t heads, int64_t rows) {
   const int64_t units = (T * G + rows - 1) / rows * heads;
-  const int64_t n = 2 * kMaxCus / (units < 1 ? 1 : units);
+  const int64_t n = 4 * kMaxCus / (units < 1 ? 1 : units);
   return n < 1 ? 1 : (n > 64 ? 64 : n);
 }
 
-// What is known of a call without its lengths: tiles of so many rows at least, steps of a row at
-// most and in the mean (all keys but half the tokens).
+// What is known of a call without its lengths: tiles of so many rows at least, and the steps of a
+// row, from the fewest to the most (all keys but the tokens behind it).
 struct Outline {
   int64_t tiles, longest;
-  double mean;
+  double fewest, mean;
 };
 inline Outline outline(const PromptArgs& a, int64_t rows, int64_t step) {
   const int64_t G = a.Hq / a.cache.heads, full = (a.T * G + rows - 1) / rows, most = longest(a);
-  const double each = (double)(a.T / a.B < most ? a.T / a.B : most);
-  return {full > a.B ? full : a.B, (most + step - 1) / step, most <= 0 ? 0. : (most - 0.5 * each) / (double)step};
+  const int64_t each = a.T / a.B < most ? a.T / a.B : most, longest = (most + step - 1) / step;
+  const double fewest = (double)(most - each) / (double)step;
+  return {full > a.B ? full : a.B, longest, fewest, 0.5 * (longest + fewest)};
 }
 
 // Microseconds of a call whose keys are cut into `parts`, from what was measured: products at
-// 1000 TFLOP/s over the chip (16 bits; 700 for rows of 64 and less, 150 for fp32), 5% less for two
+// 1000 TFLOP/s over the chip (16 bits; 700 for rows of 64 and less, 103 for fp32), 5% less for two
 // blocks a CU; 15 us of a block before and after its steps, 3 more for a partial result; 6 us and
 // 4 TB/s to join them. Blocks are taken longest first. A block of 4 waves alone on its
-// CU is 1.6 times as fast as next to another. Rows that see unlike numbers of keys leave
-// CUs free for each other; where all are alike, a last round is as long as any.
+// CU is 1.6 times as fast as next to another, in fp32 1.95 times. Rows that see unlike numbers
+// of keys leave CUs free for each other; where all are alike, a last round is as long as any.
 inline double estimate(int dt, int DC, int W, int step, const PromptArgs& a, const Outline& o, int64_t parts) {
   const double cus = device_cus(), slots = cus * tile_blocks(dt, DC, W), rows = W * 32;
-  const double rate = dt == FK_F32 ? 150e6 : DC <= 64 ? 700e6 : 1000e6;
+  const double rate = dt == FK_F32 ? 103e6 : DC <= 64 ? 700e6 : 1000e6;
   const double together = (slots > cus ? 1.05 : 1.) * 4. * rows * step * DC / (rate / slots);
-  const double blocks = (double)o.tiles * a.cache.heads * parts;
-  const double alone = slots > cus ? together / 1.6 : together;
-  const double fixed = parts > 1 ? 18. : 15., alike = o.longest > 0 ? 2. * (o.mean / o.longest - 0.5) : 1.;
-  const double last = (double)((o.longest + parts - 1) / parts);
+  const double alone = slots > cus ? together / (dt == FK_F32 ? 1.95 : 1.6) : together;
+  const double units = (double)o.tiles * a.cache.heads, fixed = parts > 1 ? 18. : 15.;
+  const int64_t chunk = (o.longest + parts - 1) / parts;
+  double blocks = 0.;                                  // with work: rows with few keys have few parts
+  for (int64_t p = 0; p < parts && p * chunk < o.longest; ++p) {
+    const double from = p * chunk > o.fewest ? (double)(p * chunk) : o.fewest;
+    blocks += units * (p * chunk <= o.fewest ? 1. : (o.longest - from) / (o.longest - o.fewest));
+  }
   double us;
   if (blocks <= slots) {
-    // next to another block until that ends
-    const double both = blocks > cus ? 0.5 * (last + o.mean / parts) * together : 0.;
-    us = (last * alone > both ? last * alone : both) + fixed;
+    // next to another block until that ends, a long one next to a short one
+    const double first = chunk * alone + (parts == 1 && blocks > cus ? o.fewest * (together - alone) : 0.);
+    const double mean = parts == 1 ? o.fewest : units * o.mean / blocks;         // beside the longest
+    const double both = blocks > cus ? 0.5 * (chunk + mean) * together : 0.;
+    us = (first > both ? first : both) + fixed;
   } else {
-    const double one = last * together + fixed, all = blocks * (o.mean / parts * together + fixed) / slots;
+    const double alike = o.longest > 0 ? 2. * (o.mean / o.longest - 0.5) : 1.;
+    const double one = chunk * together + fixed, all = (units * o.mean * together + blocks * fixed) / slots;
     const double uneven = (all > one ? all : one) + 0.2 * one, even = ceil(blocks / slots) * one;
-    const double u = alike < 0. ? 0. : (alike > 1. ? 1. : alike);
-    us = (1. - u) * uneven + u * even;
+    us = (1. - alike) * uneven + alike * even;
   }
   if (parts > 1) us += 6. + (double)(a.T * a.Hq) * parts * (a.cache.dim + 2) * 8. / 4e6;
   return us;
@@ -933,16 +971,24 @@ template <int DT, int DC, int W> hipError_t run_tiles(const PromptArgs& a, int p
   p.heads = (int)a.cache.heads;
   p.G = (int)(a.Hq / a.cache.heads);
   const Outline o = outline(a, L::rows, L::step);
-  const int64_t tiles = a.T * p.G / L::rows + a.B;                         // numbers of tiles
+  const int64_t tiles = a.B <= 64 ? (a.T * p.G + L::rows - 1) / L::rows + a.B - 1         // at most so many
+                                  : a.T * p.G / L::rows + a.B;                            // numbers
   p.parts = parts;
   p.chunk = p.parts == 1 ? 0x7FFFFFFF / L::step : (int)((o.longest + p.parts - 1) / p.parts);
   p.o = (float*)ws;
   p.ml = p.o + (int64_t)p.parts * a.T * a.Hq * a.cache.dim;
   p.page = fast_div((uint32_t)a.cache.page);
   p.by_heads = fast_div((uint32_t)p.heads);
-  p.by_parts = fast_div((uint32_t)p.parts);
+  p.by_tiles = fast_div((uint32_t)tiles);
   p.by_G = fast_div((uint32_t)p.G);
   const int64_t blocks = tiles * p.heads * p.parts;
+  // Where every block finds room at once, two to a CU, the second half comes in turned order: the
+  // longest share a CU with the shortest. (2048 tokens, bf16: 70 us in one order, 61; fp32 rows of
+  // 64: 253 and 205.)
+  const int64_t each = device_cus() / p.heads;
+  const bool pairs = tile_blocks(DT, DC, W) == 2 && p.parts == 1 && blocks <= 2 * device_cus() + p.heads * a.B;
+  p.last = (uint32_t)(tiles * p.parts - 1);
+  p.turn = pairs ? (uint32_t)each : 0xFFFFFFFFu;
   if (blocks > 0x7FFFFF || a.T * p.G > 0x7FFFFFFF - 512) return hipErrorInvalidConfiguration;
   auto kernel = prompt_mfma_kernel<DT, DC, W, kCapScore>;
   if constexpr (DT != FK_F32) {
@@ -958,8 +1004,8 @@ template <int DT, int DC, int W> hipError_t run_tiles(const PromptArgs& a, int p
 }
 
 // Tiles of 256 rows or of 128, of which two blocks share a CU. (16-bit, 32 heads of 128 on 8, 4096
-// tokens: 182 us, 197 with 128 rows; 16384: 2340 and 2510; 512: 30 and 24; 8192 tokens of 8
-// heads on 8: 278 and 212; 64 requests of one token over 8192 keys: 341 and 238.)
+// tokens: 163 us, 178 with 128 rows; 16384: 2340 and 2510; 512: 29 and 23; 8192 tokens of 8
+// heads on 8: 236 and 193; 64 requests of one token over 8192 keys: 341 and 215.)
 template <int DT, int DC> hipError_t run_mfma(const PromptArgs& a, void* ws, hipStream_t s) {
   const Best four = best_parts(DT, DC, 4, Tile<DT, DC, 4>::step, a);
   if constexpr (!only_four(DT, DC)) {
