@@ -6,25 +6,219 @@
 namespace fk {
 namespace {
 
-template <int DT, int EPL>
-__global__ __launch_bounds__(kWaves * 64) void prompt_any_kernel(PromptArgs a) {
-  const int64_t r = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  const int64_t t = r / a.Hq, b = t < a.T ? request_of(a, t) : -1;
-  if (b < 0) return;
-  float m, l, o[EPL];
-  row_sums<DT, EPL>(a, b, t, r - t * a.Hq, 0, seen_by(a, b, t), m, l, o);
-  put_row<DT, EPL>(a, r, m, l, o);
+// Any size, stride and alignment. The rows of a request are laid out as for the matrix-core kernel
+// (row r is head r % G of token r / G); a block takes R of one cache head, a wave every
+// fourth step of 64 keys. For scores a lane has a key: 64 elements of every key go to LDS, an
+// element a lane as they lie in memory, and are read back a key a lane, next to the R queries'
+// elements. For sums a lane has every 64th element, and probabilities come back from LDS a key
+// at a time. So a key or value is loaded once for R rows, and nothing is summed over lanes but a
+// step's maxima. Bound by instructions and, with few blocks, by a step's chain of loads: 2048
+// tokens, 32 heads of 90 on 8, fp16, 1.38 ms (a row a wave, each score summed over the lanes: 10.2 ms);
+// 1024 of 512, bf16, 6.6 and 9.3; one token over 8192 keys of 90 0.57 and 10.7; but 100 requests
+// of 1 to 40 tokens 0.18 and 0.09, where a block has few keys.
+template <int DT, int EPL, int R>
+__global__ __launch_bounds__(kWaves * 64) void prompt_any_kernel(PromptArgs a, PromptPlan p) {
+  using E = typename Val<DT>::type;
+  typedef float Row __attribute__((ext_vector_type(R)));
+  constexpr int pitch = 65;                            // of 64 elements of a key: lanes meet in no bank
+  static_assert(R * EPL <= pitch);
+  __shared__ __attribute__((aligned(16))) float queries[EPL * 64][R], probs[kWaves][64][R];
+  __shared__ float keys[kWaves][64 * pitch];           // in the end the waves' sums
+  __shared__ float tops[kWaves][R], totals[kWaves][R];
+  const fk_kv_cache_t& c = a.cache;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int D = (int)c.dim;
+
+  const uint32_t order = div_by(blockIdx.x, p.by_heads), hk = blockIdx.x - order * p.heads;
+  const Where at = a.B <= 64 ? count_tiles<R>(a, p.G, order) : search_tile<R>(a, p.G, order);
+  if (at.b < 0) return;
+  const int64_t cu0 = at.cu0, cu1 = at.cu1, len = at.len;
+  const int rows = (int)min((cu1 - cu0) * p.G - (int64_t)at.tile * R, (int64_t)R);
+  const int64_t held = min(a.width * c.page, (int64_t)0x7FFFFFFF);
+  // row r's token, query head and keys; past the last row its own again
+  const auto token = [&](int r) { return cu0 + div_by((uint32_t)(at.tile * R + min(r, rows - 1)), p.by_G); };
+  const auto head = [&](int r) {
+    const uint32_t i = at.tile * R + min(r, rows - 1);
+    return (int64_t)hk * p.G + (i - div_by(i, p.by_G) * p.G);
+  };
+  int limit[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    limit[r] = (int)max((int64_t)0, min(len - cu1 + token(r) + 1, held));
+  const int most = limit[R - 1], steps = (int)(((uint32_t)most + 63) / 64);
+
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t t = token(r);
+    const E* q = (const E*)a.q + t * a.q_stride[0] + head(r) * a.q_stride[1];
+    for (int e = threadIdx.x; e < EPL * 64; e += kWaves * 64)
+      queries[e][r] = e < D && t >= 0 && t < a.T ? Val<DT>::get(q + e) : 0.f;
+  }
+  __syncthreads();
+
+  const int32_t* table = a.table + at.b * a.ld_table;
+  // (a sum in 32 bits stands still after 2^24 terms alike: every kRun steps it joins `all`)
+  constexpr int kRun = 1 << 10;
+  Row m = -INFINITY, l = 0.f, l_all = 0.f;
+  float o[R][EPL], all[R][EPL];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) o[r][i] = all[r][i] = 0.f;
+  int el[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) el[i] = lane + 64 * i < D ? lane + 64 * i : 0;
+  for (int st = w, n = 1; st < steps; st += kWaves, ++n) {
+    const uint32_t key = (uint32_t)st * 64 + lane, pos = min(key, (uint32_t)most - 1);
+    const uint32_t pg_at = div_by(pos, p.page), tok = pos - pg_at * p.page.d;
+    const int64_t page = table[pg_at];
+    bool live = key == pos && page >= 0 && page < c.pages;
+    float bias = 0.f;
+    if (c.key_bias && live) {
+      bias = c.key_bias[page * c.bias_stride[0] + tok * c.bias_stride[1] + hk * c.bias_stride[2]];
+      live = bias != -INFINITY;
+    }
+    const uint64_t counts = __ballot(live);
+    if (counts == 0) continue;
+    const int held_here = min(64, most - st * 64);
+    // (in the place of a key that is out another one is read, and not used)
+    const int64_t ko = page * c.k_stride[0] + tok * c.k_stride[1] + hk * c.k_stride[2];
+    const int64_t vo = page * c.v_stride[0] + tok * c.v_stride[1] + hk * c.v_stride[2];
+    const int first = __builtin_ctzll(counts);
+    const auto of_lane = [](int64_t x, int i) {
+      return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)x, i) |
+                       (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), i) << 32);
+    };
+    const int64_t k_at = live ? ko : of_lane(ko, first), v_at = live ? vo : of_lane(vo, first);
+
+    Row s = 0.f;
+    float* const mine = keys[w];
+    for (int e0 = 0; e0 < D; e0 += 64) {
+      const int e = e0 + lane < D ? e0 + lane : 0;
+#pragma unroll 1
+      for (int j0 = 0; j0 < held_here; j0 += 32) {
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = Val<DT>::get((const E*)c.k + of_lane(k_at, j0 + j) + e);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) mine[(j0 + j) * pitch + lane] = x[j];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const int count = min(64, D - e0);
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) s += *(const Row*)queries[e0 + i] * mine[lane * pitch + i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    Row pr, alpha;
+    const bool whole = (uint32_t)st * 64 + 64 <= (uint32_t)limit[0];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float x = s[r] * a.scale;
+      if (a.softcap > 0.f) x = capped(x, a.softcap, 1.f / a.softcap);
+      x = live && key < (uint32_t)limit[r] ? x + bias : -INFINITY;
+      float top = x;
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+      const float mr = m[r], mn = fmaxf(mr, top);
+      alpha[r] = mr == -INFINITY ? 0.f : fast_exp2((mr - mn) * kLog2e);
+      pr[r] = x == -INFINITY ? 0.f : fast_exp2((x - mn) * kLog2e);       // NaN stays NaN
+      m[r] = mn;
+    }
+    l = l * alpha + pr;
+    l_all *= alpha;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) o[r][i] *= alpha[r], all[r][i] *= alpha[r];
+    *(Row*)probs[w][lane] = pr;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const auto sums = [&](auto tag) {
+      constexpr bool masked = !decltype(tag)::value;
+      constexpr int U = EPL <= 4 ? 8 : 2;
+#pragma unroll 1
+      for (int j0 = 0; j0 < held_here; j0 += U) {
+        float x[U][EPL];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          const E* v = (const E*)c.v + of_lane(v_at, j0 + j);
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) x[j][i] = Val<DT>::get(v + el[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          const Row y = *(const Row*)probs[w][j0 + j];
+          const bool out = !((counts >> (j0 + j)) & 1);
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) {
+            const float v = out ? 0.f : x[j][i];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              // (a value that is not finite does not reach the rows it is hidden from)
+              const float sum = fmaf(y[r], v, o[r][i]);
+              o[r][i] = !masked || (uint32_t)(st * 64u + j0 + j) < (uint32_t)limit[r] ? sum : o[r][i];
+            }
+          }
+        }
+      }
+    };
+    if (whole) sums(std::true_type());
+    else sums(std::false_type());
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (n % kRun == 0) {
+      l_all += l, l = 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) all[r][i] += o[r][i], o[r][i] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float total = wave_sum(l[r] + l_all[r]);
+    if (lane == 0) tops[w][r] = m[r], totals[w][r] = total;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) keys[w][(r * EPL + i) * 64 + lane] = o[r][i] + all[r][i];
+  }
+  __syncthreads();
+  for (int r = 0; r < rows; ++r) {
+    const int64_t t = token(r), row = t * a.Hq + head(r);
+    if (t < 0 || t >= a.T) continue;
+    float top = tops[0][r];
+    for (int i = 1; i < kWaves; ++i) top = fmaxf(top, tops[i][r]);
+    float f[kWaves], total = 0.f;
+    for (int i = 0; i < kWaves; ++i) {
+      f[i] = join_factor(tops[i][r], totals[i][r], top);
+      total += f[i] * totals[i][r];
+    }
+    const bool any = total != 0.f;       // true for NaN: it has to reach the result
+    for (int e = threadIdx.x; e < D; e += kWaves * 64) {
+      float x = 0.f;
+      for (int i = 0; i < kWaves; ++i) x += f[i] * keys[i][r * EPL * 64 + e];
+      Val<DT>::put((E*)a.out + row * D + e, any ? x / total : 0.f);
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[row] = any ? top + logf(total) : -INFINITY;
+  }
+}
+
+template <int DT, int EPL, int R> hipError_t run_any_as(const PromptArgs& a, hipStream_t s) {
+  PromptPlan p{};
+  p.heads = (int)a.cache.heads;
+  p.G = (int)(a.Hq / a.cache.heads);
+  p.page = fast_div((uint32_t)a.cache.page);
+  p.by_heads = fast_div((uint32_t)p.heads);
+  p.by_G = fast_div((uint32_t)p.G);
+  const int64_t tiles = a.B <= 64 ? (a.T * p.G + R - 1) / R + a.B - 1 : a.T * p.G / R + a.B, blocks = tiles * p.heads;
+  if (blocks > 0xFFFFFF || a.T * p.G > 0x7FFFFFFF - R) return hipErrorInvalidConfiguration;      // (fewer than 2^32 threads)
+  prompt_any_kernel<DT, EPL, R><<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, p);
+  return hipGetLastError();
 }
 
 template <int DT> hipError_t run_any(const PromptArgs& a, hipStream_t s) {
-  const int64_t D = a.cache.dim, blocks = (a.T * a.Hq + kWaves - 1) / kWaves;
-  if (blocks > 0xFFFFFF) return hipErrorInvalidConfiguration;        // (fewer than 2^32 threads)
-  const auto kernel = D <= 64    ? prompt_any_kernel<DT, 1>
-                      : D <= 128 ? prompt_any_kernel<DT, 2>
-                      : D <= 256 ? prompt_any_kernel<DT, 4>
-                                 : prompt_any_kernel<DT, 16>;
-  kernel<<<(unsigned)blocks, kWaves * 64, 0, s>>>(a);
-  return hipGetLastError();
+  const int64_t D = a.cache.dim;
+  return D <= 64    ? run_any_as<DT, 1, 8>(a, s)
+         : D <= 128 ? run_any_as<DT, 2, 8>(a, s)
+         : D <= 256 ? run_any_as<DT, 4, 8>(a, s)
+                    : run_any_as<DT, 16, 4>(a, s);
 }
 
 // Rows the matrix-core kernel can load: whole, aligned 16-byte units.
