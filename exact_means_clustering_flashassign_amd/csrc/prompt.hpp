@@ -127,7 +127,7 @@ __device__ __forceinline__ void put_row(const PromptArgs& a, int64_t row, float 
 //
 // What bounds it: with 32 rows a wave a product of 32 cycles reads 1 KB of LDS, of which a CU
 // gives four SIMDs 128 bytes a cycle, so products and reads would both fill their time at
-// the peak; before that, power: 53% of the matrix units' cycles are used at a clock of
+// the peak; before that, power: half of the matrix units' cycles are used at a clock of
 // 1.85 GHz (2.1 where the units wait more). Measured: 32768 tokens, 32 heads of 128 on 8, bf16, 8.45 to
 // 8.7 ms, 1010 to 1040 TFLOP/s (a large library product on random numbers reaches 1142 on the
 // same card); with probabilities and products in turn instead of together 9.6 ms, and
