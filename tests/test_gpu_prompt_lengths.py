@@ -204,3 +204,29 @@ def test_mean_rounding(fk, dtype):
     out = fk.fk_paged_attn8(q[:1], k8, v8, ks, vs, table, _i32([n]))
     want, *_ = oracle.prompt_attn(host_f64(q[:1], dtype), kd, vd, table.cpu().numpy(), [n], [0, 1], 1.0 / math.sqrt(D))
     assert rms(host_f64(out, dtype) - want) <= U[dtype] * rms(want)
+
+
+@pytest.mark.parametrize("dims", [(2, 1, 33), (3, 3, 130), (2, 2, 300)], ids=["d33", "d130", "d300"])
+def test_long_sums_of_any_layout(fk, dims):
+    """2^20 keys whose scores grow, in rows that the vector units take; bound as above."""
+    import torch
+    Hq, Hkv, D = dims
+    T, page, pages, width = 3, 1 << 10, 4, 1 << 10
+    n = width * page - 77
+    g = torch.Generator(device="cuda").manual_seed(D)
+    q, k, v = (torch.randn(s, device="cuda", generator=g) for s in ((T, Hq, D), (pages, page, Hkv, D + 1), (pages, page, Hkv, D + 1)))
+    k[..., 0] = torch.arange(pages, device="cuda").view(pages, 1, 1) * 3.0
+    k, v, q = k[..., :D], v[..., 1:], q * 0.25
+    table = torch.div(torch.arange(width, device="cuda") * pages, width, rounding_mode="floor").int()
+    out, lse = fk.fk_prompt_attn(q, k, v, table.view(1, width), _i32([n]), _i32([0, T]), 1.0, return_lse=True)
+    k64, v64 = (host_f64(t.contiguous(), "f32").reshape(pages * page, Hkv, D) for t in (k, v))
+    for t in range(T):
+        for h in range(Hq):
+            hk = h // (Hq // Hkv)
+            counts = np.repeat(np.bincount(table.cpu().numpy(), minlength=pages).astype(np.float64), page)
+            counts[pages * page - (width * page - n) - (T - 1 - t):] -= 1.0
+            s = k64[:, hk] @ host_f64(q[t, h], "f32")
+            w = counts * np.exp(s - s.max())
+            want, big = w @ v64[:, hk] / w.sum(), np.abs(v64).max()
+            assert np.abs(host_f64(out[t, h], "f32") - want).max() <= 2.0 ** -11 * big
+            assert abs(float(lse[t, h]) - (s.max() + np.log(w.sum()))) <= 2.0 ** -11
