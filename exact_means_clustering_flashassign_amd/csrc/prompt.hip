@@ -13,17 +13,16 @@ namespace {
 // elements. For sums a lane has every 64th element, and probabilities come back from LDS a key
 // at a time. So a key or value is loaded once for R rows, and nothing is summed over lanes but a
 // step's maxima. Bound by instructions and, with few blocks, by a step's chain of loads: 2048
-// tokens, 32 heads of 90 on 8, fp16, 1.38 ms (a row a wave, each score summed over the lanes: 10.2 ms);
-// 1024 of 512, bf16, 6.6 and 9.3; one token over 8192 keys of 90 0.57 and 10.7; but 100 requests
+// tokens, 32 heads of 90 on 8, fp16, 1.27 ms (a row a wave, each score summed over the lanes: 10.2 ms);
+// 1024 of 512, bf16, 3.5 and 9.3; one token over 8192 keys of 90 0.57 and 10.7; but 100 requests
 // of 1 to 40 tokens 0.18 and 0.09, where a block has few keys.
 template <int DT, int EPL, int R>
 __global__ __launch_bounds__(kWaves * 64) void prompt_any_kernel(PromptArgs a, PromptPlan p) {
   using E = typename Val<DT>::type;
   typedef float Row __attribute__((ext_vector_type(R)));
   constexpr int pitch = 65;                            // of 64 elements of a key: lanes meet in no bank
-  static_assert(R * EPL <= pitch);
   __shared__ __attribute__((aligned(16))) float queries[EPL * 64][R], probs[kWaves][64][R];
-  __shared__ float keys[kWaves][64 * pitch];           // in the end the waves' sums
+  __shared__ float keys[kWaves][64 * pitch];
   __shared__ float tops[kWaves][R], totals[kWaves][R];
   const fk_kv_cache_t& c = a.cache;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -110,7 +109,7 @@ __global__ __launch_bounds__(kWaves * 64) void prompt_any_kernel(PromptArgs a, P
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     Row pr, alpha;
-    const bool whole = (uint32_t)st * 64 + 64 <= (uint32_t)limit[0];
+    const bool whole = counts == ~(uint64_t)0 && (uint32_t)st * 64 + 64 <= (uint32_t)limit[0];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float x = s[r] * a.scale;
@@ -134,7 +133,7 @@ __global__ __launch_bounds__(kWaves * 64) void prompt_any_kernel(PromptArgs a, P
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     const auto sums = [&](auto tag) {
       constexpr bool masked = !decltype(tag)::value;
-      constexpr int U = EPL <= 4 ? 8 : 2;
+      constexpr int U = EPL <= 4 ? 8 : 32 / EPL;
 #pragma unroll 1
       for (int j0 = 0; j0 < held_here; j0 += U) {
         float x[U][EPL];
@@ -147,7 +146,7 @@ __global__ __launch_bounds__(kWaves * 64) void prompt_any_kernel(PromptArgs a, P
 #pragma unroll
         for (int j = 0; j < U; ++j) {
           const Row y = *(const Row*)probs[w][j0 + j];
-          const bool out = !((counts >> (j0 + j)) & 1);
+          const bool out = masked && !((counts >> (j0 + j)) & 1);
 #pragma unroll
           for (int i = 0; i < EPL; ++i) {
             const float v = out ? 0.f : x[j][i];
@@ -176,27 +175,35 @@ __global__ __launch_bounds__(kWaves * 64) void prompt_any_kernel(PromptArgs a, P
   for (int r = 0; r < R; ++r) {
     const float total = wave_sum(l[r] + l_all[r]);
     if (lane == 0) tops[w][r] = m[r], totals[w][r] = total;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) keys[w][(r * EPL + i) * 64 + lane] = o[r][i] + all[r][i];
   }
-  __syncthreads();
-  for (int r = 0; r < rows; ++r) {
-    const int64_t t = token(r), row = t * a.Hq + head(r);
-    if (t < 0 || t >= a.T) continue;
-    float top = tops[0][r];
-    for (int i = 1; i < kWaves; ++i) top = fmaxf(top, tops[i][r]);
-    float f[kWaves], total = 0.f;
-    for (int i = 0; i < kWaves; ++i) {
-      f[i] = join_factor(tops[i][r], totals[i][r], top);
-      total += f[i] * totals[i][r];
+  // the waves' sums, in the keys' place, as many elements at a time as it holds
+  constexpr int G = R * EPL <= pitch ? EPL : pitch / R;
+#pragma unroll
+  for (int i0 = 0; i0 < EPL; i0 += G) {
+    if (i0 > 0) __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = i0; i < i0 + G; ++i) keys[w][(r * G + i - i0) * 64 + lane] = o[r][i] + all[r][i];
+    __syncthreads();
+    for (int r = 0; r < rows; ++r) {
+      const int64_t t = token(r), row = t * a.Hq + head(r);
+      if (t < 0 || t >= a.T) continue;
+      float top = tops[0][r];
+      for (int k = 1; k < kWaves; ++k) top = fmaxf(top, tops[k][r]);
+      float f[kWaves], total = 0.f;
+      for (int k = 0; k < kWaves; ++k) {
+        f[k] = join_factor(tops[k][r], totals[k][r], top);
+        total += f[k] * totals[k][r];
+      }
+      const bool any = total != 0.f;     // true for NaN: it has to reach the result
+      for (int e = threadIdx.x; e < G * 64 && i0 * 64 + e < D; e += kWaves * 64) {
+        float x = 0.f;
+        for (int k = 0; k < kWaves; ++k) x += f[k] * keys[k][r * G * 64 + e];
+        Val<DT>::put((E*)a.out + row * D + i0 * 64 + e, any ? x / total : 0.f);
+      }
+      if (a.lse && i0 == 0 && threadIdx.x == 0) a.lse[row] = any ? top + logf(total) : -INFINITY;
     }
-    const bool any = total != 0.f;       // true for NaN: it has to reach the result
-    for (int e = threadIdx.x; e < D; e += kWaves * 64) {
-      float x = 0.f;
-      for (int i = 0; i < kWaves; ++i) x += f[i] * keys[i][r * EPL * 64 + e];
-      Val<DT>::put((E*)a.out + row * D + e, any ? x / total : 0.f);
-    }
-    if (a.lse && threadIdx.x == 0) a.lse[row] = any ? top + logf(total) : -INFINITY;
   }
 }
 
@@ -218,7 +225,8 @@ template <int DT> hipError_t run_any(const PromptArgs& a, hipStream_t s) {
   return D <= 64    ? run_any_as<DT, 1, 8>(a, s)
          : D <= 128 ? run_any_as<DT, 2, 8>(a, s)
          : D <= 256 ? run_any_as<DT, 4, 8>(a, s)
-                    : run_any_as<DT, 16, 4>(a, s);
+         : D <= 512 ? run_any_as<DT, 8, 8>(a, s)
+                    : run_any_as<DT, 16, 8>(a, s);
 }
 
 // Rows the matrix-core kernel can load: whole, aligned 16-byte units.
