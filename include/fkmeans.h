@@ -386,11 +386,11 @@ size_t fk_workspace_size_attn(fk_dtype_t dt, int64_t B, int64_t Hq, int64_t Hkv,
  * Scores, softmax statistics and sums are fp32; with 16-bit caches each
  * probability is rounded to dt before its product with the value, and the result
  * is rounded once. out, lse and ws may not overlap each other or an input.
- * D <= 1024, and T Hq below 2^26 where rows are not on the matrix cores, 2^30 where
- * they are (FK_ERR_UNSUPPORTED above). The same arguments give the same bits on every
- * run; other requests around one, or another max_len, may change its last bits.
- * Rows of at most 256 elements that start at multiples of 16 bytes and hold whole
- * 16-byte units, in q and out as well, run on the matrix cores.
+ * D <= 1024 (FK_ERR_UNSUPPORTED above, and where a launch would hold 2^32 threads:
+ * T Hq of 2^26 at least). The same arguments give the same bits on every run; other
+ * requests around one, or another max_len, may change its last bits. Rows of
+ * at most 256 elements that start at multiples of 16 bytes and hold whole 16-byte
+ * units, in q and out as well, are the fast ones; other fp32 rows run on the vector units.
  */
 fk_status_t fk_prompt_attn(const void* q, const int64_t q_stride[2], fk_dtype_t dt, int64_t T,
                            int64_t B, int64_t Hq, const fk_kv_cache_t* cache,
