@@ -253,7 +253,7 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
   const uint64_t kbase = (uint64_t)c.k + (uint64_t)hk * c.k_stride[2];
   const uint64_t vbase = (uint64_t)c.v + (uint64_t)hk * c.v_stride[2];
   const uint64_t zero = (uint64_t)zero_row;
-  const bool cap = EXTRA && a.softcap > 0.f;
+  const bool cap = EXTRA && a.softcap > 0.f, near = cap && DT != FK_F32 && a.softcap <= kNearCap;
   const float inv_cap = cap ? 1.f / a.softcap : 0.f;
   const bool has_bias = EXTRA && c.key_bias && c.pages > 0;
   const uint64_t bbase = (uint64_t)c.key_bias + (uint64_t)hk * c.bias_stride[2] * 4;
@@ -360,12 +360,21 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
 #pragma unroll
       for (int u = 0; u < S::tiles; ++u)
 #pragma unroll
+        for (int i = 0; i < 4; ++i) s[h][u][i] *= now.ks[16 * u + 4 * g + i];
+      const auto every = [&](auto f) {
+#pragma unroll
+        for (int u = 0; u < S::tiles; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[h][u][i] = f(s[h][u][i]);
+      };
+      if (near) every([&](float x) { return cap_16bit(x, a.softcap, inv_cap); });
+      else if (cap) every([&](float x) { return capped(x, a.softcap, inv_cap); });
+#pragma unroll
+      for (int u = 0; u < S::tiles; ++u)
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
           // -inf where a key does not count
-          const int at = 16 * u + 4 * g + i;
-          const float bias = now.bias[at];
-          float x = s[h][u][i] * now.ks[at];
-          if (cap) x = DT == FK_F32 ? capped(x, a.softcap, inv_cap) : cap_16bit(x, a.softcap, inv_cap);
+          const float bias = now.bias[16 * u + 4 * g + i], x = s[h][u][i];
           s[h][u][i] = bias == -INFINITY ? bias : (EXTRA ? x + bias : x);
           top = fmaxf(top, s[h][u][i]);
         }

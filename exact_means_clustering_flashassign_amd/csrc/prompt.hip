@@ -345,7 +345,7 @@ __global__ __launch_bounds__(kWaves * 64) void prompt_split_kernel(PromptArgs a,
     for (int i = 0; i < 16; ++i) {
       const int kk = (i & 3) + 8 * (i >> 2) + 4 * h;
       x[i] *= a.scale;
-      if (a.softcap > 0.f) x[i] = cap_16bit(x[i], a.softcap, 1.f / a.softcap);
+      if (a.softcap > 0.f) x[i] = capped(x[i], a.softcap, 1.f / a.softcap);
       x[i] += biases[w][kk];
       x[i] = ((counts >> kk) & 1) && (uint32_t)st * 32 + kk < limit ? x[i] : -INFINITY;
       top = fmaxf(top, x[i]);

@@ -313,8 +313,9 @@ struct PromptPlan {
   float* ml;                      // (parts, T, Hq, 2) their maximum and sum
 };
 
-// What a score takes part in: the scale alone; scale and bias; cap as well.
-enum { kPlainScore, kBiasScore, kCapScore };
+// What a score takes part in: the scale alone; scale and bias; cap as well, by capped() or, for 16-bit
+// types and caps of at most kNearCap, by cap_16bit().
+enum { kPlainScore, kBiasScore, kCapScore, kNearCapScore };
 
 template <int DT, int DC, int W, int SCORE>
 __global__ __launch_bounds__(W * 64, W / 4 * tile_blocks(DT, DC, W))
@@ -522,9 +523,11 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float x = s[u][j4 * 4 + j];
-          if constexpr (SCORE == kCapScore) {
+          if constexpr (SCORE == kNearCapScore) {
+            x = cap_16bit(x * a.scale, cap, inv_cap) + bb[j];
+          } else if constexpr (SCORE == kCapScore) {
             x *= a.scale;
-            if (DT != FK_F32 || cap > 0.f) x = DT == FK_F32 ? capped(x, cap, inv_cap) : cap_16bit(x, cap, inv_cap);
+            if (DT != FK_F32 || cap > 0.f) x = capped(x, cap, inv_cap);
             x += bb[j];
           } else if constexpr (EXTRA) {
             x = fmaf(x, a.scale, bb[j]);
@@ -992,7 +995,9 @@ template <int DT, int DC, int W> hipError_t run_tiles(const PromptArgs& a, int p
   if (blocks > 0x7FFFFF || a.T * p.G > 0x7FFFFFFF - 512) return hipErrorInvalidConfiguration;
   auto kernel = prompt_mfma_kernel<DT, DC, W, kCapScore>;
   if constexpr (DT != FK_F32) {
-    if (a.softcap == 0.f)
+    if (a.softcap > 0.f && a.softcap <= kNearCap)
+      kernel = prompt_mfma_kernel<DT, DC, W, kNearCapScore>;
+    else if (a.softcap == 0.f)
       kernel = a.cache.key_bias || !(a.scale > 0.f) ? prompt_mfma_kernel<DT, DC, W, kBiasScore>
                                                     : prompt_mfma_kernel<DT, DC, W, kPlainScore>;
   }

@@ -384,8 +384,8 @@ size_t fk_workspace_size_attn(fk_dtype_t dt, int64_t B, int64_t Hq, int64_t Hkv,
  *   out (T,Hq,D) dt out; lse (T,Hq) fp32 out, may be null.
  *   ws: fk_workspace_size_prompt(dt, T, B, Hq, Hkv, D) bytes, 256-byte aligned.
  * Scores, softmax statistics and sums are fp32; with 16-bit caches each
- * probability is rounded to dt before its product with the value, and the result
- * is rounded once. out, lse and ws may not overlap each other or an input.
+ * probability is rounded to dt before its product with the value, a softcap of at
+ * most 64 is off by up to 2^-21 of itself, and the result is rounded once. out, lse and ws may not overlap each other or an input.
  * D <= 1024 (FK_ERR_UNSUPPORTED above, and where a launch would hold 2^32 threads:
  * T Hq of 2^26 at least). The same arguments give the same bits on every run; other
  * requests around one, or another max_len, may change its last bits. Rows of
@@ -446,7 +446,8 @@ fk_status_t fk_kv_load8(const fk_kv_cache8_t* cache, const int32_t* slots, fk_dt
 
 /*
  * fk_paged_attn over an 8-bit cache: the same definition, with key and value of a
- * slot the numbers that its codes and scales stand for. q and out are dt.
+ * slot the numbers that its codes and scales stand for. q and out are dt; for
+ * 16-bit ones a softcap of at most 64 is off by up to 2^-21 of itself.
  *   ws: fk_workspace_size_attn8(dt, B, Hq, Hkv, D) bytes, 256-byte aligned.
  * Rows of at most 256 elements that start at multiples of 16 bytes and hold whole
  * 16-byte units (of codes; q and out as in fk_paged_attn) run on the matrix cores.
