@@ -780,6 +780,7 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
       for (int d = 0; d < L::dt; ++d)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[d][j] *= grown;
+      grew = false, grown = 1.f;                       // (done, for take_back() too)
       each<PV>([&](auto number) {
         constexpr int at = decltype(number)::value;
         add_value(value_at((lptr8c)values_of(NB - 1), value_place, at), at);
