@@ -638,10 +638,11 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
   const auto after = [&](int k) { return NB == 2 ? buf ^ (k & 1) : (buf + k) % 3; };
   const auto keys_of = [&](int k) { return (lptr8)(lk[0]) + after(k) * (kStep * rb); };
   const auto values_of = [&](int k) { return (lptr8)(lv[0]) + after(k) * (kStep * rb); };
-  // fp32 products add a key or two at a time, and a sum in 32 bits stands still after 2^24 terms
-  // alike (16-bit ones add 16 keys and reach 2^28): the sums over kRun steps are added to the row's
-  // place in the results or the workspace, where they are held scaled to `m_kept`.
-  constexpr int kRun = 1 << 15;
+  // A sum in 32 bits of n terms alike may be off by n 2^-25 of itself, and fp32 products add two keys at a
+  // time (16-bit ones 16): the sums over kRun steps, 2^15 terms, are added to the row's place in the
+  // results or the workspace, where they are held scaled to `m_kept`. l has a term a step and stays in one
+  // piece (held apart as well, in a register or in LDS, every fp32 call took 1 to 3% longer).
+  constexpr int kRun = 1 << 10;
   bool kept = false;
   float m_kept = -INFINITY;
   const auto with_kept = [&](auto each_four) {         // the lane's sums and their place, four by four

@@ -44,3 +44,27 @@ def test_a_last_key_above_all_others(fk, D, heads):
     want = ((n - count) * v64[0, 0] + w * v64[1, -1]) / (n - count + w)
     assert np.abs(host_f64(out[0], "f32") / want - 1).max() <= 2.0 ** -16
     assert np.abs(lse.double().cpu().numpy() - math.log(n - count + w)).max() <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("D", [8, 72, 200])
+def test_values_that_are_alike(fk, D):
+    """One token over 2^22 keys and some, equal scores below the first key's and for each element equal values,
+    so that every addition may round the same way: a run of up to 2^15 terms is off by 2^-10 of itself at
+    most, 2^7 runs and their join by 2^-17, the exponential by 2^-20; the weights' sum, of up to 2^17 steps,
+    by 2^-8."""
+    import torch
+    step, n = 64, (1 << 22) + 39
+    x = 1.21484375
+    g = torch.Generator(device="cuda").manual_seed(D)
+    k = torch.zeros((2, step, 1, D), device="cuda")
+    k[..., 0] = -x
+    k[1, 0] = 0.0
+    v = torch.rand((1, 1, 1, D), device="cuda", generator=g).add(0.5).repeat(2, step, 1, 1)
+    q = torch.zeros((1, 1, D), device="cuda")
+    q[..., 0] = 1.0
+    table = torch.zeros((1, n // step + 1), dtype=torch.int32, device="cuda")
+    table[0, 0] = 1
+    for hint in (1, 0):
+        out, lse = fk.fk_prompt_attn(q, k, v, table, _i32([n]), _i32([0, 1]), 1.0, max_len=hint, return_lse=True)
+        assert np.abs(host_f64(out[0, 0], "f32") / host_f64(v[0, 0, 0], "f32") - 1).max() <= 2.0 ** -8 + 2.0 ** -9
+        assert abs(float(lse) - math.log(1.0 + (n - 1) * math.exp(-x))) <= 2.0 ** -8
