@@ -260,14 +260,14 @@ template <int ROWS> __device__ __forceinline__ Where search_tile(const PromptArg
   }
 }
 
-// Which of a lane's sums are not finite, a bit each.
-template <int N> struct NotFinite { uint32_t bits[(N + 1) / 2]; };
-template <int N> __device__ __forceinline__ NotFinite<N> not_finite(const floatx16_t (&o)[N]) {
-  NotFinite<N> r = {};
+// Whether a lane's sums are all finite, and which of them are NaN, a bit each.
+template <int N> struct NotFinite { uint32_t none, bits[(N + 1) / 2]; };
+template <int N> __device__ __forceinline__ NotFinite<N> not_finite(const floatx16_t (&o)[N], bool none) {
+  NotFinite<N> r = {none};
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int j = 0; j < 16; ++j) r.bits[i / 2] |= (o[i][j] - o[i][j] == 0.f ? 0u : 1u) << ((i & 1) * 16 + j);
+    for (int j = 0; j < 16; ++j) r.bits[i / 2] |= (o[i][j] == o[i][j] ? 0u : 1u) << ((i & 1) * 16 + j);
   return r;
 }
 template <int N> __device__ __forceinline__ bool all_finite(const floatx16_t (&o)[N]) {
@@ -279,7 +279,7 @@ template <int N> __device__ __forceinline__ bool all_finite(const floatx16_t (&o
   return x == 0.f;
 }
 template <int N> __device__ __forceinline__ bool newly(const NotFinite<N>& now, const NotFinite<N>& before) {
-  uint32_t r = 0;
+  uint32_t r = before.none;
 #pragma unroll
   for (int i = 0; i < (N + 1) / 2; ++i) r |= now.bits[i] & ~before.bits[i];
   return r != 0;
@@ -770,8 +770,9 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
     if (!looked && (uint32_t)(st + 1) * kStep > (uint32_t)low) {           // (its hidden values have not been added yet)
       looked = true;
       if (DT == FK_F32 && kept) take_back();
-      broken_before = __any(!all_finite<L::dt>(o));
-      if (broken_before) broken[threadIdx.x] = not_finite<L::dt>(o);
+      const bool fine = all_finite<L::dt>(o);
+      broken_before = __any(!fine);
+      if (broken_before) broken[threadIdx.x] = not_finite<L::dt>(o, fine);
     }
   }
   for (; st <= t1 && t0 < t1; ++st, here = false) {    // the last values, and the other waves' steps
@@ -821,9 +822,10 @@ void prompt_mfma_kernel(PromptArgs a, PromptPlan p) {
     if (a.lse && h == 0) a.lse[row] = l == 0.f ? -INFINITY : m_nat + (logf(l) - shift * kLn2);
   }
   // A hidden key's probability is 0, but 0 times an infinity or NaN of its value is NaN. Rows whose
-  // sums stopped being finite in steps that hide keys are done again, key by key.
+  // sums stopped being finite in steps that hide keys, or where some were not finite before and others became NaN,
+  // are done again, key by key.
   bool again = looked && put && l - l == 0.f && !all_finite<L::dt>(o);
-  if (broken_before && __any(again)) again = again && newly<L::dt>(not_finite<L::dt>(o), broken[threadIdx.x]);
+  if (broken_before && __any(again)) again = again && newly<L::dt>(not_finite<L::dt>(o, false), broken[threadIdx.x]);
   uint64_t todo = __ballot(again);
   todo = (todo | todo >> 32) & 0xFFFFFFFFu;
   constexpr int EPL = (DC + 63) / 64;
