@@ -11,6 +11,7 @@ template <int DT, int EPL>
 __global__ __launch_bounds__(kWaves * 64) void attn8_any_kernel(AttnArgs8 a, int parts, float* po,
                                                                 float* pml) {
   using E = typename Val<DT>::type;
+  __shared__ float sm[kWaves], sl[kWaves], so[kWaves][EPL * 64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t bh = blockIdx.x / parts, b = bh / a.Hq, h = bh - b * a.Hq;
   const int part = (int)(blockIdx.x - bh * parts);
@@ -29,7 +30,10 @@ __global__ __launch_bounds__(kWaves * 64) void attn8_any_kernel(AttnArgs8 a, int
   const int64_t cap_len = a.width * c.page;
   const int64_t len = a.lens[b] < 0 ? 0 : (a.lens[b] < cap_len ? a.lens[b] : cap_len);
   const int64_t last = len * (part + 1) / parts;
+  Runs<EPL> runs{so[w] + lane};
+  int n = 0;
   for (int64_t j = len * part / parts + w; j < last; j += kWaves) {
+    if (n++ == kKeyRun) runs.add(m, l, o), n = 1;
     const int64_t page = a.table[b * a.ld_table + j / c.page], tok = j % c.page;
     if (page < 0 || page >= c.pages) continue;
     float bias = 0.f;
@@ -61,7 +65,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn8_any_kernel(AttnArgs8 a, int
       if (e < D) o[i] = fmaf(p, e4m3_get(v[e]) * vs, o[i] * alpha);
     }
   }
-  __shared__ float sm[kWaves], sl[kWaves], so[kWaves][EPL * 64];
+  runs.join(m, l, o);
   if (lane == 0) sm[w] = m, sl[w] = l;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) so[w][lane + 64 * i] = o[i];
