@@ -15,6 +15,7 @@ template <int DT, int EPL>
 __global__ __launch_bounds__(kWaves * 64) void attn_any_kernel(AttnArgs a, int parts, float* po,
                                                                float* pml) {
   using E = typename Val<DT>::type;
+  __shared__ float sm[kWaves], sl[kWaves], so[kWaves][EPL * 64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t bh = blockIdx.x / parts, b = bh / a.Hq, h = bh - b * a.Hq;
   const int part = (int)(blockIdx.x - bh * parts);
@@ -33,7 +34,10 @@ __global__ __launch_bounds__(kWaves * 64) void attn_any_kernel(AttnArgs a, int p
   const int64_t cap_len = a.width * c.page;
   const int64_t len = a.lens[b] < 0 ? 0 : (a.lens[b] < cap_len ? a.lens[b] : cap_len);
   const int64_t last = len * (part + 1) / parts;
+  Runs<EPL> runs{so[w] + lane};
+  int n = 0;
   for (int64_t j = len * part / parts + w; j < last; j += kWaves) {
+    if (n++ == kKeyRun) runs.add(m, l, o), n = 1;
     const int64_t page = a.table[b * a.ld_table + j / c.page], tok = j % c.page;
     if (page < 0 || page >= c.pages) continue;
     float bias = 0.f;
@@ -63,7 +67,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_any_kernel(AttnArgs a, int p
       if (e < D) o[i] = fmaf(p, Val<DT>::get(v + e), o[i] * alpha);
     }
   }
-  __shared__ float sm[kWaves], sl[kWaves], so[kWaves][EPL * 64];
+  runs.join(m, l, o);
   if (lane == 0) sm[w] = m, sl[w] = l;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) so[w][lane + 64 * i] = o[i];

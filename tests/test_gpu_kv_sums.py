@@ -17,7 +17,7 @@ def _i32(x):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("call", ["fk_paged_attn8"])
+@pytest.mark.parametrize("call", ["fk_paged_attn", "fk_paged_attn8"])
 def test_long_sums_of_any_layout(fk, call, dtype):
     """2^22 keys of one weight, 0.2968 of the largest, which a wave adds a quarter of one by one: in one
     run the last half of them would be added as multiples of 2^-5 (0.28125 or 0.3125). Runs of at most
