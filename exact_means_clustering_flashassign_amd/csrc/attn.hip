@@ -405,7 +405,7 @@ bool aligned16(const AttnArgs& a, int eb) {
 }
 
 template <int DT_, int DP_, int HT_, bool EXTRA> struct Op {
-  static constexpr int DT = DT_, DP = DP_, HT = HT_;
+  static constexpr int DT = DT_, DP = DP_, HT = HT_, PT = DT_;
   using Args = AttnArgs;
   using S = Shape<DT, DP>;
   using Rows = fk::Rows<DT, DP>;
@@ -445,7 +445,7 @@ hipError_t run_mfma(const AttnArgs& a, void* ws, hipStream_t s) {
   kernel<<<(unsigned)c.blocks, c.W * 64, 0, s>>>(a, c.p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !c.cut) return e;
-  return join_parts<DT>(a, c.p, s);
+  return join_parts<DT, DT>(a, c.p, s);
 }
 
 template <int DT>

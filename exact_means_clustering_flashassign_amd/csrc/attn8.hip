@@ -141,6 +141,7 @@ template <int DT, int DP_> struct Shape8 {
   static constexpr int qn = DT == FK_F32 ? 3 : 1;           // 16-bit numbers of a query's element
   static constexpr int pn = DT == FK_F32 ? 3 : 2;           // and of a probability
   static constexpr int qt = DT == FK_F16 ? FK_F16 : FK_BF16;
+  static constexpr int pt = DT == FK_F32 ? FK_F32 : FK_BF16;       // (no factor: the largest scales' products overflow)
 };
 
 // Row addresses and numbers of one step's keys, per wave and parity.
@@ -394,7 +395,7 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
       for (int u = 0; u < S::tiles; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float x = prob<DT>(s[h][u][i] - ref);
+          const float x = prob<S::pt>(s[h][u][i] - ref);
           part += x;
           s[h][u][i] = x * now.vs[16 * u + 4 * g + i];
         }
@@ -450,6 +451,7 @@ template <int DT_, int DP_, int HT_, bool EXTRA> struct Op8 {
   static constexpr int DT = DT_, DP = DP_, HT = HT_;
   using Args = AttnArgs8;
   using S = Shape8<DT, DP>;
+  static constexpr int PT = S::pt;
   using Rows = Rows8;
   template <int KIND, class... A> __device__ static __forceinline__ void attend(A&&... args) {
     attend8<DT, DP, HT, EXTRA, KIND>(args...);
@@ -495,7 +497,7 @@ hipError_t run_mfma(const AttnArgs8& a, void* ws, hipStream_t s) {
   kernel<<<(unsigned)c.blocks, c.W * 64, 0, s>>>(a, c.p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !c.cut) return e;
-  return join_parts<DT>(a, c.p, s);
+  return join_parts<DT, Shape8<DT, DP>::pt>(a, c.p, s);
 }
 
 template <int DT> hipError_t run(const AttnArgs8& a, void* ws, hipStream_t s) {

@@ -448,7 +448,7 @@ void attn_mfma_kernel(typename Op::Args a, Plan p) {
             for (int j = 0; j < 4; ++j) x[j] *= r;
             store4<DT>(a.out, row * D + e, x);
             if (e == 0 && a.lse)
-              a.lse[row] = l == 0.f ? -INFINITY : top + (logf(l) - kProbShift<DT> * kLn2);
+              a.lse[row] = l == 0.f ? -INFINITY : top + (logf(l) - kProbShift<Op::PT> * kLn2);
           } else {
             const int64_t pr = ps + h2 * kHeadTile + h;
             *(float4*)(p.o + pr * D + e) = make_float4(x[0], x[1], x[2], x[3]);
@@ -472,8 +472,8 @@ constexpr int kJoin = 256;        // threads of a joining block
 // Joins the partial results of a request that was cut: slot 1 of its first part,
 // slot 0 of the others. R (request, query head) rows a block: one a wave, or one whose
 // columns are dealt to `slices` blocks. Bound by latency: the parts' numbers, their
-// maxima and sums, then the rows.
-template <int DT, int R>
+// maxima and sums, then the rows. Probabilities are scaled as those of type PT.
+template <int DT, int PT, int R>
 __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Plan p, int slices) {
   constexpr int threads = kJoin / R;
   __shared__ float fac[R][kMaxParts], part_l[R][kMaxParts];
@@ -544,7 +544,7 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Plan p, in
   for (int j = 0; j < 4; ++j) x[j] *= r;
   store4<DT>(a.out, out_row * D + e, x);
   if (e == 0 && a.lse)
-    a.lse[out_row] = l == 0.f ? -INFINITY : top + (logf(l) - kProbShift<DT> * kLn2);
+    a.lse[out_row] = l == 0.f ? -INFINITY : top + (logf(l) - kProbShift<PT> * kLn2);
 }
 
 // Query heads a wave serves at once: 32 where there are more than 16 and the registers
@@ -630,19 +630,19 @@ inline Choice choose(const AttnArgs& a, int keys, int HT, int DP, void* ws) {
 }
 
 // Joins what a call cut.
-template <int DT> hipError_t join_parts(const AttnArgs& a, const Plan& p, hipStream_t s) {
+template <int DT, int PT> hipError_t join_parts(const AttnArgs& a, const Plan& p, hipStream_t s) {
   const int64_t cus = device_cus();
   // Many rows: most were not cut or have few parts, and a wave is enough for one.
   const int64_t outs = a.B * a.Hq;
   if (outs >= 8 * cus) {
-    attn_join_kernel<DT, 4><<<(unsigned)((outs + 3) / 4), kJoin, 0, s>>>(a, p, 1);
+    attn_join_kernel<DT, PT, 4><<<(unsigned)((outs + 3) / 4), kJoin, 0, s>>>(a, p, 1);
     return hipGetLastError();
   }
   // Few rows have many parts: as many blocks a row as there are CUs for, down to 64 bytes
   // of a partial result (one request of 131072 keys, 32 query heads: 95.9 -> 94.5 us).
   int slices = 1;
   while (2 * slices * outs <= cus && a.cache.dim / (2 * slices) >= 16) slices *= 2;
-  attn_join_kernel<DT, 1><<<(unsigned)(outs * slices), kJoin, 0, s>>>(a, p, slices);
+  attn_join_kernel<DT, PT, 1><<<(unsigned)(outs * slices), kJoin, 0, s>>>(a, p, slices);
   return hipGetLastError();
 }
 
