@@ -297,7 +297,7 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
     r.k[lane] = live ? ka : zero;
     r.v[lane] = live ? va : zero;
     r.bias[lane] = x.bias;
-    r.ks[lane] = x.ks * a.scale;
+    r.ks[lane] = x.ks;
     r.vs[lane] = x.vs;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
@@ -365,7 +365,8 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
 #pragma unroll
       for (int u = 0; u < S::tiles; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[h][u][i] *= now.ks[16 * u + 4 * g + i];
+        // (one after the other: the product of both scales may overflow where the score is 0)
+        for (int i = 0; i < 4; ++i) s[h][u][i] = s[h][u][i] * now.ks[16 * u + 4 * g + i] * a.scale;
       const auto every = [&](auto f) {
 #pragma unroll
         for (int u = 0; u < S::tiles; ++u)
