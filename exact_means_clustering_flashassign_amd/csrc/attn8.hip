@@ -96,7 +96,7 @@ template <int DT>
 hipError_t run_any(const AttnArgs8& a, int64_t most, void* ws, hipStream_t s) {
   const int parts = most > 128 ? (int)any_parts(a.B, a.Hq) : 1;
   const int64_t heads = a.B * a.Hq, blocks = heads * parts;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (blocks > most_blocks(kWaves)) return hipErrorInvalidConfiguration;
   const int64_t D = a.cache.dim;
   float* po = (float*)ws;
   float* pml = po + blocks * D;

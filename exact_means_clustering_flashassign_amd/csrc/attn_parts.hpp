@@ -11,6 +11,9 @@ namespace {
 
 constexpr int kWaves = 4;
 
+// Blocks of so many waves that a launch may have: fewer than 2^32 threads.
+constexpr int64_t most_blocks(int waves) { return 0xFFFFFFFF / (waves * 64); }
+
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLog2eRest = 1.92596299112661746887e-8f;    // log2 e - kLog2e
@@ -624,8 +627,9 @@ inline Choice choose(const AttnArgs& a, int keys, int HT, int DP, void* ws) {
   p.team_log = p.team == 8 ? 3 : (p.team == 4 ? 2 : p.team - 1);
   p.by_tiles = fast_div((uint32_t)p.tiles);
   p.by_heads = fast_div((uint32_t)p.heads);
-  if (units * a.B + W <= 0x7FFFFFFF && a.B * a.Hq <= 0x7FFFFFFF - 4)
-    c.blocks = (units * (cut ? p.parts : a.B) * p.team + W - 1) / W;
+  const int64_t blocks = (units * (cut ? p.parts : a.B) * p.team + W - 1) / W;
+  const bool joined = !cut || (a.B * a.Hq + 3) / 4 <= most_blocks(kWaves);      // (join_parts)
+  if (units * a.B + W <= 0x7FFFFFFF && joined && blocks <= most_blocks(W)) c.blocks = blocks;
   return c;
 }
 

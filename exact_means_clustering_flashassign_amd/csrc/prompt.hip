@@ -212,8 +212,8 @@ template <int DT, int EPL, int R> hipError_t run_any_as(const PromptArgs& a, hip
   p.page = fast_div((uint32_t)a.cache.page);
   p.by_heads = fast_div((uint32_t)p.heads);
   p.by_G = fast_div((uint32_t)p.G);
-  const int64_t tiles = a.B <= 64 ? (a.T * p.G + R - 1) / R + a.B - 1 : a.T * p.G / R + a.B, blocks = tiles * p.heads;
-  if (blocks > 0xFFFFFF || a.T * p.G > 0x7FFFFFFF - R) return hipErrorInvalidConfiguration;      // (fewer than 2^32 threads)
+  const int64_t blocks = tile_numbers(a, R) * p.heads;
+  if (blocks > most_blocks(kWaves) || a.T * p.G > 0x7FFFFFFF - R) return hipErrorInvalidConfiguration;
   prompt_any_kernel<DT, EPL, R><<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, p);
   return hipGetLastError();
 }
@@ -445,8 +445,8 @@ template <int DT, int NT> hipError_t run_split_as(const PromptArgs& a, bool unit
   p.page = fast_div((uint32_t)a.cache.page);
   p.by_heads = fast_div((uint32_t)p.heads);
   p.by_G = fast_div((uint32_t)p.G);
-  const int64_t tiles = a.B <= 64 ? (a.T * p.G + 31) / 32 + a.B - 1 : a.T * p.G / 32 + a.B, blocks = tiles * p.heads;
-  if (blocks > 0xFFFFFF || a.T * p.G > 0x7FFFFFFF - 32) return hipErrorInvalidConfiguration;     // (fewer than 2^32 threads)
+  const int64_t blocks = tile_numbers(a, 32) * p.heads;
+  if (blocks > most_blocks(kWaves) || a.T * p.G > 0x7FFFFFFF - 32) return hipErrorInvalidConfiguration;
   (units ? prompt_split_kernel<DT, NT, true> : prompt_split_kernel<DT, NT, false>)
       <<<(unsigned)blocks, kWaves * 64, 0, s>>>(a, p);
   return hipGetLastError();

@@ -899,6 +899,12 @@ __global__ __launch_bounds__(kWaves * 64) void prompt_join_kernel(PromptArgs a, 
   if (a.lse && lane == 0) a.lse[r] = l == 0.f ? -INFINITY : m + (logf(l) - prob_shift<DT> * kLn2);
 }
 
+// Numbers of a cache head's tiles: as many as there can be (count_tiles), or as are searched (search_tile).
+int64_t tile_numbers(const PromptArgs& a, int64_t rows) {
+  const int64_t all = a.T * (a.Hq / a.cache.heads);
+  return a.B <= 64 ? (all + rows - 1) / rows + a.B - 1 : all / rows + a.B;
+}
+
 // Parts that a row's keys may be cut into: four blocks a CU at most. (Two of them keep the
 // workspace half as large, and 4 requests of 250 to 999 tokens behind 1056 centres, fp32, take 117 us
 // instead of 106, 1024 tokens of 64 elements 102 instead of 94.)
@@ -956,7 +962,7 @@ inline double estimate(int dt, int DC, int W, int step, const PromptArgs& a, con
   return us;
 }
 
-// The number of parts with the shortest estimate.
+// The number of parts with the shortest estimate, of those that a launch can hold.
 struct Best {
   double us;
   int parts;
@@ -964,8 +970,9 @@ struct Best {
 inline Best best_parts(int dt, int DC, int W, int step, const PromptArgs& a) {
   const Outline o = outline(a, W * 32, step);
   const int64_t most = most_parts(a.T, a.Hq / a.cache.heads, a.cache.heads, W * 32);
+  const int64_t blocks = tile_numbers(a, W * 32) * a.cache.heads;
   Best best{1e300, 1};
-  for (int64_t n = 1; n <= most && (n == 1 || o.longest >= 4 * n); ++n) {
+  for (int64_t n = 1; n <= most && (n == 1 || o.longest >= 4 * n) && blocks <= most_blocks(W) / n; ++n) {
     const double us = estimate(dt, DC, W, step, a, o, n);
     if (us < best.us) best = {us, (int)n};
   }
@@ -978,8 +985,10 @@ template <int DT, int DC, int W> hipError_t run_tiles(const PromptArgs& a, int p
   p.heads = (int)a.cache.heads;
   p.G = (int)(a.Hq / a.cache.heads);
   const Outline o = outline(a, L::rows, L::step);
-  const int64_t tiles = a.B <= 64 ? (a.T * p.G + L::rows - 1) / L::rows + a.B - 1         // at most so many
-                                  : a.T * p.G / L::rows + a.B;                            // numbers
+  const int64_t tiles = tile_numbers(a, L::rows), blocks = tiles * p.heads * parts;
+  if (blocks > most_blocks(W) || a.T * p.G > 0x7FFFFFFF - 512 ||
+      (parts > 1 && (a.T * a.Hq + kWaves - 1) / kWaves > most_blocks(kWaves)))
+    return hipErrorInvalidConfiguration;
   p.parts = parts;
   p.chunk = p.parts == 1 ? 0x7FFFFFFF / L::step : (int)((o.longest + p.parts - 1) / p.parts);
   p.o = (float*)ws;
@@ -988,7 +997,6 @@ template <int DT, int DC, int W> hipError_t run_tiles(const PromptArgs& a, int p
   p.by_heads = fast_div((uint32_t)p.heads);
   p.by_tiles = fast_div((uint32_t)tiles);
   p.by_G = fast_div((uint32_t)p.G);
-  const int64_t blocks = tiles * p.heads * p.parts;
   // Where every block finds room at once, two to a CU, the second half comes in turned order: the
   // longest share a CU with the shortest. (2048 tokens, bf16: 70 us in one order, 61; fp32 rows of
   // 64: 253 and 205.)
@@ -996,7 +1004,6 @@ template <int DT, int DC, int W> hipError_t run_tiles(const PromptArgs& a, int p
   const bool pairs = tile_blocks(DT, DC, W) == 2 && p.parts == 1 && blocks <= 2 * device_cus() + p.heads * a.B;
   p.last = (uint32_t)(tiles * p.parts - 1);
   p.turn = pairs ? (uint32_t)each : 0xFFFFFFFFu;
-  if (blocks > 0x7FFFFF || a.T * p.G > 0x7FFFFFFF - 512) return hipErrorInvalidConfiguration;
   auto kernel = prompt_mfma_kernel<DT, DC, W, kCapScore>;
   if constexpr (DT != FK_F32) {
     if (a.softcap > 0.f && a.softcap <= kNearCap)

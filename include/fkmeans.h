@@ -351,7 +351,8 @@ fk_status_t fk_qk_norm_rope(const void* q, const int64_t q_stride[2], const void
  *   ws: fk_workspace_size_attn(dt, B, Hq, Hkv, D) bytes, 256-byte aligned.
  * out, lse and ws may not overlap each other or an input, but out may be q itself
  * where q is contiguous.
- * D <= 1024 (FK_ERR_UNSUPPORTED above). Rows of at most 256 elements that
+ * D <= 1024 (FK_ERR_UNSUPPORTED above, and where a launch would hold 2^32 threads:
+ * B Hq of 2^24 at least). Rows of at most 256 elements that
  * start at multiples of 16 bytes and hold whole 16-byte units run on the
  * matrix cores, others on a path 10 to 40 times slower. The same arguments give
  * the same bits on every run; another batch around a request, or another
@@ -386,8 +387,8 @@ size_t fk_workspace_size_attn(fk_dtype_t dt, int64_t B, int64_t Hq, int64_t Hkv,
  * Scores, softmax statistics and sums are fp32; with 16-bit caches each
  * probability is rounded to dt before its product with the value, a softcap of at
  * most 64 is off by up to 2^-21 of itself, and the result is rounded once. out, lse and ws may not overlap each other or an input.
- * D <= 1024 (FK_ERR_UNSUPPORTED above, and where a launch would hold 2^32 threads:
- * T Hq of 2^26 at least). The same arguments give the same bits on every run; other
+ * D <= 1024 (FK_ERR_UNSUPPORTED above, and where a launch would hold 2^32 threads, which
+ * takes T Hq of 2^26 or T Hq + 8 B Hkv of 2^27 at least). The same arguments give the same bits on every run; other
  * requests around one, or another max_len, may change its last bits. Rows of
  * at most 256 elements that start at multiples of 16 bytes and hold whole 16-byte
  * units, in q and out as well, are the fast ones; other fp32 rows run on the vector units.
