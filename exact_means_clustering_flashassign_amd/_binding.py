@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import struct
 from typing import Optional, Tuple
@@ -436,6 +437,44 @@ def _meets(lo, hi, t):
     return lo < hi and within(lo, hi, axes, sum((n - 1) * s for s, n in axes) + size)
 
 
+def _share(t, u, at_t=None, at_u=None):
+    """Whether two tensors have a byte in common; at_t, at_u: their addresses. Indices of both that meet have
+    offsets whose difference lies in a range as wide as an element of each, so the question is whether
+    a sum of multiples of all strides does: those of u counted down from their last index, so that all
+    are added. True too where strides that do not nest leave too many sums to look at."""
+    at_t = t.data_ptr() if at_t is None else at_t
+    at_u = u.data_ptr() if at_u is None else at_u
+    if not t.numel() or not u.numel():
+        return False
+    axes, back = {}, 0
+    for x in (t, u):
+        size = x.element_size()
+        for s, n in zip(x.stride(), x.shape):
+            if s and n > 1:
+                axes[s * size] = axes.get(s * size, 0) + n - 1
+                back += (n - 1) * s * size if x is u else 0
+    lo = at_u - at_t + back - t.element_size() + 1
+    hi = at_u - at_t + back + u.element_size()           # a sum in [lo, hi) is looked for
+    axes = sorted(axes.items(), reverse=True)
+    looks = 0
+
+    def within(lo, hi, i, extent):                       # extent: the largest sum of axes from i on
+        nonlocal looks
+        if hi <= 0 or lo > extent:
+            return False
+        if i == len(axes):
+            return True                                  # (the sum is 0, in the range)
+        looks += 1
+        if looks > 10000:
+            return True
+        s, most = axes[i]
+        extent -= most * s
+        first, last = max(0, -((extent - lo) // s)), min(most, (hi - 1) // s)
+        return any(within(lo - k * s, hi - k * s, i + 1, extent) for k in range(first, last + 1))
+
+    return within(lo, hi, 0, sum(s * n for s, n in axes))
+
+
 def _no_grad(t, name):
     """Parameters may be given where no gradient is asked for; else it would be lost."""
     if t.requires_grad and _tc.grad():
@@ -782,13 +821,26 @@ def _kv_cache8(k_cache, v_cache, k_scale, v_scale, key_bias, heads, dim, index):
                         k0, k1, k2, v0, v1, v2, *ssk, *ssv, *sb), h, d
 
 
+_first = operator.itemgetter(0)
+
+
+def _apart_cache(tensors):
+    """Refuses a cache's tensors (address, end, name, tensor) that have elements in common."""
+    for i, (lo, hi, name, t) in enumerate(tensors):
+        for a, b, other, u in tensors[:i]:
+            if max(lo, a) < min(hi, b) and _share(t, u):
+                raise ValueError(f"{name} overlaps {other}: keys and values, their scales and biases need "
+                                 f"elements of their own")
+
+
 def fk_kv_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, key_bias=None) -> None:
     """Keys and values k, v (T,Hkv,D) quantised to e4m3 as they are stored in slots (T)
     int32 of k_cache and v_cache (pages, page, Hkv, D) float8_e4m3fn: a row's scale, in
     k_scale and v_scale (pages, page, Hkv) fp32, is the smallest power of two that takes its
     largest element to 448 at most. key_bias (pages, page, Hkv) becomes 0. Slots outside
     the cache are skipped, the others have to be distinct. k, v and slots may not
-    lie between the first and the last byte of any of the cache's tensors."""
+    lie between the first and the last byte of any of the cache's tensors, and these may
+    lie between one another's elements but not share any."""
     tc = _tc or _calls()
     dt, index = k.dtype, _gpu_index(k, "k")
     code = tc.codes.get(dt)
@@ -809,7 +861,7 @@ def fk_kv_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, key_bias=None)
         b, (u0, u1, _) = v.data_ptr(), sv
         ins = ((a, a + (t1 * s0 + h1 * s1 + D) * e), (b, b + (t1 * u0 + h1 * u1 + D) * e),
                (p_slots, p_slots + 4 * T))
-        at = set()
+        cache_at = []
         for name, t, d, size in (("k_cache", k_cache, D, 1), ("v_cache", v_cache, D, 1),
                                  ("k_scale", k_scale, 1, 4), ("v_scale", v_scale, 1, 4),
                                  ("key_bias", key_bias, 1, 4)):
@@ -820,9 +872,14 @@ def fk_kv_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, key_bias=None)
             for a, b in ins:
                 if a < hi and lo < b:
                     raise ValueError(f"{name} overlaps k, v or slots, which the call reads")
-            if lo in at:
-                raise ValueError("keys and values, their scales and biases need tensors of their own")
-            at.add(lo)
+            cache_at.append((lo, hi, name, t))
+        cache_at.sort(key=_first)
+        end = 0
+        for lo, hi, _, _ in cache_at:
+            if lo < end:
+                _apart_cache(cache_at)
+                break
+            end = hi
     st = _launch(index, _lib.fk_kv_store8, k.data_ptr(), _pack2(sk[0], sk[1]), v.data_ptr(),
                  _pack2(sv[0], sv[1]), code, T, p_slots, cache, tc.stream(index))
     if st:
