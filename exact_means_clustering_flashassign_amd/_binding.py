@@ -60,7 +60,10 @@ def load(path: Optional[str] = None):
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: build it first "
                            "(python -m exact_means_clustering_flashassign_amd.build)")
-    _torch()          # brings its HIP runtime, which this library then finds as its own
+    try:
+        _torch()      # brings its HIP runtime, which this library then finds as its own
+    except ImportError:
+        pass          # what takes no tensors works without
     lib = ctypes.CDLL(path)
     P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
     sig = {
