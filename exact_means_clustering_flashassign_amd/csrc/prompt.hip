@@ -6,7 +6,7 @@
 namespace fk {
 namespace {
 
-// fp32 rows of any size, stride and alignment. The rows of a request are laid out as for the
+// Rows of any size, stride and alignment: all fp32 ones, 16-bit ones where they are few (few_rows). The rows of a request are laid out as for the
 // matrix-core kernel (row r is head r % G of token r / G); a block takes R of one cache head, a wave every
 // fourth step of 64 keys. For scores a lane has a key: 64 elements of every key go to LDS, an
 // element a lane as they lie in memory, and are read back a key a lane, next to the R queries'
@@ -220,11 +220,24 @@ template <int DT, int EPL, int R> hipError_t run_any_as(const PromptArgs& a, hip
 
 template <int DT> hipError_t run_any(const PromptArgs& a, hipStream_t s) {
   const int64_t D = a.cache.dim;
-  return D <= 64    ? run_any_as<DT, 1, 8>(a, s)
-         : D <= 128 ? run_any_as<DT, 2, 8>(a, s)
-         : D <= 256 ? run_any_as<DT, 4, 8>(a, s)
-         : D <= 512 ? run_any_as<DT, 8, 8>(a, s)
-                    : run_any_as<DT, 16, 8>(a, s);
+  if (D <= 64) return run_any_as<DT, 1, 8>(a, s);
+  if (D <= 128) return run_any_as<DT, 2, 8>(a, s);
+  if constexpr (DT == FK_F32) {
+    if (D > 512) return run_any_as<DT, 16, 8>(a, s);
+    if (D > 256) return run_any_as<DT, 8, 8>(a, s);
+  }
+  return run_any_as<DT, 4, 8>(a, s);
+}
+
+// Whether 16-bit rows run there too: up to 256 elements, where the chip holds all blocks at once (two a CU
+// up to 128 elements) and there are keys for the waves, of which each has its own. A block of
+// prompt_split_kernel has all keys to itself. (One token of 32 heads on 8 over 8192 keys, 90 elements 446 us,
+// there 1100; 33 284 and 862; 250 1430 and 1680; 512 8700 and 1070. 128 tokens behind 8192, 512 blocks, of 90
+// 563 and 1102; 256 tokens 1099 and 1121, 512 2186 and 1327. 64 tokens alone 28 and 14.)
+bool few_rows(const PromptArgs& a) {
+  const Outline o = outline(a, 8, 64);
+  return a.cache.dim <= 256 && longest(a) >= 256 &&
+         o.tiles * a.cache.heads <= device_cus() * (a.cache.dim <= 128 ? 2 : 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -475,7 +488,7 @@ template <int DT> hipError_t run(const PromptArgs& a, void* ws, hipStream_t s) {
   const bool units = aligned16(a, Val<DT>::bytes);
   if (D > 256 || !units) {
     if constexpr (DT == FK_F32) return run_any<DT>(a, s);
-    else return run_split<DT>(a, units, s);
+    else return few_rows(a) ? run_any<DT>(a, s) : run_split<DT>(a, units, s);
   }
   return D <= 128 ? launch_prompt_narrow<DT>(a, ws, s) : launch_prompt_wide(a, DT, ws, s);
 }
