@@ -440,28 +440,23 @@ def _meets(lo, hi, t):
     return lo < hi and within(lo, hi, axes, sum((n - 1) * s for s, n in axes) + size)
 
 
-def _share(t, u, at_t=None, at_u=None):
-    """Whether two tensors have a byte in common; at_t, at_u: their addresses. Indices of both that meet have
-    offsets whose difference lies in a range as wide as an element of each, so the question is whether
-    a sum of multiples of all strides does: those of u counted down from their last index, so that all
-    are added. True too where strides that do not nest leave too many sums to look at."""
-    at_t = t.data_ptr() if at_t is None else at_t
-    at_u = u.data_ptr() if at_u is None else at_u
-    if not t.numel() or not u.numel():
-        return False
+@functools.lru_cache(256)
+def _layouts_meet(apart, *layouts):
+    """Whether two tensors of these layouts (shape, strides, bytes of an element), the second `apart` bytes
+    behind the first, have a byte in common. Indices that meet have offsets whose difference lies in a range
+    as wide as both elements, so the question is whether a sum of multiples of all strides does: those of
+    the second counted down from its last index, so that all are added. True too where strides that do
+    not nest leave too many sums to look at."""
     axes, back = {}, 0
-    for x in (t, u):
-        size = x.element_size()
-        for s, n in zip(x.stride(), x.shape):
+    for i, (shape, strides, size) in enumerate(layouts):
+        for n, s in zip(shape, strides):
             if s and n > 1:
                 axes[s * size] = axes.get(s * size, 0) + n - 1
-                back += (n - 1) * s * size if x is u else 0
-    lo = at_u - at_t + back - t.element_size() + 1
-    hi = at_u - at_t + back + u.element_size()           # a sum in [lo, hi) is looked for
+                back += i * (n - 1) * s * size
     axes = sorted(axes.items(), reverse=True)
     looks = 0
 
-    def within(lo, hi, i, extent):                       # extent: the largest sum of axes from i on
+    def within(lo, hi, i, extent):                       # a sum in [lo, hi); extent: the largest of axes from i on
         nonlocal looks
         if hi <= 0 or lo > extent:
             return False
@@ -475,7 +470,16 @@ def _share(t, u, at_t=None, at_u=None):
         first, last = max(0, -((extent - lo) // s)), min(most, (hi - 1) // s)
         return any(within(lo - k * s, hi - k * s, i + 1, extent) for k in range(first, last + 1))
 
-    return within(lo, hi, 0, sum(s * n for s, n in axes))
+    apart += back
+    return within(apart - layouts[0][2] + 1, apart + layouts[1][2], 0, sum(s * n for s, n in axes))
+
+
+def _share(t, u, at_t=None, at_u=None):
+    """Whether two tensors have a byte in common; at_t, at_u: their addresses."""
+    at_t = t.data_ptr() if at_t is None else at_t
+    at_u = u.data_ptr() if at_u is None else at_u
+    return t.numel() > 0 and u.numel() > 0 and _layouts_meet(
+        at_u - at_t, *((x.shape, x.stride(), x.element_size()) for x in (t, u)))
 
 
 def _no_grad(t, name):
