@@ -385,14 +385,16 @@ size_t fk_workspace_size_attn(fk_dtype_t dt, int64_t B, int64_t Hq, int64_t Hkv,
  *   out (T,Hq,D) dt out; lse (T,Hq) fp32 out, may be null.
  *   ws: fk_workspace_size_prompt(dt, T, B, Hq, Hkv, D) bytes, 256-byte aligned.
  * Scores, softmax statistics and sums are fp32; with 16-bit caches a
- * probability may be rounded to dt before its product with the value, a softcap of at
- * most 64 is off by up to 2^-21 of itself, and the result is rounded once. out, lse and ws may not overlap each other or an input.
- * D <= 1024 (FK_ERR_UNSUPPORTED above, and where a launch would hold 2^32 threads, which
- * takes T Hq of 2^26 or T Hq + 8 B Hkv of 2^27 at least). The same arguments give the same bits on every run; other
- * requests around one, or another max_len, may change its last bits. Rows of
- * at most 256 elements that start at multiples of 16 bytes and hold whole 16-byte
- * units, in q and out as well, are the fast ones; other fp32 rows, and few 16-bit ones over
- * long keys, run on the vector units.
+ * probability may be rounded to dt before its product with the value (in fp16 one below
+ * 2^-37 of the row's largest may count as that), a softcap of at most 64 is
+ * off by up to 2^-21 of itself, and the result is rounded once. out, lse and ws may
+ * not overlap each other or an input.
+ * D <= 1024 (FK_ERR_UNSUPPORTED above, and where a launch would hold 2^32 threads,
+ * which takes T Hq of 2^26 or T Hq + 8 B Hkv of 2^27 at least). The same arguments
+ * give the same bits on every run; other requests around one, or another max_len, may
+ * change its last bits. Rows of at most 256 elements that start at multiples of 16
+ * bytes and hold whole 16-byte units, in q and out as well, are the fast ones; other
+ * fp32 rows, and few 16-bit ones over long keys, run on the vector units.
  */
 fk_status_t fk_prompt_attn(const void* q, const int64_t q_stride[2], fk_dtype_t dt, int64_t T,
                            int64_t B, int64_t Hq, const fk_kv_cache_t* cache,
