@@ -185,12 +185,17 @@ template <int N> __device__ __forceinline__ void split_bf16(const float (&x)[8],
   }
 }
 
-template <int DT, int DP, int HT, bool EXTRA, int KIND>
+// What a score takes part in: the scales alone; a bias and a cap of at most kNearCap (16-bit types); a bias
+// and any cap.
+enum { kPlainScore, kNearCapScore, kCapScore };
+
+template <int DT, int DP, int HT, int SCORE, int KIND>
 __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64_t b, int hk, int ht, int len,
                                         int step, int stride, int end, Rows8* rows,
                                         Acc<Shape8<DT, DP>, HT>& acc) {
   using S = Shape8<DT, DP>;
   constexpr int QT = S::qt;
+  constexpr bool EXTRA = SCORE != kPlainScore;
   const fk_kv_cache_t& c = a.cache;
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const int D = KIND == kNarrow ? (int)c.dim : DP;
@@ -258,7 +263,7 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
   const uint64_t kbase = (uint64_t)c.k + (uint64_t)hk * c.k_stride[2];
   const uint64_t vbase = (uint64_t)c.v + (uint64_t)hk * c.v_stride[2];
   const uint64_t zero = (uint64_t)zero_row;
-  const bool cap = EXTRA && a.softcap > 0.f, near = cap && DT != FK_F32 && a.softcap <= kNearCap;
+  const bool cap = EXTRA && a.softcap > 0.f;
   const float inv_cap = cap ? 1.f / a.softcap : 0.f;
   const bool has_bias = EXTRA && c.key_bias && c.pages > 0;
   const uint64_t bbase = (uint64_t)c.key_bias + (uint64_t)hk * c.bias_stride[2] * 4;
@@ -365,22 +370,13 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
 #pragma unroll
       for (int u = 0; u < S::tiles; ++u)
 #pragma unroll
-        // (one after the other: the product of both scales may overflow where the score is 0)
-        for (int i = 0; i < 4; ++i) s[h][u][i] = s[h][u][i] * now.ks[16 * u + 4 * g + i] * a.scale;
-      const auto every = [&](auto f) {
-#pragma unroll
-        for (int u = 0; u < S::tiles; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[h][u][i] = f(s[h][u][i]);
-      };
-      if (near) every([&](float x) { return cap_16bit(x, a.softcap, inv_cap); });
-      else if (cap) every([&](float x) { return capped(x, a.softcap, inv_cap); });
-#pragma unroll
-      for (int u = 0; u < S::tiles; ++u)
-#pragma unroll
         for (int i = 0; i < 4; ++i) {
           // -inf where a key does not count
-          const float bias = now.bias[16 * u + 4 * g + i], x = s[h][u][i];
+          const int at = 16 * u + 4 * g + i;
+          const float bias = now.bias[at];
+          // (one after the other: the product of both scales may overflow where the score is 0)
+          float x = s[h][u][i] * now.ks[at] * a.scale;
+          if (cap) x = SCORE == kNearCapScore ? cap_16bit(x, a.softcap, inv_cap) : capped(x, a.softcap, inv_cap);
           s[h][u][i] = bias == -INFINITY ? bias : (EXTRA ? x + bias : x);
           top = fmaxf(top, s[h][u][i]);
         }
@@ -448,14 +444,14 @@ __device__ __forceinline__ void attend8(const AttnArgs8& a, const Plan& p, int64
   }
 }
 
-template <int DT_, int DP_, int HT_, bool EXTRA> struct Op8 {
+template <int DT_, int DP_, int HT_, int SCORE> struct Op8 {
   static constexpr int DT = DT_, DP = DP_, HT = HT_;
   using Args = AttnArgs8;
   using S = Shape8<DT, DP>;
   static constexpr int PT = S::pt;
   using Rows = Rows8;
   template <int KIND, class... A> __device__ static __forceinline__ void attend(A&&... args) {
-    attend8<DT, DP, HT, EXTRA, KIND>(args...);
+    attend8<DT, DP, HT, SCORE, KIND>(args...);
   }
 };
 
@@ -477,24 +473,22 @@ hipError_t run_mfma(const AttnArgs8& a, void* ws, hipStream_t s) {
   // Caches that the 256 MB last-level cache may still hold from the step before are read
   // without the mark.
   const double bytes = 2.0 * a.B * c.most * a.cache.heads * DP;
-  const bool full = a.cache.dim == DP, extra = a.softcap > 0.f || a.cache.key_bias;
-  auto kernel = full ? (extra ? attn_mfma_kernel<Op8<DT, DP, HT, true>, kWhole, kWaves>
-                              : attn_mfma_kernel<Op8<DT, DP, HT, false>, kWhole, kWaves>)
-                     : (extra ? attn_mfma_kernel<Op8<DT, DP, HT, true>, kNarrow, kWaves>
-                              : attn_mfma_kernel<Op8<DT, DP, HT, false>, kNarrow, kWaves>);
-  if constexpr (DP % 128 == 0) {
-    if (full && bytes >= (double)(128 << 20) && c.p.tiles == 1 &&
-        aligned((uintptr_t)a.cache.k, a.cache.k_stride) && aligned((uintptr_t)a.cache.v, a.cache.v_stride))
-      kernel = extra ? attn_mfma_kernel<Op8<DT, DP, HT, true>, kStream, kWaves>
-                     : attn_mfma_kernel<Op8<DT, DP, HT, false>, kStream, kWaves>;
-  }
-  if constexpr (DP <= 128) {
-    if (c.eight)
-      kernel = full ? (extra ? attn_mfma_kernel<Op8<DT, DP, HT, true>, kWhole, 8>
-                             : attn_mfma_kernel<Op8<DT, DP, HT, false>, kWhole, 8>)
-                    : (extra ? attn_mfma_kernel<Op8<DT, DP, HT, true>, kNarrow, 8>
-                             : attn_mfma_kernel<Op8<DT, DP, HT, false>, kNarrow, 8>);
-  }
+  const bool full = a.cache.dim == DP;
+  const bool stream = DP % 128 == 0 && full && bytes >= (double)(128 << 20) && c.p.tiles == 1 &&
+                      aligned((uintptr_t)a.cache.k, a.cache.k_stride) && aligned((uintptr_t)a.cache.v, a.cache.v_stride);
+  const auto choose_kernel = [&](auto op) {
+    using Op = decltype(op);
+    auto kernel = full ? attn_mfma_kernel<Op, kWhole, kWaves> : attn_mfma_kernel<Op, kNarrow, kWaves>;
+    if constexpr (DP % 128 == 0)
+      if (stream) kernel = attn_mfma_kernel<Op, kStream, kWaves>;
+    if constexpr (DP <= 128)
+      if (c.eight) kernel = full ? attn_mfma_kernel<Op, kWhole, 8> : attn_mfma_kernel<Op, kNarrow, 8>;
+    return kernel;
+  };
+  auto kernel = a.softcap > 0.f || a.cache.key_bias ? choose_kernel(Op8<DT, DP, HT, kCapScore>())
+                                                    : choose_kernel(Op8<DT, DP, HT, kPlainScore>());
+  if constexpr (DT != FK_F32)
+    if ((a.softcap > 0.f || a.cache.key_bias) && a.softcap <= kNearCap) kernel = choose_kernel(Op8<DT, DP, HT, kNearCapScore>());
   kernel<<<(unsigned)c.blocks, c.W * 64, 0, s>>>(a, c.p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !c.cut) return e;
