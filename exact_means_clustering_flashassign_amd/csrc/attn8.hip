@@ -127,7 +127,7 @@ hipError_t run_any(const AttnArgs8& a, int64_t most, void* ws, hipStream_t s) {
 //     queries are, as the sum of two numbers, or three for fp32. fp32 queries are
 //     the sum of three bf16 numbers (24 bits); products of those with codes are exact.
 // Bound by bytes where requests are long: 2.28 GB of codes and scales (32 requests of up to 65536
-// keys, 8 heads of 128) in 397 us, 5.75 TB/s; the conversions' vector instructions keep it from
+// keys, 8 heads of 128) in 391 us, 5.8 TB/s; the conversions' vector instructions keep it from
 // the 6.6 that rows of 192 and 256 reach. Short requests are bound by the launch and
 // the chain of dependent loads (lengths, table, scales, codes): one of 2048 keys takes 17 us.
 template <int DT, int DP_> struct Shape8 {
