@@ -6,9 +6,9 @@
 namespace fk {
 namespace {
 
-// Rows of any size, stride and alignment: all fp32 ones, 16-bit ones where they are few (few_rows). The rows of a request are laid out as for the
-// matrix-core kernel (row r is head r % G of token r / G); a block takes R of one cache head, a wave every
-// fourth step of 64 keys. For scores a lane has a key: 64 elements of every key go to LDS, an
+// Rows of any size, stride and alignment: all fp32 ones, 16-bit ones where they are few (few_rows). The
+// rows of a request are laid out as for the matrix-core kernel (row r is head r % G of token
+// r / G); a block takes R of one cache head, a wave every fourth step of 64 keys. For scores a lane has a key: 64 elements of every key go to LDS, an
 // element a lane as they lie in memory, and are read back a key a lane, next to the R queries'
 // elements. For sums a lane has every 64th element, and probabilities come back from LDS a key
 // at a time. So a key or value is loaded once for R rows, and nothing is summed over lanes but a

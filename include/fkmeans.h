@@ -433,8 +433,8 @@ typedef struct {
  *   k, v (T,heads,dim) dt in; *_stride: elements between tokens and between heads.
  *   slots (T) int32 in: as in fk_qk_norm_rope (a key_bias, where the cache has
  *             one, becomes 0; slots outside the cache are skipped, the others have to differ).
- * The cache may not overlap an input. The pages name low-bit quantisation of
- * keys and values among the uses of clusters.
+ * The cache may not overlap an input, nor its tensors one another. The pages name
+ * low-bit quantisation of keys and values among the uses of clusters.
  */
 fk_status_t fk_kv_store8(const void* k, const int64_t k_stride[2], const void* v,
                          const int64_t v_stride[2], fk_dtype_t dt, int64_t T,
